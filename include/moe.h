@@ -79,8 +79,15 @@ typedef enum moe_entry {
   MOE_ENTRY_PERMUTE = 0,
   MOE_ENTRY_MLP_FWD = 1,
   MOE_ENTRY_MLP_BWD = 2,
-  MOE_ENTRY_ROUTER_BWD = 3
+  MOE_ENTRY_ROUTER_BWD = 3,
+  MOE_ENTRY_NORM_BWD = 4
 } moe_entry;
+
+/* Row normalization of moe_norm_fwd and moe_norm_bwd. */
+typedef enum moe_norm {
+  MOE_NORM_LAYER = 0,  /* centred, optional beta                         */
+  MOE_NORM_RMS = 1     /* not centred, no beta                           */
+} moe_norm;
 
 /* Short name of a status code (static string). */
 const char* moe_status_str(moe_status s);
@@ -551,8 +558,76 @@ moe_status moe_mxfp4_quantize(const void* src, int32_t src_fmt,
 int64_t moe_mxfp8_padded_rows(int64_t rows, int32_t nseg);
 
 /*
+ * moe_norm_fwd -- the normalization in front of the layer, row by row:
+ *   MOE_NORM_LAYER: mean = sum_i x[t][i] / d,
+ *     rstd = 1 / sqrt(sum_i (x[t][i] - mean)^2 / d + eps),
+ *     y[t][i] = (x[t][i] - mean) * rstd * gamma[i] + beta[i]
+ *   MOE_NORM_RMS: the same with mean = 0 and no beta.
+ *   x [T][d] bf16 (x_fp32 == 0) or fp32; gamma [d] fp32; beta [d] fp32 or
+ *   NULL (NULL for RMS); y [T][d] bf16 out; mean, rstd [T] fp32 out, each
+ *   may be NULL (both are what moe_norm_bwd reads; mean is not written for
+ *   RMS).  Statistics are fp32, the variance is summed from centred values,
+ *   y is rounded once.
+ * d a multiple of 8 and at most 16384 (MOE_ERR_UNSUPPORTED above), T >= 1,
+ * eps >= 0 and finite.  Outputs must overlap neither inputs nor each other.
+ * No workspace.
+ */
+moe_status moe_norm_fwd(moe_norm kind, const void* x, int32_t x_fp32,
+                        const float* gamma, const float* beta, float eps,
+                        int64_t T, int64_t d, void* y, float* mean,
+                        float* rstd, hipStream_t stream);
+
+/*
+ * moe_norm_bwd -- gradient of moe_norm_fwd.  With xh = (x - mean) * rstd and
+ * g = dy * gamma:
+ *   dx = dres + rstd * (g - sum_i g / d - xh * sum_i (g * xh) / d)
+ *     (RMS: without the sum_i g term),
+ *   dgamma[i] = sum_t dy * xh,  dbeta[i] = sum_t dy.
+ *   dy [T][d] bf16; x, dres (NULL: zero) and dx out [T][d] bf16 or fp32,
+ *   all three of one type (x_fp32); mean (NULL for RMS) and rstd [T] from
+ *   the forward; dgamma, dbeta [d] fp32 out, each may be NULL (dbeta must
+ *   be for RMS).  dres is the gradient that passes the block along its
+ *   residual path; dx may be dres itself, otherwise outputs overlap nothing.
+ *   Sums are fp32 in a fixed order; dx is rounded once.  Sizes as
+ *   moe_norm_fwd.  Workspace: MOE_ENTRY_NORM_BWD (none is used, and it may
+ *   be NULL, when dgamma and dbeta are NULL).
+ */
+moe_status moe_norm_bwd(moe_norm kind, const void* dy, const void* x,
+                        int32_t x_fp32, const float* gamma, const float* mean,
+                        const float* rstd, const void* dres, int64_t T,
+                        int64_t d, void* dx, float* dgamma, float* dbeta,
+                        void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/*
+ * moe_dropout -- dropout with an optional residual sum, its mask drawn from
+ * a counter-based generator and never stored:
+ *   out[i] = res[i] + (keep(i) ? x[i] * scale : 0),  0 <= i < n
+ * and, called on the upstream gradient with res NULL and the same p, rng and
+ * delta, its own backward pass.  keep(i): the 16-bit draw of element i is at
+ * least thr = floor(65536 p + 0.5); scale = 65536 / (65536 - thr), so p is
+ * rounded to a multiple of 2^-16 (p below 2^-17 drops nothing) and thr =
+ * 65536 drops every element.  The draw is half i % 2 (low half first) of
+ * word (i % 8) / 2 of Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", SC'11) with key rng[0] (low word first) and
+ * counter (i / 8, rng[1] + delta mod 2^64), each 64 bits, low word first.
+ *   x, res (may be NULL) and out: n values, all bf16 (fp32 == 0) or all
+ *   fp32; rng: 2 uint64 {seed, offset} in DEVICE memory, read when the
+ *   kernel runs, so a captured graph draws a new mask on every replay once
+ *   its caller advances rng[1]; delta tells apart the calls that share rng
+ *   (layers of a step).  Element i's mask depends on i, rng and delta only.
+ * A dropped element adds exactly 0 even where x is infinite or NaN; fp32
+ * arithmetic, one rounding.  out may be x or res itself; it must not
+ * overlap them otherwise, nor rng.  n >= 1, 0 <= p <= 1.  No workspace.
+ */
+moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
+                       int64_t n, double p, const uint64_t* rng,
+                       uint64_t delta, void* out, hipStream_t stream);
+
+/*
  * moe_workspace_bytes -- workspace size an entry point needs for the given
- * problem (0 when none).  Returns 0 for invalid arguments.
+ * problem (0 when none).  Returns 0 for invalid arguments.  The norm's
+ * backward has neither experts nor slots: E = k = 1, and f is ignored.
  */
 size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
                            int32_t E, int32_t k, int64_t d, int64_t f);

@@ -280,6 +280,50 @@ moe_status permute_launch(moe_prec prec, const int32_t* topk_idx,
   return hip_status(e, "moe_permute/scatter");
 }
 
+// A tensor argument as a byte range, for the overlap checks of the entries
+// that say which of their tensors may coincide.
+struct Range {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+
+bool overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p);
+  const uintptr_t pb = reinterpret_cast<uintptr_t>(b.p);
+  return pa < pb + static_cast<uintptr_t>(b.bytes) &&
+         pb < pa + static_cast<uintptr_t>(a.bytes);
+}
+
+// No output may overlap an input or another output.
+template <size_t NO, size_t NI>
+moe_status check_disjoint(const Range (&outs)[NO], const Range (&ins)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < NI; ++j)
+      REQUIRE(!overlap(outs[i], ins[j]), MOE_ERR_INVALID_ARG,
+              "%s overlaps %s", outs[i].name, ins[j].name);
+    for (size_t j = 0; j < i; ++j)
+      REQUIRE(!overlap(outs[i], outs[j]), MOE_ERR_INVALID_ARG,
+              "%s overlaps %s", outs[i].name, outs[j].name);
+  }
+  return MOE_OK;
+}
+
+moe_status check_norm_dims(moe_norm kind, int64_t T, int64_t d) {
+  REQUIRE(kind == MOE_NORM_LAYER || kind == MOE_NORM_RMS,
+          MOE_ERR_INVALID_ARG, "unknown norm %d", static_cast<int>(kind));
+  REQUIRE(T >= 1, MOE_ERR_INVALID_ARG, "T must be >= 1 (got %lld)",
+          static_cast<long long>(T));
+  if (moe_status st = check_feature("d", d, MOE_BF16)) return st;
+  REQUIRE(d <= moe::kMaxNormWidth, MOE_ERR_UNSUPPORTED,
+          "d must be at most %lld (got %lld)",
+          static_cast<long long>(moe::kMaxNormWidth),
+          static_cast<long long>(d));
+  REQUIRE(T <= (int64_t{1} << 40) / d, MOE_ERR_UNSUPPORTED, "T too large");
+  return MOE_OK;
+}
+
 }  // namespace
 
 // ------------------------------------------------------- allocation-free
@@ -350,6 +394,9 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       return mx_fwd_layout(Tk, f).total;
     case MOE_ENTRY_ROUTER_BWD:
       return moe::router_backward_workspace(T, E, d < 1 ? 1 : d);
+    case MOE_ENTRY_NORM_BWD:
+      if (d < 8 || d > moe::kMaxNormWidth) return 0;
+      return moe::norm_bwd_workspace(T, d);
     case MOE_ENTRY_MLP_BWD:
       if (f < 1 || d < 1) return 0;
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
@@ -1123,6 +1170,107 @@ moe_status moe_mxfp4_quantize(const void* src, int32_t src_fmt,
                                    rows, cols, seg_offsets, nseg, codes,
                                    scales, rows_pad, stream),
       "moe_mxfp4_quantize/tokens");
+}
+
+moe_status moe_norm_fwd(moe_norm kind, const void* x, int32_t x_fp32,
+                        const float* gamma, const float* beta, float eps,
+                        int64_t T, int64_t d, void* y, float* mean,
+                        float* rstd, hipStream_t stream) {
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(gamma);
+  REQUIRE_OPT_PTR(beta);
+  REQUIRE_PTR(y);
+  REQUIRE_OPT_PTR(mean);
+  REQUIRE_OPT_PTR(rstd);
+  if (moe_status st = check_norm_dims(kind, T, d)) return st;
+  const bool layer = kind == MOE_NORM_LAYER;
+  REQUIRE(layer || !beta, MOE_ERR_INVALID_ARG, "RMS norm takes no beta");
+  REQUIRE(eps >= 0.0f && eps <= 3.4e38f, MOE_ERR_INVALID_ARG,
+          "eps must be finite and >= 0");
+  if (!layer) mean = nullptr;
+  const int64_t sx = x_fp32 ? 4 : 2;
+  const Range outs[] = {
+      {"y", y, T * d * 2}, {"mean", mean, T * 4}, {"rstd", rstd, T * 4}};
+  const Range ins[] = {
+      {"x", x, T * d * sx}, {"gamma", gamma, d * 4}, {"beta", beta, d * 4}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  return hip_status(
+      moe::launch_norm_fwd(layer, x, x_fp32 != 0, gamma, beta, eps, T, d,
+                           static_cast<bf16_t*>(y), mean, rstd, stream),
+      "moe_norm_fwd");
+}
+
+moe_status moe_norm_bwd(moe_norm kind, const void* dy, const void* x,
+                        int32_t x_fp32, const float* gamma, const float* mean,
+                        const float* rstd, const void* dres, int64_t T,
+                        int64_t d, void* dx, float* dgamma, float* dbeta,
+                        void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(gamma);
+  REQUIRE_OPT_PTR(mean);
+  REQUIRE_PTR(rstd);
+  REQUIRE_OPT_PTR(dres);
+  REQUIRE_PTR(dx);
+  REQUIRE_OPT_PTR(dgamma);
+  REQUIRE_OPT_PTR(dbeta);
+  if (moe_status st = check_norm_dims(kind, T, d)) return st;
+  const bool layer = kind == MOE_NORM_LAYER;
+  REQUIRE(layer ? mean != nullptr : mean == nullptr, MOE_ERR_INVALID_ARG,
+          "mean is required for layer norm and must be NULL for RMS norm");
+  REQUIRE(layer || !dbeta, MOE_ERR_INVALID_ARG, "RMS norm has no dbeta");
+  const int64_t sx = x_fp32 ? 4 : 2;
+  int64_t need = 0;
+  if (dgamma || dbeta) {
+    need = static_cast<int64_t>(moe::norm_bwd_workspace(T, d));
+    REQUIRE_PTR(workspace);
+    REQUIRE(workspace_bytes >= static_cast<size_t>(need), MOE_ERR_WORKSPACE,
+            "workspace too small: %zu < %lld", workspace_bytes,
+            static_cast<long long>(need));
+  }
+  const Range outs[] = {{"dx", dx, T * d * sx},
+                        {"dgamma", dgamma, d * 4},
+                        {"dbeta", dbeta, d * 4},
+                        {"workspace", need ? workspace : nullptr, need}};
+  const Range ins[] = {
+      {"dy", dy, T * d * 2},   {"x", x, T * d * sx},
+      {"gamma", gamma, d * 4}, {"mean", mean, T * 4},
+      {"rstd", rstd, T * 4},   {"dres", dres == dx ? nullptr : dres,
+                                T * d * sx}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  return hip_status(
+      moe::launch_norm_bwd(layer, static_cast<const bf16_t*>(dy), x,
+                           x_fp32 != 0, gamma, mean, rstd, dres, T, d, dx,
+                           dgamma, dbeta, workspace, stream),
+      "moe_norm_bwd");
+}
+
+moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
+                       int64_t n, double p, const uint64_t* rng,
+                       uint64_t delta, void* out, hipStream_t stream) {
+  REQUIRE_PTR(x);
+  REQUIRE_OPT_PTR(res);
+  REQUIRE_PTR(rng);
+  REQUIRE_PTR(out);
+  REQUIRE(n >= 1, MOE_ERR_INVALID_ARG, "n must be >= 1 (got %lld)",
+          static_cast<long long>(n));
+  REQUIRE(n <= (int64_t{1} << 40), MOE_ERR_UNSUPPORTED, "n too large");
+  REQUIRE(p >= 0.0 && p <= 1.0, MOE_ERR_INVALID_ARG, "p must be in [0, 1]");
+  const int64_t bytes = n * (fp32 ? 4 : 2);
+  const Range outs[] = {{"out", out, bytes}};
+  const Range ins[] = {{"x", x == out ? nullptr : x, bytes},
+                       {"res", res == out ? nullptr : res, bytes},
+                       {"rng", rng, 16}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  const uint32_t thr = static_cast<uint32_t>(p * 65536.0 + 0.5);
+  const float scale =
+      thr < 65536u
+          ? static_cast<float>(65536.0 / static_cast<double>(65536u - thr))
+          : 0.0f;
+  return hip_status(moe::launch_dropout(x, res, fp32 != 0, n, thr, scale, rng,
+                                        delta, out, stream),
+                    "moe_dropout");
 }
 
 }  // extern "C"

@@ -154,4 +154,23 @@ hipError_t gemm_mx_wgrad(const uint8_t* aq, const uint8_t* as,
                          int64_t ldt, const int32_t* offsets, int E,
                          int64_t M, int64_t N, bf16_t* c, hipStream_t st);
 
+// row normalization (norm.hip); d a multiple of 8, at most kMaxNormWidth
+constexpr int64_t kMaxNormWidth = 16384;
+size_t norm_bwd_workspace(int64_t T, int64_t d);
+hipError_t launch_norm_fwd(int layer, const void* x, int x_fp32,
+                           const float* gamma, const float* beta, float eps,
+                           int64_t T, int64_t d, bf16_t* y, float* mean,
+                           float* rstd, hipStream_t s);
+hipError_t launch_norm_bwd(int layer, const bf16_t* dy, const void* x,
+                           int x_fp32, const float* gamma, const float* mean,
+                           const float* rstd, const void* dres, int64_t T,
+                           int64_t d, void* dx, float* dgamma, float* dbeta,
+                           void* ws, hipStream_t s);
+
+// dropout (dropout.hip): thr in [0, 65536], dropped when the draw < thr
+hipError_t launch_dropout(const void* x, const void* res, int fp32,
+                          int64_t n, uint32_t thr, float scale,
+                          const uint64_t* rng, uint64_t delta, void* out,
+                          hipStream_t s);
+
 }  // namespace moe

@@ -22,6 +22,9 @@ MOE_ENTRY_PERMUTE = 0
 MOE_ENTRY_MLP_FWD = 1
 MOE_ENTRY_MLP_BWD = 2
 MOE_ENTRY_ROUTER_BWD = 3
+MOE_ENTRY_NORM_BWD = 4
+MOE_NORM_LAYER = 0
+MOE_NORM_RMS = 1
 
 EXPORTED = [
     "moe_status_str", "moe_last_error", "moe_version", "moe_router_logits",
@@ -34,6 +37,7 @@ EXPORTED = [
     "moe_row_planes", "moe_mx_gate_up_swiglu_fwd", "moe_mx_down_fwd",
     "moe_mx_down_swiglu_bwd", "moe_mx_gate_up_dgrad", "moe_mx_grouped_wgrad",
     "moe_router_backward", "moe_mxfp4_quantize", "moe_permute_noalloc",
+    "moe_norm_fwd", "moe_norm_bwd", "moe_dropout",
 ]
 # fixed per-GPU scratch of moe_permute_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 2 << 20
@@ -102,6 +106,12 @@ def _load():
         "moe_router_backward": (I32, [P, P, P, P, P, ctypes.c_float, I64,
                                       I32, I32, I32, P, P, I64, P, P, P, P,
                                       P, P, P, SZ, P]),
+        "moe_norm_fwd": (I32, [I32, P, I32, P, P, ctypes.c_float, I64, I64,
+                               P, P, P, P]),
+        "moe_norm_bwd": (I32, [I32, P, P, I32, P, P, P, P, I64, I64, P, P, P,
+                               P, SZ, P]),
+        "moe_dropout": (I32, [P, P, I32, I64, ctypes.c_double, P,
+                              ctypes.c_uint64, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -643,3 +653,99 @@ def moe_mx_grouped_wgrad(aq, as_, bq, bs, offsets, Tk, c, stream=None,
     _check("moe_mx_grouped_wgrad", lib.moe_mx_grouped_wgrad(
         _p(aq), _p(as_), _p(bq), _p(bs), int(bool(b_fp4)), ldt,
         _p(offsets), E, Tk, M, N, _p(c), _stream(stream)))
+
+
+# ------------------------------------------------- around the expert layer
+# The entries below take their device from their tensors: all must lie on
+# one GPU, and the call runs on that GPU's current stream (or on `stream`,
+# which must be one of that GPU's) whichever device is current.
+
+def _enqueue(name, stream, tensors, fn, *args):
+    """fn(*args, stream) on the tensors' device; raises MoeError."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a GPU, got {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{name}: tensors on {dev}, stream on "
+                         f"{stream.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(name, fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(name, fn(*args, _stream(stream)))
+
+
+def _act_dtype(t, name):
+    """1 for fp32, 0 for bf16 (the types of the residual stream)."""
+    if t.dtype == torch.float32:
+        return 1
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, "
+                        f"got {t.dtype}")
+    return 0
+
+
+def _want_ws(workspace):
+    """Bytes of a contiguous workspace tensor (0 for None)."""
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def moe_norm_fwd(kind, x, gamma, beta, eps, y, mean=None, rstd=None,
+                 stream=None):
+    """Layer norm or RMS norm of the rows of x (see include/moe.h); mean and
+    rstd are written for moe_norm_bwd where given."""
+    T, d = x.shape
+    x_fp32 = _act_dtype(x, "x")
+    _want(x, "x", x.dtype)
+    _want(gamma, "gamma", torch.float32, (d,))
+    _want(beta, "beta", torch.float32, (d,), allow_none=True)
+    _want(y, "y", torch.bfloat16, (T, d))
+    _want(mean, "mean", torch.float32, (T,), allow_none=True)
+    _want(rstd, "rstd", torch.float32, (T,), allow_none=True)
+    _enqueue("moe_norm_fwd", stream, (x, gamma, beta, y, mean, rstd),
+             lib.moe_norm_fwd, kind, _p(x), x_fp32, _p(gamma), _p(beta),
+             float(eps), T, d, _p(y), _p(mean), _p(rstd))
+
+
+def moe_norm_bwd(kind, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta,
+                 workspace, stream=None):
+    """Gradient of moe_norm_fwd; dx = dres + the norm's (dres may be None,
+    and dx may be dres)."""
+    T, d = x.shape
+    x_fp32 = _act_dtype(x, "x")
+    _want(x, "x", x.dtype)
+    _want(dy, "dy", torch.bfloat16, (T, d))
+    _want(gamma, "gamma", torch.float32, (d,))
+    _want(mean, "mean", torch.float32, (T,), allow_none=True)
+    _want(rstd, "rstd", torch.float32, (T,))
+    _want(dres, "dres", x.dtype, (T, d), allow_none=True)
+    _want(dx, "dx", x.dtype, (T, d))
+    _want(dgamma, "dgamma", torch.float32, (d,), allow_none=True)
+    _want(dbeta, "dbeta", torch.float32, (d,), allow_none=True)
+    nbytes = _want_ws(workspace)
+    _enqueue("moe_norm_bwd", stream,
+             (x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace),
+             lib.moe_norm_bwd, kind, _p(dy), _p(x), x_fp32, _p(gamma),
+             _p(mean), _p(rstd), _p(dres), T, d, _p(dx), _p(dgamma),
+             _p(dbeta), _p(workspace), nbytes)
+
+
+def moe_dropout(x, res, p, rng, delta, out, stream=None):
+    """out = res + dropout(x) (res may be None; out may be x or res).  rng is
+    an int64 tensor {seed, offset} on the device; the call on the upstream
+    gradient with the same p, rng and delta is the backward pass."""
+    fp32 = _act_dtype(x, "x")
+    _want(x, "x", x.dtype)
+    _want(res, "res", x.dtype, x.shape, allow_none=True)
+    _want(rng, "rng", torch.int64, (2,))
+    _want(out, "out", x.dtype, x.shape)
+    _enqueue("moe_dropout", stream, (x, res, rng, out), lib.moe_dropout,
+             _p(x), _p(res), fp32, x.numel(), float(p), _p(rng),
+             int(delta) % (1 << 64), _p(out))
