@@ -80,8 +80,16 @@ typedef enum moe_entry {
   MOE_ENTRY_MLP_FWD = 1,
   MOE_ENTRY_MLP_BWD = 2,
   MOE_ENTRY_ROUTER_BWD = 3,
-  MOE_ENTRY_NORM_BWD = 4
+  MOE_ENTRY_NORM_BWD = 4,
+  MOE_ENTRY_FFN_FWD = 5,
+  MOE_ENTRY_FFN_BWD = 6
 } moe_entry;
+
+/* Gate activation of moe_ffn_fwd and moe_ffn_bwd. */
+typedef enum moe_act {
+  MOE_ACT_SILU = 0,       /* a / (1 + exp(-a))                            */
+  MOE_ACT_GELU_TANH = 1   /* a (1 + tanh(sqrt(2/pi)(a + 0.044715 a^3)))/2 */
+} moe_act;
 
 /* Row normalization of moe_norm_fwd and moe_norm_bwd. */
 typedef enum moe_norm {
@@ -625,9 +633,55 @@ moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
                        uint64_t delta, void* out, hipStream_t stream);
 
 /*
+ * moe_ffn_fwd -- a dense gated feed-forward block over all T rows (the
+ * expert every token uses beside its routed ones, or a dense layer's MLP):
+ *   AB[t] = x[t] . w_gu^T                  (gate: first f columns)
+ *   S[t]  = act(AB[t][:f]) * AB[t][f:]
+ *   y[t]  = y_add[t] + S[t] . w2^T         (y_add NULL: zero)
+ *   x [T][d], w_gu [2f][d], w2 [d][f], y_add [T][d] bf16; ab_saved [T][2f]
+ *   and s_saved [T][f] bf16 out, for the backward (each NULL when it is not
+ *   wanted); y [T][d] bf16 out.  y_add is typically the routed experts'
+ *   output; y may be y_add itself.  Otherwise outputs (and the workspace)
+ *   overlap neither inputs nor each other.
+ * fp32 accumulation; S is computed from the fp32 sums and rounded to bf16
+ * for the second product, y is rounded once.  One to a few tokens stream the
+ * weights once; the bits of a row may differ between calls of different T.
+ * d and f multiples of 8, 1 <= T < 2^30, the w_gu tensor at most
+ * 4 GiB - 256 B (MOE_ERR_UNSUPPORTED above).  Workspace: MOE_ENTRY_FFN_FWD.
+ */
+moe_status moe_ffn_fwd(moe_act act, const void* x, const void* w_gu,
+                       const void* w2, const void* y_add, int64_t T,
+                       int64_t d, int64_t f, void* ab_saved, void* s_saved,
+                       void* y, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * moe_ffn_bwd -- gradient of moe_ffn_fwd.  With A = ab_saved[:, :f],
+ * U = ab_saved[:, f:]:
+ *   dS = dy . w2,  dA = dS * U * act'(A),  dU = dS * act(A),
+ *   dw2 = dy^T . s_saved,  dw_gu = [dA dU]^T . x,
+ *   dx = dx_add + [dA dU] . w_gu          (dx_add NULL: zero)
+ *   dy, x, dx_add, dx out [T][d] bf16; ab_saved, s_saved from the forward;
+ *   dw_gu [2f][d], dw2 [d][f] bf16 out.  dx, dw_gu and dw2 may each be NULL
+ *   (not wanted; s_saved may be NULL without dw2, x without dw_gu).  dx may
+ *   be dx_add itself; otherwise outputs (and the workspace) overlap neither
+ *   inputs nor each other.
+ * fp32 accumulation; [dA dU] is rounded to bf16 for its two products, every
+ * output is rounded once.  All sums run in a fixed order.  Sizes as
+ * moe_ffn_fwd.  Workspace: MOE_ENTRY_FFN_BWD.
+ */
+moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
+                       const void* w_gu, const void* w2,
+                       const void* ab_saved, const void* s_saved,
+                       const void* dx_add, int64_t T, int64_t d, int64_t f,
+                       void* dx, void* dw_gu, void* dw2, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/*
  * moe_workspace_bytes -- workspace size an entry point needs for the given
- * problem (0 when none).  Returns 0 for invalid arguments.  The norm's
- * backward has neither experts nor slots: E = k = 1, and f is ignored.
+ * problem (0 when none).  Returns 0 for invalid arguments.  The norm and
+ * the dense feed-forward block have neither experts nor slots: E = k = 1
+ * and prec MOE_BF16 (the norm ignores f).
  */
 size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
                            int32_t E, int32_t k, int64_t d, int64_t f);

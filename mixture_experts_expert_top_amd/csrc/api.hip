@@ -324,6 +324,25 @@ moe_status check_norm_dims(moe_norm kind, int64_t T, int64_t d) {
   return MOE_OK;
 }
 
+bool ffn_dims_ok(int64_t T, int64_t d, int64_t f) {
+  return T >= 1 && T < (int64_t{1} << 30) && d >= 8 && d % 8 == 0 &&
+         f >= 8 && f % 8 == 0 && f <= (int64_t{1} << 28) &&
+         d <= kMaxRange / (4 * f);
+}
+
+moe_status check_ffn_dims(moe_act act, int64_t T, int64_t d, int64_t f) {
+  REQUIRE(act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH,
+          MOE_ERR_INVALID_ARG, "unknown activation %d",
+          static_cast<int>(act));
+  REQUIRE(T >= 1, MOE_ERR_INVALID_ARG, "T must be >= 1 (got %lld)",
+          static_cast<long long>(T));
+  if (moe_status st = check_feature("d", d, MOE_BF16)) return st;
+  if (moe_status st = check_feature("f", f, MOE_BF16)) return st;
+  REQUIRE(ffn_dims_ok(T, d, f), MOE_ERR_UNSUPPORTED,
+          "T must be below 2^30 and w_gu at most 4 GiB - 256 B");
+  return MOE_OK;
+}
+
 }  // namespace
 
 // ------------------------------------------------------- allocation-free
@@ -397,6 +416,11 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
     case MOE_ENTRY_NORM_BWD:
       if (d < 8 || d > moe::kMaxNormWidth) return 0;
       return moe::norm_bwd_workspace(T, d);
+    case MOE_ENTRY_FFN_FWD:
+    case MOE_ENTRY_FFN_BWD:
+      if (!ffn_dims_ok(T, d, f)) return 0;
+      return entry == MOE_ENTRY_FFN_FWD ? moe::ffn_fwd_workspace(T, d, f)
+                                        : moe::ffn_bwd_workspace(T, d, f);
     case MOE_ENTRY_MLP_BWD:
       if (f < 1 || d < 1) return 0;
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
@@ -1271,6 +1295,97 @@ moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
   return hip_status(moe::launch_dropout(x, res, fp32 != 0, n, thr, scale, rng,
                                         delta, out, stream),
                     "moe_dropout");
+}
+
+moe_status moe_ffn_fwd(moe_act act, const void* x, const void* w_gu,
+                       const void* w2, const void* y_add, int64_t T,
+                       int64_t d, int64_t f, void* ab_saved, void* s_saved,
+                       void* y, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream) {
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w_gu);
+  REQUIRE_PTR(w2);
+  REQUIRE_OPT_PTR(y_add);
+  REQUIRE_OPT_PTR(ab_saved);
+  REQUIRE_OPT_PTR(s_saved);
+  REQUIRE_PTR(y);
+  if (moe_status st = check_ffn_dims(act, T, d, f)) return st;
+  const size_t need = moe::ffn_fwd_workspace(T, d, f);
+  REQUIRE_PTR(workspace);
+  REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE,
+          "workspace too small: %zu < %zu", workspace_bytes, need);
+  const Range outs[] = {{"y", y, T * d * 2},
+                        {"ab_saved", ab_saved, T * f * 4},
+                        {"s_saved", s_saved, T * f * 2},
+                        {"workspace", workspace,
+                         static_cast<int64_t>(need)}};
+  const Range ins[] = {{"x", x, T * d * 2},
+                       {"w_gu", w_gu, f * d * 4},
+                       {"w2", w2, f * d * 2},
+                       {"y_add", y_add == y ? nullptr : y_add, T * d * 2}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  return hip_status(
+      moe::launch_ffn_fwd(
+          act == MOE_ACT_SILU ? moe::kActSilu : moe::kActGeluTanh,
+          static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(w_gu),
+          static_cast<const bf16_t*>(w2), static_cast<const bf16_t*>(y_add),
+          T, d, f, static_cast<bf16_t*>(ab_saved),
+          static_cast<bf16_t*>(s_saved), static_cast<bf16_t*>(y), workspace,
+          stream),
+      "moe_ffn_fwd");
+}
+
+moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
+                       const void* w_gu, const void* w2,
+                       const void* ab_saved, const void* s_saved,
+                       const void* dx_add, int64_t T, int64_t d, int64_t f,
+                       void* dx, void* dw_gu, void* dw2, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  REQUIRE_PTR(dy);
+  REQUIRE_OPT_PTR(x);
+  REQUIRE_PTR(w_gu);
+  REQUIRE_PTR(w2);
+  REQUIRE_PTR(ab_saved);
+  REQUIRE_OPT_PTR(s_saved);
+  REQUIRE_OPT_PTR(dx_add);
+  REQUIRE_OPT_PTR(dx);
+  REQUIRE_OPT_PTR(dw_gu);
+  REQUIRE_OPT_PTR(dw2);
+  REQUIRE(dx || dw_gu || dw2, MOE_ERR_INVALID_ARG,
+          "no output: dx, dw_gu and dw2 are all NULL");
+  REQUIRE(!dw2 || s_saved, MOE_ERR_INVALID_ARG, "dw2 needs s_saved");
+  REQUIRE(!dw_gu || x, MOE_ERR_INVALID_ARG, "dw_gu needs x");
+  REQUIRE(dx || !dx_add, MOE_ERR_INVALID_ARG, "dx_add given without dx");
+  if (moe_status st = check_ffn_dims(act, T, d, f)) return st;
+  const size_t need = moe::ffn_bwd_workspace(T, d, f);
+  REQUIRE_PTR(workspace);
+  REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE,
+          "workspace too small: %zu < %zu", workspace_bytes, need);
+  const Range outs[] = {{"dx", dx, T * d * 2},
+                        {"dw_gu", dw_gu, f * d * 4},
+                        {"dw2", dw2, f * d * 2},
+                        {"workspace", workspace,
+                         static_cast<int64_t>(need)}};
+  const Range ins[] = {{"dy", dy, T * d * 2},
+                       {"x", x, T * d * 2},
+                       {"w_gu", w_gu, f * d * 4},
+                       {"w2", w2, f * d * 2},
+                       {"ab_saved", ab_saved, T * f * 4},
+                       {"s_saved", s_saved, T * f * 2},
+                       {"dx_add", dx_add == dx ? nullptr : dx_add,
+                        T * d * 2}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  return hip_status(
+      moe::launch_ffn_bwd(
+          act == MOE_ACT_SILU ? moe::kActSilu : moe::kActGeluTanh,
+          static_cast<const bf16_t*>(dy), static_cast<const bf16_t*>(x),
+          static_cast<const bf16_t*>(w_gu), static_cast<const bf16_t*>(w2),
+          static_cast<const bf16_t*>(ab_saved),
+          static_cast<const bf16_t*>(s_saved),
+          static_cast<const bf16_t*>(dx_add), T, d, f,
+          static_cast<bf16_t*>(dx), static_cast<bf16_t*>(dw_gu),
+          static_cast<bf16_t*>(dw2), workspace, stream),
+      "moe_ffn_bwd");
 }
 
 }  // extern "C"

@@ -112,6 +112,27 @@ __device__ __forceinline__ float sigmoidf_(float a) {
   return __builtin_amdgcn_rcpf(1.0f + __expf(-a));
 }
 
+// Gated activations act(a) = a s(z(a)), s the logistic function: SiLU has
+// z = a, tanh GELU z = 2 sqrt(2/pi) (a + 0.044715 a^3) (since
+// (1 + tanh(z/2)) / 2 = s(z)).  act' = s + a s (1 - s) z'.
+template <int ACT>
+__device__ __forceinline__ float act_arg(float a) {
+  if constexpr (ACT == kActSilu) return a;
+  constexpr float k = 1.5957691216057308f;        // 2 sqrt(2/pi)
+  return k * a * fmaf(0.044715f * a, a, 1.0f);
+}
+template <int ACT>
+__device__ __forceinline__ void act_both(float a, float* h, float* slope) {
+  const float s = sigmoidf_(act_arg<ACT>(a));
+  *h = a * s;
+  const float t = s * (1.0f - s);
+  float dz = 1.0f;
+  if constexpr (ACT == kActGeluTanh)
+    dz = 1.5957691216057308f * fmaf(3.0f * 0.044715f * a, a, 1.0f);
+  // t is 0 where s has saturated: z' may have overflowed there
+  *slope = t > 0.0f ? fmaf(a * t, dz, s) : s;
+}
+
 // ---------------------------------------------------------------- waves
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 

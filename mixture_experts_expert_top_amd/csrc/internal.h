@@ -167,6 +167,24 @@ hipError_t launch_norm_bwd(int layer, const bf16_t* dy, const void* x,
                            int64_t d, void* dx, float* dgamma, float* dbeta,
                            void* ws, hipStream_t s);
 
+// gated activations (values of moe_act)
+constexpr int kActSilu = 0;
+constexpr int kActGeluTanh = 1;
+
+// dense gated feed-forward block (ffn.hip)
+size_t ffn_fwd_workspace(int64_t T, int64_t d, int64_t f);
+size_t ffn_bwd_workspace(int64_t T, int64_t d, int64_t f);
+hipError_t launch_ffn_fwd(int act, const bf16_t* x, const bf16_t* w_gu,
+                          const bf16_t* w2, const bf16_t* y_add, int64_t T,
+                          int64_t d, int64_t f, bf16_t* ab, bf16_t* s_saved,
+                          bf16_t* y, void* ws, hipStream_t s);
+hipError_t launch_ffn_bwd(int act, const bf16_t* dy, const bf16_t* x,
+                          const bf16_t* w_gu, const bf16_t* w2,
+                          const bf16_t* ab, const bf16_t* s_saved,
+                          const bf16_t* dx_add, int64_t T, int64_t d,
+                          int64_t f, bf16_t* dx, bf16_t* dw_gu, bf16_t* dw2,
+                          void* ws, hipStream_t s);
+
 // dropout (dropout.hip): thr in [0, 65536], dropped when the draw < thr
 hipError_t launch_dropout(const void* x, const void* res, int fp32,
                           int64_t n, uint32_t thr, float scale,

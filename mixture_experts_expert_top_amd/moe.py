@@ -23,8 +23,12 @@ MOE_ENTRY_MLP_FWD = 1
 MOE_ENTRY_MLP_BWD = 2
 MOE_ENTRY_ROUTER_BWD = 3
 MOE_ENTRY_NORM_BWD = 4
+MOE_ENTRY_FFN_FWD = 5
+MOE_ENTRY_FFN_BWD = 6
 MOE_NORM_LAYER = 0
 MOE_NORM_RMS = 1
+MOE_ACT_SILU = 0
+MOE_ACT_GELU_TANH = 1
 
 EXPORTED = [
     "moe_status_str", "moe_last_error", "moe_version", "moe_router_logits",
@@ -37,7 +41,8 @@ EXPORTED = [
     "moe_row_planes", "moe_mx_gate_up_swiglu_fwd", "moe_mx_down_fwd",
     "moe_mx_down_swiglu_bwd", "moe_mx_gate_up_dgrad", "moe_mx_grouped_wgrad",
     "moe_router_backward", "moe_mxfp4_quantize", "moe_permute_noalloc",
-    "moe_norm_fwd", "moe_norm_bwd", "moe_dropout",
+    "moe_norm_fwd", "moe_norm_bwd", "moe_dropout", "moe_ffn_fwd",
+    "moe_ffn_bwd",
 ]
 # fixed per-GPU scratch of moe_permute_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 2 << 20
@@ -112,6 +117,10 @@ def _load():
                                P, SZ, P]),
         "moe_dropout": (I32, [P, P, I32, I64, ctypes.c_double, P,
                               ctypes.c_uint64, P, P]),
+        "moe_ffn_fwd": (I32, [I32, P, P, P, P, I64, I64, I64, P, P, P, P, SZ,
+                              P]),
+        "moe_ffn_bwd": (I32, [I32, P, P, P, P, P, P, P, I64, I64, I64, P, P,
+                              P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -749,3 +758,50 @@ def moe_dropout(x, res, p, rng, delta, out, stream=None):
     _enqueue("moe_dropout", stream, (x, res, rng, out), lib.moe_dropout,
              _p(x), _p(res), fp32, x.numel(), float(p), _p(rng),
              int(delta) % (1 << 64), _p(out))
+
+
+def moe_ffn_fwd(act, x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace,
+                stream=None):
+    """Dense gated feed-forward block, y = y_add + (act(gate) * up) . w2^T
+    (y_add may be None, and y may be y_add); ab_saved and s_saved are written
+    for moe_ffn_bwd where given."""
+    T, d = x.shape
+    f = w2.shape[1]
+    bf = torch.bfloat16
+    _want(x, "x", bf)
+    _want(w_gu, "w_gu", bf, (2 * f, d))
+    _want(w2, "w2", bf, (d, f))
+    _want(y_add, "y_add", bf, (T, d), allow_none=True)
+    _want(ab_saved, "ab_saved", bf, (T, 2 * f), allow_none=True)
+    _want(s_saved, "s_saved", bf, (T, f), allow_none=True)
+    _want(y, "y", bf, (T, d))
+    nbytes = _want_ws(workspace)
+    _enqueue("moe_ffn_fwd", stream,
+             (x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace),
+             lib.moe_ffn_fwd, act, _p(x), _p(w_gu), _p(w2), _p(y_add), T, d,
+             f, _p(ab_saved), _p(s_saved), _p(y), _p(workspace), nbytes)
+
+
+def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
+                dw2, workspace, stream=None):
+    """Gradient of moe_ffn_fwd; dx, dw_gu and dw2 may each be None, dx =
+    dx_add + the block's (dx_add may be None, and dx may be dx_add)."""
+    T, d = dy.shape
+    f = w2.shape[1]
+    bf = torch.bfloat16
+    _want(dy, "dy", bf)
+    _want(x, "x", bf, (T, d), allow_none=True)
+    _want(w_gu, "w_gu", bf, (2 * f, d))
+    _want(w2, "w2", bf, (d, f))
+    _want(ab_saved, "ab_saved", bf, (T, 2 * f))
+    _want(s_saved, "s_saved", bf, (T, f), allow_none=True)
+    _want(dx_add, "dx_add", bf, (T, d), allow_none=True)
+    _want(dx, "dx", bf, (T, d), allow_none=True)
+    _want(dw_gu, "dw_gu", bf, (2 * f, d), allow_none=True)
+    _want(dw2, "dw2", bf, (d, f), allow_none=True)
+    nbytes = _want_ws(workspace)
+    _enqueue("moe_ffn_bwd", stream,
+             (dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu, dw2,
+              workspace), lib.moe_ffn_bwd, act, _p(dy), _p(x), _p(w_gu),
+             _p(w2), _p(ab_saved), _p(s_saved), _p(dx_add), T, d, f, _p(dx),
+             _p(dw_gu), _p(dw2), _p(workspace), nbytes)
