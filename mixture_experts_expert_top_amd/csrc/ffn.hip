@@ -52,6 +52,9 @@ struct TileParams {
 };
 
 constexpr int kBK = 64;
+// tiles in flight from global memory, 128- and 64-wide
+constexpr int kDepthWide = 2;
+constexpr int kDepthNarrow = 4;
 
 __device__ __forceinline__ int swz8(int r) { return (r >> 1) & 7; }
 
@@ -207,18 +210,25 @@ __device__ __forceinline__ void lds8(const float* p, float* v) {
   }
 }
 
-// 256 threads, 2 x 2 waves, each (W / 2) x (W / 2) of a W x W tile.
-template <int W, bool AKC, bool BKC, int EPI, int ACT>
-__global__ __launch_bounds__(256, 2) void ffn_tile_kernel(TileParams P) {
+// NG groups of 256 threads; a group is 2 x 2 waves, each (W / 2) x (W / 2)
+// of a W x W tile.  With two groups each runs half of the reduction out of
+// its own LDS stages and the second group's sums are added to the first's:
+// what a CU with a single tile needs to keep its matrix cores busy.
+template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
+__global__ __launch_bounds__(256 * NG, NG == 1 ? 2 : 1) void ffn_tile_kernel(
+    TileParams P) {
   constexpr int BI = W / 64;                      // 32-blocks a wave and side
   constexpr int kTile = W * kBK * 2;              // bytes of one operand tile
   constexpr int kLd = W + 4;                      // fp32 stage stride
   constexpr int kSmem =
-      4 * kTile > W * kLd * 4 ? 4 * kTile : W * kLd * 4;
+      NG * 4 * kTile > W * kLd * 4 ? NG * 4 * kTile : W * kLd * 4;
   constexpr bool kDual = EPI == kAct;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kSmem];
+  __shared__ __attribute__((aligned(16))) uint8_t smem_all[kSmem];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int grp = NG == 1 ? 0
+                          : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
+  uint8_t* const smem = smem_all + grp * 4 * kTile;
   const int wm = wave >> 1, wn = wave & 1;
   // tiles an XCD gets are consecutive; blocks of 8 m-tiles, m fastest, so
   // that they share B columns and A rows in its L2
@@ -230,9 +240,13 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(TileParams P) {
   const int mt = mb * 8 + rem % mh, nt = rem / mh;
   const int m0 = mt * W;
   const int n0 = nt * (kDual ? W / 2 : W);
-  const int kbeg = blockIdx.y * P.kchunk;
-  const int kend = min(P.K, kbeg + P.kchunk);
-  const int nk = (kend - kbeg + kBK - 1) / kBK;
+  // the workgroup's range of the reduction, then the group's; groups take
+  // equally many steps (barriers are shared), empty past the range's end
+  const int kb0 = blockIdx.y * P.kchunk;
+  const int kend0 = min(P.K, kb0 + P.kchunk);
+  const int nk = ((kend0 - kb0 + kBK - 1) / kBK + NG - 1) / NG;
+  const int kbeg = kb0 + grp * nk * kBK;
+  const int kend = min(kend0, kbeg + nk * kBK);
 
   TileMover<W, AKC> ma;
   TileMover<W, BKC> mb_;
@@ -248,67 +262,135 @@ __global__ __launch_bounds__(256, 2) void ffn_tile_kernel(TileParams P) {
   for (int i = 0; i < BI; ++i)
 #pragma unroll
     for (int j = 0; j < BI; ++j) acc[i][j] = f32x16{};
-  i32x4 va[TileMover<W, AKC>::NP], vb[TileMover<W, BKC>::NP];
 
-  // LDS: [A 0][A 1][B 0][B 1].  Iteration kt computes on stage kt & 1; the
-  // registers hold tile kt + 1, which goes to the other stage (last read
-  // before the previous barrier) half way through, and are refilled with
-  // tile kt + 2.
-  ma.load(va, kbeg, kend);
-  mb_.load(vb, kbeg, kend);
-  ma.store(va, smem);
-  mb_.store(vb, smem + 2 * kTile);
-  ma.load(va, kbeg + kBK, kend);
-  mb_.load(vb, kbeg + kBK, kend);
+  // LDS: [A 0][A 1][B 0][B 1], tile kt in stage kt & 1.  The registers hold
+  // the next kDepth tiles from global memory and two sets of fragments:
+  // while the products of one group of kG k-slices run from one set, the
+  // next group is read into the other.  Step kt sends tile kt + 1 to its
+  // stage (whose fragments every wave held before the previous barrier),
+  // refills the freed registers with tile kt + 1 + kDepth, and before its
+  // last group's products passes the barrier that completes tile kt + 1 and
+  // reads the first group of it.
+  constexpr int kDepth = W == 128 ? kDepthWide : kDepthNarrow;
+  static_assert(kDepth % 2 == 0, "the LDS stage is a compile-time constant");
+  i32x4 va[kDepth][TileMover<W, AKC>::NP], vb[kDepth][TileMover<W, BKC>::NP];
+  {
+    i32x4 fa0[TileMover<W, AKC>::NP], fb0[TileMover<W, BKC>::NP];
+    ma.load(fa0, kbeg, kend);
+    mb_.load(fb0, kbeg, kend);
+#pragma unroll
+    for (int q = 0; q < kDepth; ++q) {
+      // in order, so that the loop's waits need not assume the worst
+      __builtin_amdgcn_sched_barrier(0);
+      ma.load(va[q], kbeg + (q + 1) * kBK, kend);
+      mb_.load(vb[q], kbeg + (q + 1) * kBK, kend);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    ma.store(fa0, smem);
+    mb_.store(fb0, smem + 2 * kTile);
+  }
   __syncthreads();
-  for (int kt = 0; kt < nk; ++kt) {
-    const int cs = kt & 1, ns = cs ^ 1;
-    const uint8_t* ta = smem + cs * kTile;
-    const uint8_t* tb = smem + 2 * kTile + cs * kTile;
+  constexpr int kG = W == 128 ? 2 : 4;           // k-slices a group
+  constexpr int kGroups = 4 / kG;
+  bf16x8_v fra[2][kG][BI], frb[2][kG][BI];
+  auto read_group = [&](int set, int stage, int group) {
+    const uint8_t* ta = smem + stage * kTile;
+    const uint8_t* tb = smem + 2 * kTile + stage * kTile;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      bf16x8_v a[BI], b[BI];
+    for (int k = 0; k < kG; ++k) {
 #pragma unroll
-      for (int i = 0; i < BI; ++i) a[i] = fa.read(ta, wm * BI + i, kk);
+      for (int i = 0; i < BI; ++i)
+        fra[set][k][i] = fa.read(ta, wm * BI + i, group * kG + k);
 #pragma unroll
-      for (int j = 0; j < BI; ++j) b[j] = fb.read(tb, wn * BI + j, kk);
+      for (int j = 0; j < BI; ++j)
+        frb[set][k][j] = fb.read(tb, wn * BI + j, group * kG + k);
+    }
+  };
+  auto products = [&](int set, int k0, int k1) {
+#pragma unroll
+    for (int k = k0; k < k1; ++k)
 #pragma unroll
       for (int i = 0; i < BI; ++i)
 #pragma unroll
         for (int j = 0; j < BI; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              a[i], b[j], acc[i][j], 0, 0, 0);
-      if (kk == 1) {
-        ma.store(va, smem + ns * kTile);
-        mb_.store(vb, smem + 2 * kTile + ns * kTile);
-        const int k2 = kbeg + (kt + 2) * kBK;
-        ma.load(va, k2, kend);
-        mb_.load(vb, k2, kend);
-      }
+              fra[set][k][i], frb[set][k][j], acc[i][j], 0, 0, 0);
+  };
+  // Instruction order: a group's fragment reads right after its first
+  // product, so that they land while the others run from registers; LDS
+  // stores and global loads one after each product.
+  constexpr int kRd = kG * BI * ((AKC ? 1 : 2) + (BKC ? 1 : 2));
+  constexpr int kMv = TileMover<W, AKC>::NP + TileMover<W, BKC>::NP;
+  constexpr int kMf = 2 * BI * BI;               // products a section
+  constexpr int kSgMfma = 0x008, kSgVmem = 0x020, kSgRead = 0x100,
+                kSgWrite = 0x200;
+  constexpr int kPer = (kMv + kMf - 1) / kMf;    // moves a product
+  read_group(0, 0, 0);
+  // step kt with kt % kDepth == q, a compile-time constant
+  auto step = [&](int q, int kt) {
+    const int cs = q & 1, ns = cs ^ 1;
+    const int s1 = kGroups == 1 ? cs : 0;      // set before the barrier
+    const int s2 = kGroups == 1 ? cs : 1;      // and after it
+    __builtin_amdgcn_sched_barrier(0);
+    if (kGroups > 1) read_group(1, cs, 1);
+    ma.store(va[q], smem + ns * kTile);
+    mb_.store(vb[q], smem + 2 * kTile + ns * kTile);
+    const int k2 = kbeg + (kt + 1 + kDepth) * kBK;
+    ma.load(va[q], k2, kend);
+    mb_.load(vb[q], k2, kend);
+    products(s1, 0, 2);
+#pragma unroll
+    for (int i = 0; i < kMf; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+      if (kGroups > 1 && i == 0)
+        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd, 0);
+      __builtin_amdgcn_sched_group_barrier(kSgWrite, kPer, 0);
+      __builtin_amdgcn_sched_group_barrier(kSgVmem, kPer, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    read_group(s2 ^ 1, ns, 0);
+    products(s2, kGroups == 1 ? 2 : 0, kGroups == 1 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < kMf; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
+      if (i == 0) __builtin_amdgcn_sched_group_barrier(kSgRead, kRd, 0);
+    }
+  };
+  int kt0 = 0;
+  for (; kt0 + kDepth <= nk; kt0 += kDepth)
+#pragma unroll
+    for (int q = 0; q < kDepth; ++q) step(q, kt0 + q);
+#pragma unroll
+  for (int q = 0; q < kDepth - 1; ++q)
+    if (kt0 + q < nk) step(q, kt0 + q);
+
+  // The whole tile goes through LDS as fp32 (after the K-loop's last barrier
+  // only fragments that no product uses are read there), then each thread takes 8 columns of a row at a time.
+  float* st = reinterpret_cast<float*>(smem_all);
+#pragma unroll
+  for (int h = NG - 1; h >= 0; --h) {
+    if (grp == h)
+#pragma unroll
+      for (int i = 0; i < BI; ++i)
+#pragma unroll
+        for (int j = 0; j < BI; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int r = (wm * BI + i) * 32 + (v >> 2) * 8 +
+                          (lane >> 5) * 4 + (v & 3);
+            float* p = st + r * kLd + (wn * BI + j) * 32 + (lane & 31);
+            *p = h == NG - 1 ? acc[i][j][v] : acc[i][j][v] + *p;
+          }
     __syncthreads();
   }
-
-  // The whole tile goes through LDS as fp32 (the K-loop's last barrier
-  // freed it), then each thread takes 8 columns of a row at a time.
-  float* st = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int i = 0; i < BI; ++i)
-#pragma unroll
-    for (int j = 0; j < BI; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int r = (wm * BI + i) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 +
-                      (v & 3);
-        st[r * kLd + (wn * BI + j) * 32 + (lane & 31)] = acc[i][j][v];
-      }
-  __syncthreads();
   constexpr int kCols = kDual ? W / 2 : W;
   constexpr int kCh = kCols / 8;                  // chunks a row
-  constexpr int kIt = W * kCh / 256;
+  constexpr int kThr = 256 * NG;
 #pragma unroll
-  for (int it = 0; it < kIt; ++it) {
-    const int idx = tid + 256 * it;
+  for (int it = 0; it < (W * kCh + kThr - 1) / kThr; ++it) {
+    const int idx = static_cast<int>(threadIdx.x) + kThr * it;
+    if (W * kCh < kThr && idx >= W * kCh) continue;
     const int r = idx / kCh, c = (idx % kCh) * 8;
     const int row = m0 + r, col = n0 + c;
     if (row >= P.M || col >= P.N) continue;
@@ -540,51 +622,79 @@ hipError_t thin(const ThinParams& P, hipStream_t s) {
 }
 
 // ---------------------------------------------------------- tile launches
-template <int W, bool AKC, bool BKC, int EPI, int ACT>
+template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
 hipError_t tile_w(TileParams P, int splits, hipStream_t s) {
   constexpr int wn = EPI == kAct ? W / 2 : W;
   P.mtn = (P.M + W - 1) / W;
   P.ntn = (P.N + wn - 1) / wn;
-  hipLaunchKernelGGL((ffn_tile_kernel<W, AKC, BKC, EPI, ACT>),
+  hipLaunchKernelGGL((ffn_tile_kernel<W, NG, AKC, BKC, EPI, ACT>),
                      dim3(static_cast<uint32_t>(P.mtn) * P.ntn, splits),
-                     dim3(256), 0, s, P);
+                     dim3(256 * NG), 0, s, P);
   return hipGetLastError();
 }
 
-// 128 x 128 tiles once they give every CU about one; below that 64 x 64
-// ones spread the product over four times as many CUs.
-constexpr int64_t kWideTiles = 192;
-bool wide_tiles(int64_t M, int64_t N, int cols) {
-  return ((M + 127) / 128) * ((N + cols - 1) / cols) >= kWideTiles;
-}
+// The form of one product: output tiles of `width` (64, 128, or 256 for the
+// grouped GEMM's kernel), `groups` of 256 threads a tile, the reduction in
+// `splits` ranges of kchunk.
+struct Plan {
+  int width, groups, splits, kchunk;
+};
 
 template <bool AKC, bool BKC, int EPI, int ACT>
-hipError_t tile(const TileParams& P, int splits, bool wide, hipStream_t s) {
-  return wide ? tile_w<128, AKC, BKC, EPI, ACT>(P, splits, s)
-              : tile_w<64, AKC, BKC, EPI, ACT>(P, splits, s);
+hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
+  P.kchunk = r.kchunk;
+  if (r.width == 64)
+    return r.groups == 1
+               ? tile_w<64, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
+               : tile_w<64, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
+  return r.groups == 1 ? tile_w<128, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
+                       : tile_w<128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
 }
 
-// Splits of a row output's reduction (fc2 and the data gradient), and the
-// tile width: with few tiles the reduction is cut so that about two
-// workgroups a CU run, each with at least 4 k-steps.
-struct RowPlan {
-  bool wide;
-  int splits, kchunk;
-};
-RowPlan row_plan(int64_t T, int64_t N, int64_t K) {
-  RowPlan r;
-  r.wide = wide_tiles(T, N, 128);
-  const int64_t w = r.wide ? 128 : 64;
-  const int64_t tiles = ((T + w - 1) / w) * ((N + w - 1) / w);
+// The form with the least estimated time.  cols: output columns of a
+// width-256 tile (128 where a tile holds gate and up).  split: the reduction
+// may be cut over workgroups (row outputs, through fp32 planes).
+//
+// A CU with n tiles of a width takes a + b n microseconds for a k-step of
+// all of them, measured on MI355X over T = 65..4096, d = 2048 and 4096, f =
+// 1408..14336: (0.15, 0.16) at 64, (0.08, 0.43) at 128, (0, 1.3) at 256 --
+// per output the wide tile costs half of the narrow one, but 88 tiles of
+// 256 leave two thirds of the CUs idle (dS of 2000 x 2816 over 2048: 43,
+// 38 and 49 us).  Two groups act as twice the tiles for half the steps (45
+// to 128-wide tiles: 23.7 -> 20.2 us).  Cutting the reduction adds a pass
+// over the planes at about 4 TB/s and a launch; it pays where few tiles
+// meet a long reduction (128 x 4096 over 14336: 70 -> 47 us) and costs
+// where the tiles fill the CUs (2000 x 2048 over 2816: 27 -> 37 us).
+Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
+          bool allow256 = true) {
   const int64_t steps = (K + kBK - 1) / kBK;
-  int64_t sp = 512 / tiles;
-  if (sp > steps / 4) sp = steps / 4;
-  if (sp > 8) sp = 8;
-  if (sp < 1) sp = 1;
-  const int64_t per = (steps + sp - 1) / sp;
-  r.kchunk = static_cast<int>(per * kBK);
-  r.splits = static_cast<int>((steps + per - 1) / per);
-  return r;
+  constexpr double kA[3] = {0.15, 0.08, 0.0}, kB[3] = {0.16, 0.43, 1.3};
+  Plan best{};
+  double best_us = 1e30;
+  for (int wi = 0; wi < (allow256 ? 3 : 2); ++wi) {
+    const int64_t w = int64_t{64} << wi, c = cols * w / 256;
+    const int64_t tiles = ((M + w - 1) / w) * ((N + c - 1) / c);
+    for (int64_t sp = 1; sp <= (split && wi < 2 ? 8 : 1); sp *= 2) {
+      if (sp > 1 && sp * 4 > steps) break;       // at least 4 steps a split
+      const int64_t per = (steps + sp - 1) / sp;
+      const double n = static_cast<double>((tiles * sp + 255) / 256);
+      for (int g = 1; g <= 2; ++g) {
+        if (g == 2 && (wi == 2 || n > 1)) break;
+        double us = (kA[wi] + kB[wi] * g * n) *
+                        static_cast<double>((per + g - 1) / g) + 3 + g;
+        if (sp > 1)
+          us += 4 + static_cast<double>(sp * M) * static_cast<double>(N) *
+                        8 / 4e6;
+        if (us < best_us) {
+          best_us = us;
+          best = Plan{static_cast<int>(w), g,
+                      static_cast<int>((steps + per - 1) / per),
+                      static_cast<int>(per * kBK)};
+        }
+      }
+    }
+  }
+  return best;
 }
 
 hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
@@ -613,15 +723,15 @@ hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
   P.B = B; P.ldb = ldb; P.b_rows = N;
   P.M = static_cast<int>(T); P.N = static_cast<int>(N);
   P.K = static_cast<int>(K);
-  const RowPlan r = row_plan(T, N, K);
-  P.kchunk = r.kchunk;
+  const Plan r = plan(T, N, K, 256, true);
+  if (r.width == 256)
+    return gemm_dense_rows(A, B, BKC, T, N, K, add, out, s);
   if (r.splits == 1) {
     P.C = out; P.ldc = N; P.AB = add;
-    return tile<true, BKC, kRow, kActSilu>(P, 1, r.wide, s);
+    return tile<true, BKC, kRow, kActSilu>(P, r, s);
   }
   P.Cf = planes;
-  hipError_t e =
-      tile<true, BKC, kPlane, kActSilu>(P, r.splits, r.wide, s);
+  hipError_t e = tile<true, BKC, kPlane, kActSilu>(P, r, s);
   if (e != hipSuccess) return e;
   return finish_rows(planes, r.splits, T * N, add, out, s);
 }
@@ -629,14 +739,18 @@ hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
 // c[M][N] = sum_t a[t][m] b[t][n]
 hipError_t weight_product(const bf16_t* a, const bf16_t* b, int64_t T,
                           int64_t M, int64_t N, bf16_t* c, hipStream_t s) {
+  // the 256-wide kernel addresses an operand's rows with 32 bits
+  const bool fits = T * (M > N ? M : N) * 2 <= kMaxResourceBytes;
+  const Plan r = plan(M, N, T, 256, false, fits);
+  if (r.width == 256)
+    return gemm_dense_wgrad(a, b, T, M, N, c, s);
   TileParams P{};
   P.A = a; P.lda = M;
   P.B = b; P.ldb = N;
   P.M = static_cast<int>(M); P.N = static_cast<int>(N);
   P.K = static_cast<int>(T);
-  P.kchunk = (P.K + kBK - 1) / kBK * kBK;
   P.C = c; P.ldc = N;
-  return tile<false, false, kRow, kActSilu>(P, 1, wide_tiles(M, N, 128), s);
+  return tile<false, false, kRow, kActSilu>(P, r, s);
 }
 
 template <int ACT>
@@ -650,34 +764,38 @@ hipError_t fc1(const bf16_t* x, const bf16_t* w_gu, int64_t T, int64_t d,
     P.C = ab; P.S = s_out;
     return thin<kAct, ACT>(P, s);
   }
+  const Plan r = plan(T, f, d, 128, false);
+  if (r.width == 256)
+    return gemm_dense_fc1_fwd(x, w_gu, T, d, f, ACT, ab, s_out, s);
   TileParams P{};
   P.A = x; P.lda = d;
   P.B = w_gu; P.ldb = d; P.b_rows = 2 * f;
   P.M = static_cast<int>(T); P.N = static_cast<int>(f);
   P.K = static_cast<int>(d);
-  P.kchunk = (P.K + kBK - 1) / kBK * kBK;
   P.C = ab; P.ldc = 2 * f; P.S = s_out;
-  return tile<true, true, kAct, ACT>(P, 1, wide_tiles(T, f, 64), s);
+  return tile<true, true, kAct, ACT>(P, r, s);
 }
 
 template <int ACT>
 hipError_t dact(const bf16_t* dy, const bf16_t* w2, const bf16_t* ab,
                 int64_t T, int64_t d, int64_t f, bf16_t* dab,
                 hipStream_t s) {
+  const Plan r = plan(T, f, d, 256, false);
+  if (r.width == 256)
+    return gemm_dense_fc2_dgrad(dy, w2, T, d, f, ACT, ab, dab, s);
   TileParams P{};
   P.A = dy; P.lda = d;
   P.B = w2; P.ldb = f; P.b_rows = d;
   P.M = static_cast<int>(T); P.N = static_cast<int>(f);
   P.K = static_cast<int>(d);
-  P.kchunk = (P.K + kBK - 1) / kBK * kBK;
   P.C = dab; P.ldc = 2 * f; P.AB = ab;
-  return tile<true, false, kDAct, ACT>(P, 1, wide_tiles(T, f, 128), s);
+  return tile<true, false, kDAct, ACT>(P, r, s);
 }
 
 // Workspaces.  Forward: S (when the caller keeps none), then the fp32
 // planes of y.  Backward: dAB, then the planes of dx.
 int64_t plane_bytes(int64_t T, int64_t N, int64_t K) {
-  const RowPlan r = row_plan(T, N, K);
+  const Plan r = plan(T, N, K, 256, true);
   return r.splits > 1 ? r.splits * T * N * 4 : 0;
 }
 

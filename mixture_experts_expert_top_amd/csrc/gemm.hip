@@ -543,7 +543,12 @@ __device__ __forceinline__ void mx_mfmas(f32x16 (&acc)[BI][BJ],
           static_cast<int>(sa[I0 + i]), OPS, static_cast<int>(sb[j]));
 }
 
-template <class C, int MODE, bool AKC, bool BKC, int EPI, bool MX, int FMT>
+// DENSE: one matrix in place of expert segments (no offsets are read): all
+// P.Tk rows (SegM) or the whole reduction (SegK) belong to it, there are no
+// routing weights, and the gate's activation is kActSilu (DENSE 1) or
+// kActGeluTanh (DENSE 2).  kStore then adds P.AB when it is not null.
+template <class C, int MODE, bool AKC, bool BKC, int EPI, bool MX, int FMT,
+          int DENSE>
 __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
     Params P) {
   // FMT bit 0 / bit 1: A / B holds MXFP4 (E2M1) codes, widened to E4M3 by
@@ -553,10 +558,13 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
   constexpr int NT = C::kThreads;
   constexpr int BI = C::BI, BJ = C::BJ, TM = C::TM, TN = C::TN;
   __shared__ __attribute__((aligned(16))) bf16_t smem[C::kSmemBytes / 2];
-  __shared__ int s_pref[kMaxExperts + 1];
+  constexpr bool kDense = DENSE != 0;
+  constexpr int kAct = DENSE == 2 ? kActGeluTanh : kActSilu;
+  static_assert(!kDense || (!MX && MODE != kSegKT), "dense: bf16 only");
+  __shared__ int s_pref[kDense ? 1 : kMaxExperts + 1];
   // weight gradients: expert sizes and their descending order
-  __shared__ int s_cnt[MODE == kSegM ? 1 : kMaxExperts];
-  __shared__ int s_ord[MODE == kSegM ? 1 : kMaxExperts];
+  __shared__ int s_cnt[MODE == kSegM || kDense ? 1 : kMaxExperts];
+  __shared__ int s_ord[MODE == kSegM || kDense ? 1 : kMaxExperts];
   __shared__ int s_stat[2];
   __shared__ float s_dp[C::WN * BM];
   // kDSwiglu: the routing weights of the tile's rows
@@ -574,7 +582,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
   int e, mt, nt;
   int64_t seg0;      // first permuted row of the expert
   int seg_len;       // rows of the expert
-  if (MODE == kSegM || MODE == kSegKT) {
+  if (!kDense && (MODE == kSegM || MODE == kSegKT)) {
     // SegM: prefix of m-tiles per expert; SegKT: prefix of the experts'
     // padded token ranges (units of two codes)
     for (int i = tid; i <= E; i += NT) {
@@ -624,7 +632,9 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
     // every XCD, and the surplus ids exit at once.  A split reduction runs
     // the first pieces of all the XCD's tiles, then their second pieces,
     // whose length (split_second_steps) lets its CUs end together.
-    const int total = s_pref[E] * P.ntn;
+    const int mt_all = kDense ? static_cast<int>((P.Tk + BM - 1) / BM)
+                              : s_pref[kDense ? 0 : E];
+    const int total = mt_all * P.ntn;
     int bid;
     if (P.ksplit == 1) {
       if (static_cast<int>(blockIdx.x) >= total) return;
@@ -639,11 +649,24 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
       const int nkf = (P.K + BK - 1) / BK;
       ksplit_at = (nkf - split_second_steps(ntx, nkf, P.xcd_cus)) * BK;
     }
-    e = find_segment(s_pref, E, bid / P.ntn);
-    const int mte = s_pref[e + 1] - s_pref[e];
-    tile_order(bid - s_pref[e] * P.ntn, mte, P.ntn, &mt, &nt);
-    seg0 = P.offsets[e];
-    seg_len = P.offsets[e + 1] - P.offsets[e];
+    if constexpr (kDense) {
+      e = 0;
+      tile_order(bid, mt_all, P.ntn, &mt, &nt);
+      seg0 = 0;
+      seg_len = static_cast<int>(P.Tk);
+    } else {
+      e = find_segment(s_pref, E, bid / P.ntn);
+      const int mte = s_pref[e + 1] - s_pref[e];
+      tile_order(bid - s_pref[e] * P.ntn, mte, P.ntn, &mt, &nt);
+      seg0 = P.offsets[e];
+      seg_len = P.offsets[e + 1] - P.offsets[e];
+    }
+  } else if constexpr (kDense) {
+    e = 0;
+    tile_order(xcd_remap(blockIdx.x, gridDim.x), (P.M + BM - 1) / BM, P.ntn,
+               &mt, &nt);
+    seg0 = 0;
+    seg_len = static_cast<int>(P.Tk);
   } else {
     // A weight-gradient tile's depth is its expert's size (rows, or padded
     // token units), so with skewed routing the contiguous per-XCD tile
@@ -1313,7 +1336,9 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
       }
     }
   };
-  if constexpr (EPI == kDSwiglu) {
+  if constexpr (EPI == kDSwiglu && kDense) {
+    load_ab(0);
+  } else if constexpr (EPI == kDSwiglu) {
     load_ab(0);
     for (int lr = tid; lr < BM; lr += NT)
       s_wrow[lr] = (w && m0 + lr < Mvalid) ? w[m0 + lr] : 1.0f;
@@ -1350,8 +1375,13 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
             *reinterpret_cast<f32x4*>(P.Cf + split * P.plane + o) = x;
           } else {
             uint2 u;
-            u.x = pack_bf16x2(x[0], x[1]);
-            u.y = pack_bf16x2(x[2], x[3]);
+            f32x4 z = x;
+            if (kDense && P.AB) {
+              const uint2 a = *reinterpret_cast<const uint2*>(P.AB + o);
+              z += f32x4{bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
+            }
+            u.x = pack_bf16x2(z[0], z[1]);
+            u.y = pack_bf16x2(z[2], z[3]);
             st_epi<MX>(reinterpret_cast<uint2*>(P.C + o), u);
           }
         }
@@ -1388,7 +1418,8 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
         float sv[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          sv[c] = wr * (g[c] * sigmoidf_(g[c]) * u[c]);
+          sv[c] = kDense ? g[c] * sigmoidf_(act_arg<kAct>(g[c])) * u[c]
+                         : wr * (g[c] * sigmoidf_(g[c]) * u[c]);
         if constexpr (MX) {
           // S along f: one 32-column block per 8 lanes of the row
           uint32_t sbyte;
@@ -1407,8 +1438,11 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
           uint2 og, ou;
           og.x = pack_bf16x2(g[0], g[1]); og.y = pack_bf16x2(g[2], g[3]);
           ou.x = pack_bf16x2(u[0], u[1]); ou.y = pack_bf16x2(u[2], u[3]);
-          st_epi<MX>(reinterpret_cast<uint2*>(AB + ro * P.ldc + col), og);
-          st_epi<MX>(reinterpret_cast<uint2*>(AB + ro * P.ldc + f + col), ou);
+          if (!kDense || P.C) {
+            st_epi<MX>(reinterpret_cast<uint2*>(AB + ro * P.ldc + col), og);
+            st_epi<MX>(reinterpret_cast<uint2*>(AB + ro * P.ldc + f + col),
+                       ou);
+          }
           if (P.S) st_epi<MX>(reinterpret_cast<uint2*>(S + ro * f + col), os);
         }
         if constexpr (kTokEpi) {
@@ -1494,6 +1528,13 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
           const float wr = s_wrow[row - m0];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            if constexpr (kDense) {
+              float h, slope;
+              act_both<kAct>(g[c], &h, &slope);
+              dg[c] = ds[c] * u[c] * slope;
+              du[c] = ds[c] * h;
+              continue;
+            }
             const float sg = sigmoidf_(g[c]);
             const float sl = g[c] * sg;
             part += ds[c] * (sl * u[c]);
@@ -1538,6 +1579,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
           }
         }
         // row sum over the lanes of this row, fixed order
+        if constexpr (kDense) return;
         if constexpr (kLanesPerRow <= 16) {
           part = dpp_group_sum<kLanesPerRow>(part);
         } else {
@@ -1660,7 +1702,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void grouped_gemm_kernel(
       }
     }
   }
-  if (EPI == kDSwiglu) {
+  if (EPI == kDSwiglu && !kDense) {
     // the tile's column groups, added in order (wn = 0, 1, ...): the one
     // read of other waves' LDS in the epilogue
     __syncthreads();
@@ -1710,14 +1752,15 @@ int xcd_cus() {
 }
 
 template <class C, int MODE, bool AKC, bool BKC, int EPI, bool MX = false,
-          int FMT = 0>
+          int FMT = 0, int DENSE = 0>
 hipError_t launch(Params P, int grid, hipStream_t s) {
   if (grid <= 0) return hipSuccess;
   if (P.ksplit != 2) P.ksplit = 1;
   // two pieces a tile: every XCD needs twice its share of ids
   if (P.ksplit == 2) grid = 16 * ((grid + 7) / 8);
   P.xcd_cus = xcd_cus();
-  hipLaunchKernelGGL((grouped_gemm_kernel<C, MODE, AKC, BKC, EPI, MX, FMT>),
+  hipLaunchKernelGGL((grouped_gemm_kernel<C, MODE, AKC, BKC, EPI, MX, FMT,
+                                          DENSE>),
                      dim3(grid), dim3(C::kThreads), 0, s, P);
   return hipGetLastError();
 }
@@ -1808,6 +1851,91 @@ hipError_t gemm_wgrad(const bf16_t* a, int64_t lda, const bf16_t* b,
   const int64_t mtiles = (M + BM - 1) / BM;
   const int grid = static_cast<int>(E * mtiles * P.ntn);
   return launch<CfgWgrad, kSegK, false, false, kStore>(P, grid, st);
+}
+
+// ------------------------------------------------------------------ dense
+// The products of a dense gated feed-forward block (ffn.hip): the same
+// kernel with one matrix in place of the experts' segments.
+namespace {
+
+template <int MODE, bool AKC, bool BKC, int EPI>
+hipError_t launch_dense(const Params& P, int act, int grid, hipStream_t st) {
+  if constexpr (EPI == kSwiglu || EPI == kDSwiglu) {
+    if (act == kActGeluTanh)
+      return launch<CfgFwd, MODE, AKC, BKC, EPI, false, 0, 2>(P, grid, st);
+  }
+  return launch<CfgFwd, MODE, AKC, BKC, EPI, false, 0, 1>(P, grid, st);
+}
+
+int dense_grid(int64_t M, int ntn) {
+  return static_cast<int>((M + BM - 1) / BM * ntn);
+}
+
+}  // namespace
+
+hipError_t gemm_dense_fc1_fwd(const bf16_t* x, const bf16_t* w_gu, int64_t T,
+                              int64_t d, int64_t f, int act, bf16_t* ab,
+                              bf16_t* s, hipStream_t st) {
+  Params P{};
+  P.A = x; P.lda = d;
+  P.B = w_gu; P.ldb = d; P.b_rows = static_cast<int>(2 * f);
+  P.C = ab; P.ldc = 2 * f;
+  P.E = 1; P.Tk = T;
+  P.N = static_cast<int>(f); P.K = static_cast<int>(d);
+  P.f = static_cast<int>(f);
+  P.ntn = static_cast<int>((f + BN / 2 - 1) / (BN / 2));
+  P.S = s;
+  return launch_dense<kSegM, true, true, kSwiglu>(P, act,
+                                                  dense_grid(T, P.ntn), st);
+}
+
+// out[T][N] = add + A . B, A [T][K]; B [N][K] (b_kc) or [K][N]
+hipError_t gemm_dense_rows(const bf16_t* a, const bf16_t* b, bool b_kc,
+                           int64_t T, int64_t N, int64_t K, const bf16_t* add,
+                           bf16_t* out, hipStream_t st) {
+  Params P{};
+  P.A = a; P.lda = K;
+  P.B = b; P.ldb = b_kc ? K : N;
+  P.b_rows = static_cast<int>(b_kc ? N : K);
+  P.C = out; P.ldc = N;
+  P.E = 1; P.Tk = T;
+  P.N = static_cast<int>(N); P.K = static_cast<int>(K);
+  P.AB = add;
+  P.ntn = static_cast<int>((N + BN - 1) / BN);
+  const int grid = dense_grid(T, P.ntn);
+  return b_kc ? launch_dense<kSegM, true, true, kStore>(P, 0, grid, st)
+              : launch_dense<kSegM, true, false, kStore>(P, 0, grid, st);
+}
+
+hipError_t gemm_dense_fc2_dgrad(const bf16_t* dy, const bf16_t* w2,
+                                int64_t T, int64_t d, int64_t f, int act,
+                                const bf16_t* ab, bf16_t* dab,
+                                hipStream_t st) {
+  Params P{};
+  P.A = dy; P.lda = d;
+  P.B = w2; P.ldb = f; P.b_rows = static_cast<int>(d);
+  P.C = dab; P.ldc = 2 * f;
+  P.E = 1; P.Tk = T;
+  P.N = static_cast<int>(f); P.K = static_cast<int>(d);
+  P.f = static_cast<int>(f);
+  P.AB = ab;
+  P.ntn = static_cast<int>((f + BN - 1) / BN);
+  return launch_dense<kSegM, true, false, kDSwiglu>(P, act,
+                                                    dense_grid(T, P.ntn), st);
+}
+
+// c[M][N] = sum_t a[t][m] b[t][n]
+hipError_t gemm_dense_wgrad(const bf16_t* a, const bf16_t* b, int64_t T,
+                            int64_t M, int64_t N, bf16_t* c, hipStream_t st) {
+  Params P{};
+  P.A = a; P.lda = M;
+  P.B = b; P.ldb = N;
+  P.C = c; P.ldc = N;
+  P.E = 1; P.Tk = T;
+  P.M = static_cast<int>(M); P.N = static_cast<int>(N);
+  P.ntn = static_cast<int>((N + BN - 1) / BN);
+  return launch_dense<kSegK, false, false, kStore>(P, 0,
+                                                   dense_grid(M, P.ntn), st);
 }
 
 // ------------------------------------------------------------------ MXFP8

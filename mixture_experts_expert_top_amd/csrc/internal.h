@@ -171,6 +171,21 @@ hipError_t launch_norm_bwd(int layer, const bf16_t* dy, const void* x,
 constexpr int kActSilu = 0;
 constexpr int kActGeluTanh = 1;
 
+// its products on the 256-wide tiles of the grouped GEMM (gemm.hip); each
+// operand's rows below 4 GiB
+hipError_t gemm_dense_fc1_fwd(const bf16_t* x, const bf16_t* w_gu, int64_t T,
+                              int64_t d, int64_t f, int act, bf16_t* ab,
+                              bf16_t* s, hipStream_t st);
+hipError_t gemm_dense_rows(const bf16_t* a, const bf16_t* b, bool b_kc,
+                           int64_t T, int64_t N, int64_t K, const bf16_t* add,
+                           bf16_t* out, hipStream_t st);
+hipError_t gemm_dense_fc2_dgrad(const bf16_t* dy, const bf16_t* w2,
+                                int64_t T, int64_t d, int64_t f, int act,
+                                const bf16_t* ab, bf16_t* dab,
+                                hipStream_t st);
+hipError_t gemm_dense_wgrad(const bf16_t* a, const bf16_t* b, int64_t T,
+                            int64_t M, int64_t N, bf16_t* c, hipStream_t st);
+
 // dense gated feed-forward block (ffn.hip)
 size_t ffn_fwd_workspace(int64_t T, int64_t d, int64_t f);
 size_t ffn_bwd_workspace(int64_t T, int64_t d, int64_t f);
