@@ -619,17 +619,18 @@ moe_status moe_norm_bwd(moe_norm kind, const void* dy, const void* x,
  * word (i % 8) / 2 of Philox4x32-10 (Salmon et al., "Parallel random
  * numbers: as easy as 1, 2, 3", SC'11) with key rng[0] (low word first) and
  * counter (i / 8, rng[1] + delta mod 2^64), each 64 bits, low word first.
- *   x, res (may be NULL) and out: n values, all bf16 (fp32 == 0) or all
- *   fp32; rng: 2 uint64 {seed, offset} in DEVICE memory, read when the
+ *   x: n values, bf16 (x_fp32 == 0) or fp32; res (may be NULL) and out: n
+ *   values of one type, bf16 (out_fp32 == 0) or fp32 -- a bf16 branch joins
+ *   an fp32 residual stream, and its gradient leaves it as bf16; rng: 2 uint64 {seed, offset} in DEVICE memory, read when the
  *   kernel runs, so a captured graph draws a new mask on every replay once
  *   its caller advances rng[1]; delta tells apart the calls that share rng
  *   (layers of a step).  Element i's mask depends on i, rng and delta only.
  * A dropped element adds exactly 0 even where x is infinite or NaN; fp32
- * arithmetic, one rounding.  out may be x or res itself; it must not
- * overlap them otherwise, nor rng.  n >= 1, 0 <= p <= 1.  No workspace.
+ * arithmetic, one rounding.  out may be res itself, or x where the types
+ * are equal; it must not overlap them otherwise, nor rng.  n >= 1, 0 <= p <= 1.  No workspace.
  */
-moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
-                       int64_t n, double p, const uint64_t* rng,
+moe_status moe_dropout(const void* x, int32_t x_fp32, const void* res,
+                       int32_t out_fp32, int64_t n, double p, const uint64_t* rng,
                        uint64_t delta, void* out, hipStream_t stream);
 
 /*

@@ -1270,8 +1270,8 @@ moe_status moe_norm_bwd(moe_norm kind, const void* dy, const void* x,
       "moe_norm_bwd");
 }
 
-moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
-                       int64_t n, double p, const uint64_t* rng,
+moe_status moe_dropout(const void* x, int32_t x_fp32, const void* res,
+                       int32_t out_fp32, int64_t n, double p, const uint64_t* rng,
                        uint64_t delta, void* out, hipStream_t stream) {
   REQUIRE_PTR(x);
   REQUIRE_OPT_PTR(res);
@@ -1281,10 +1281,10 @@ moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
           static_cast<long long>(n));
   REQUIRE(n <= (int64_t{1} << 40), MOE_ERR_UNSUPPORTED, "n too large");
   REQUIRE(p >= 0.0 && p <= 1.0, MOE_ERR_INVALID_ARG, "p must be in [0, 1]");
-  const int64_t bytes = n * (fp32 ? 4 : 2);
-  const Range outs[] = {{"out", out, bytes}};
-  const Range ins[] = {{"x", x == out ? nullptr : x, bytes},
-                       {"res", res == out ? nullptr : res, bytes},
+  const int64_t xb = n * (x_fp32 ? 4 : 2), ob = n * (out_fp32 ? 4 : 2);
+  const Range outs[] = {{"out", out, ob}};
+  const Range ins[] = {{"x", x == out && xb == ob ? nullptr : x, xb},
+                       {"res", res == out ? nullptr : res, ob},
                        {"rng", rng, 16}};
   if (moe_status st = check_disjoint(outs, ins)) return st;
   const uint32_t thr = static_cast<uint32_t>(p * 65536.0 + 0.5);
@@ -1292,8 +1292,8 @@ moe_status moe_dropout(const void* x, const void* res, int32_t fp32,
       thr < 65536u
           ? static_cast<float>(65536.0 / static_cast<double>(65536u - thr))
           : 0.0f;
-  return hip_status(moe::launch_dropout(x, res, fp32 != 0, n, thr, scale, rng,
-                                        delta, out, stream),
+  return hip_status(moe::launch_dropout(x, x_fp32 != 0, res, out_fp32 != 0, n,
+                                        thr, scale, rng, delta, out, stream),
                     "moe_dropout");
 }
 

@@ -89,12 +89,12 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// One chunk of 8 elements a thread and turn.  out may be x or res: a chunk
-// is read before the thread that read it writes it.
-template <typename XT, bool RES>
+// One chunk of 8 elements a thread and turn.  out may be x (of its type) or
+// res: a chunk is read before the thread that read it writes it.
+template <typename XT, typename OT, bool RES>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(
-    const XT* x, const XT* res, int64_t n, uint32_t thr, float scale,
-    const uint64_t* __restrict__ rng, uint64_t delta, XT* out) {
+    const XT* x, const OT* res, int64_t n, uint32_t thr, float scale,
+    const uint64_t* __restrict__ rng, uint64_t delta, OT* out) {
   const uint64_t key = rng[0];
   const uint64_t off = rng[1] + delta;
   const int64_t nfull = n >> 3;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(
   }
 }
 
-template <typename XT>
+template <typename XT, typename OT>
 hipError_t dropout(const void* x, const void* res, int64_t n, uint32_t thr,
                    float scale, const uint64_t* rng, uint64_t delta,
                    void* out, hipStream_t s) {
@@ -137,28 +137,35 @@ hipError_t dropout(const void* x, const void* res, int64_t n, uint32_t thr,
   int64_t nb = (chunks + kDropThreads - 1) / kDropThreads;
   if (nb > 8192) nb = 8192;
   if (res)
-    hipLaunchKernelGGL((dropout_kernel<XT, true>),
+    hipLaunchKernelGGL((dropout_kernel<XT, OT, true>),
                        dim3(static_cast<uint32_t>(nb)), dim3(kDropThreads),
                        0, s, static_cast<const XT*>(x),
-                       static_cast<const XT*>(res), n, thr, scale, rng,
-                       delta, static_cast<XT*>(out));
+                       static_cast<const OT*>(res), n, thr, scale, rng,
+                       delta, static_cast<OT*>(out));
   else
-    hipLaunchKernelGGL((dropout_kernel<XT, false>),
+    hipLaunchKernelGGL((dropout_kernel<XT, OT, false>),
                        dim3(static_cast<uint32_t>(nb)), dim3(kDropThreads),
                        0, s, static_cast<const XT*>(x),
-                       static_cast<const XT*>(nullptr), n, thr, scale, rng,
-                       delta, static_cast<XT*>(out));
+                       static_cast<const OT*>(nullptr), n, thr, scale, rng,
+                       delta, static_cast<OT*>(out));
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_dropout(const void* x, const void* res, int fp32,
-                          int64_t n, uint32_t thr, float scale,
+hipError_t launch_dropout(const void* x, int x_fp32, const void* res,
+                          int out_fp32, int64_t n, uint32_t thr, float scale,
                           const uint64_t* rng, uint64_t delta, void* out,
                           hipStream_t s) {
-  return fp32 ? dropout<float>(x, res, n, thr, scale, rng, delta, out, s)
-              : dropout<bf16_t>(x, res, n, thr, scale, rng, delta, out, s);
+  if (x_fp32)
+    return out_fp32 ? dropout<float, float>(x, res, n, thr, scale, rng,
+                                            delta, out, s)
+                    : dropout<float, bf16_t>(x, res, n, thr, scale, rng,
+                                             delta, out, s);
+  return out_fp32 ? dropout<bf16_t, float>(x, res, n, thr, scale, rng, delta,
+                                           out, s)
+                  : dropout<bf16_t, bf16_t>(x, res, n, thr, scale, rng,
+                                            delta, out, s);
 }
 
 }  // namespace moe

@@ -706,8 +706,18 @@ hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
   return hipGetLastError();
 }
 
-// Tokens up to which the weight-streaming form runs.
-constexpr int64_t kThinRows = 64;
+// Whether the weight-streaming form runs.  Its time grows with the tokens
+// (every workgroup reads all of them), the tiles' hardly does up to 64, but
+// tiles of narrow blocks leave CUs idle.  Forward on MI355X, thin and tiles,
+// us: 16 tokens 11 and 18 (d 2048, f 1408), 18 and 21 (2048, 2816), 28 and
+// 35 (4096, 4096), 84 and 78 (4096, 14336); 24 tokens 13 and 19, 21 and 20,
+// 31 and 33, 101 and 76; 64 tokens 21 and 23, 38 and 23, 48 and 38, 163 and
+// 82.
+bool thin_form(int64_t T, int64_t d, int64_t f) {
+  const int64_t bytes = 6 * d * f;
+  return T <= 16 || (T <= 32 && bytes <= (int64_t{128} << 20)) ||
+         (T <= 64 && bytes <= (int64_t{24} << 20));
+}
 
 size_t up256(int64_t v) {
   return (static_cast<size_t>(v) + 255) & ~static_cast<size_t>(255);
@@ -756,7 +766,7 @@ hipError_t weight_product(const bf16_t* a, const bf16_t* b, int64_t T,
 template <int ACT>
 hipError_t fc1(const bf16_t* x, const bf16_t* w_gu, int64_t T, int64_t d,
                int64_t f, bf16_t* ab, bf16_t* s_out, hipStream_t s) {
-  if (T <= kThinRows) {
+  if (thin_form(T, d, f)) {
     ThinParams P{};
     P.W = w_gu; P.X = x;
     P.T = static_cast<int>(T); P.N = static_cast<int>(f);
@@ -803,7 +813,7 @@ int64_t plane_bytes(int64_t T, int64_t N, int64_t K) {
 
 size_t ffn_fwd_workspace(int64_t T, int64_t d, int64_t f) {
   return up256(T * f * 2) +
-         (T <= kThinRows ? 0 : up256(plane_bytes(T, d, f)));
+         (thin_form(T, d, f) ? 0 : up256(plane_bytes(T, d, f)));
 }
 
 size_t ffn_bwd_workspace(int64_t T, int64_t d, int64_t f) {
@@ -822,7 +832,7 @@ hipError_t launch_ffn_fwd(int act, const bf16_t* x, const bf16_t* w_gu,
           ? fc1<kActSilu>(x, w_gu, T, d, f, ab, sb, s)
           : fc1<kActGeluTanh>(x, w_gu, T, d, f, ab, sb, s);
   if (e != hipSuccess) return e;
-  if (T <= kThinRows) {
+  if (thin_form(T, d, f)) {
     ThinParams P{};
     P.W = w2; P.X = sb;
     P.T = static_cast<int>(T); P.N = static_cast<int>(d);

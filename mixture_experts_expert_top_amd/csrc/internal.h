@@ -201,8 +201,8 @@ hipError_t launch_ffn_bwd(int act, const bf16_t* dy, const bf16_t* x,
                           void* ws, hipStream_t s);
 
 // dropout (dropout.hip): thr in [0, 65536], dropped when the draw < thr
-hipError_t launch_dropout(const void* x, const void* res, int fp32,
-                          int64_t n, uint32_t thr, float scale,
+hipError_t launch_dropout(const void* x, int x_fp32, const void* res,
+                          int out_fp32, int64_t n, uint32_t thr, float scale,
                           const uint64_t* rng, uint64_t delta, void* out,
                           hipStream_t s);
 

@@ -27,6 +27,10 @@ E4M3 on its way to LDS, and the backward converts that payload to MXFP4
 blocks along each expert's tokens for the dW_gu GEMM (widened the same way)
 instead of re-permuting bf16 x.
 
+``MoEBlock`` is the residual block around either of them: the norm in
+front, optionally a dense gated feed-forward block that every token passes
+beside its routed experts, and the residual sum with dropout behind.
+
 No arithmetic happens here: every step runs in the library's kernels.
 """
 
@@ -35,9 +39,10 @@ import contextlib
 import torch
 
 from . import moe
-from .moe import (MOE_BF16, MOE_ENTRY_MLP_BWD, MOE_ENTRY_MLP_FWD,
-                  MOE_ENTRY_PERMUTE, MOE_ENTRY_ROUTER_BWD, MOE_MXFP4,
-                  MOE_MXFP8)
+from .moe import (MOE_ACT_SILU, MOE_BF16, MOE_ENTRY_FFN_BWD,
+                  MOE_ENTRY_FFN_FWD, MOE_ENTRY_MLP_BWD, MOE_ENTRY_MLP_FWD,
+                  MOE_ENTRY_NORM_BWD, MOE_ENTRY_PERMUTE, MOE_ENTRY_ROUTER_BWD,
+                  MOE_MXFP4, MOE_MXFP8, MOE_NORM_LAYER, MOE_NORM_RMS)
 
 
 class StageTimers:
@@ -431,3 +436,111 @@ class MoEPathMX(MoEPath):
                                          self.dw_gu, b_fp4=self.act_fp4)
         self._finish_dx(timers)
         return self.dx, self.dw_gu, self.dw2, self.dp
+
+
+class MoEBlock:
+    """Pre-norm residual block around an expert layer (a ``MoEPath`` or
+    ``MoEPathMX`` with bf16 output):
+
+      n = norm(x);  z = experts(n) [+ ffn(n)];  y = x + dropout(z)
+
+    f_shared > 0 adds the dense feed-forward block (the "shared expert") of
+    that width.  x, y and their gradients are the residual stream, bf16 or
+    (stream_fp32) fp32.  The buffers belong to the block and the path; y, dx
+    and the gradients are overwritten by the next call.
+
+    forward:  moe_norm_fwd -> the path's calls -> moe_ffn_fwd (into the
+              path's y) -> moe_dropout
+    backward: moe_dropout -> the path's calls -> moe_ffn_bwd (into the
+              path's dx) -> moe_norm_bwd (adding the residual's dy)
+    """
+
+    def __init__(self, path, norm=MOE_NORM_RMS, eps=1e-5, f_shared=0,
+                 act=MOE_ACT_SILU, stream_fp32=False):
+        if path.y.dtype != torch.bfloat16:
+            raise ValueError("MoEBlock needs a path with bf16 output")
+        self.path, self.norm, self.eps = path, norm, eps
+        self.f_shared, self.act = f_shared, act
+        T, d = path.T, path.d
+        dev = path.y.device
+        self.stream_dtype = torch.float32 if stream_fp32 else torch.bfloat16
+        f32, bf = torch.float32, torch.bfloat16
+        z = lambda *s, dt=bf: torch.empty(*s, dtype=dt, device=dev)  # noqa
+        self.n = z(T, d)
+        self.y = z(T, d, dt=self.stream_dtype)
+        self.mean = z(T, dt=f32) if norm == MOE_NORM_LAYER else None
+        self.rstd = z(T, dt=f32)
+        # a generator state for calls without dropout, which draw nothing
+        self._no_rng = torch.zeros(2, dtype=torch.int64, device=dev)
+        if f_shared:
+            self.ab, self.s = z(T, 2 * f_shared), z(T, f_shared)
+            self.ws_ffn = self._ws(MOE_ENTRY_FFN_FWD, f_shared)
+        self._bwd_ready = False
+
+    def _ws(self, entry, f):
+        n = moe.moe_workspace_bytes(entry, MOE_BF16, self.path.T, 1, 1,
+                                    self.path.d, f)
+        return torch.empty(max(n, 16), dtype=torch.uint8,
+                           device=self.path.y.device)
+
+    def _alloc_bwd(self):
+        T, d, f = self.path.T, self.path.d, self.f_shared
+        dev = self.path.y.device
+        f32, bf = torch.float32, torch.bfloat16
+        z = lambda *s, dt=bf: torch.empty(*s, dtype=dt, device=dev)  # noqa
+        self.dz = z(T, d)
+        self.dx = z(T, d, dt=self.stream_dtype)
+        self.dgamma = z(d, dt=f32)
+        self.dbeta = z(d, dt=f32) if self.norm == MOE_NORM_LAYER else None
+        self.ws_norm = self._ws(MOE_ENTRY_NORM_BWD, 0)
+        if f:
+            self.dsw_gu, self.dsw2 = z(2 * f, d), z(d, f)
+            self.ws_ffn_bwd = self._ws(MOE_ENTRY_FFN_BWD, f)
+        self._bwd_ready = True
+
+    def forward(self, x, gamma, w_gu, w2, beta=None, w_g=None, bias=None,
+                logits=None, sw_gu=None, sw2=None, p=0.0, rng=None, delta=0,
+                timers=None):
+        """y = x + dropout(experts(norm(x)) + ffn(norm(x))).  sw_gu, sw2 are
+        the feed-forward block's weights; rng (int64 {seed, offset} on the
+        device) and delta choose the dropout mask, as in moe_dropout, and
+        are needed when p > 0; backward uses the same p, rng and delta, so
+        rng is advanced only between a backward and the next forward."""
+        if p > 0 and rng is None:
+            raise ValueError("dropout (p > 0) needs rng")
+        if self.f_shared and (sw_gu is None or sw2 is None):
+            raise ValueError("f_shared > 0 needs sw_gu and sw2")
+        with _around(timers, "norm_fwd"):
+            moe.moe_norm_fwd(self.norm, x, gamma, beta, self.eps, self.n,
+                             self.mean, self.rstd)
+        z = self.path.forward(self.n, w_gu, w2, w_g=w_g, bias=bias,
+                              logits=logits, timers=timers)
+        if self.f_shared:
+            with _around(timers, "ffn_fwd"):
+                moe.moe_ffn_fwd(self.act, self.n, sw_gu, sw2, z, self.ab,
+                                self.s, z, self.ws_ffn)
+        self._drop = (p, self._no_rng if rng is None else rng, delta)
+        self._x = x
+        with _around(timers, "dropout_fwd"):
+            moe.moe_dropout(z, x, *self._drop, self.y)
+        return self.y
+
+    def backward(self, dy, gamma, w_gu, w2, sw_gu=None, sw2=None,
+                 timers=None):
+        """dx; the weights' gradients are left in dgamma, dbeta, dsw_gu and
+        dsw2, and in the path (dw_gu, dw2, and the router's)."""
+        if not self._bwd_ready:
+            self._alloc_bwd()
+        with _around(timers, "dropout_bwd"):
+            moe.moe_dropout(dy, None, *self._drop, self.dz)
+        dn = self.path.backward(self.dz, w_gu, w2, timers=timers)[0]
+        if self.f_shared:
+            with _around(timers, "ffn_bwd"):
+                moe.moe_ffn_bwd(self.act, self.dz, self.n, sw_gu, sw2,
+                                self.ab, self.s, dn, dn, self.dsw_gu,
+                                self.dsw2, self.ws_ffn_bwd)
+        with _around(timers, "norm_bwd"):
+            moe.moe_norm_bwd(self.norm, dn, self._x, gamma, self.mean,
+                             self.rstd, dy, self.dx, self.dgamma, self.dbeta,
+                             self.ws_norm)
+        return self.dx

@@ -115,7 +115,7 @@ def _load():
                                P, P, P, P]),
         "moe_norm_bwd": (I32, [I32, P, P, I32, P, P, P, P, I64, I64, P, P, P,
                                P, SZ, P]),
-        "moe_dropout": (I32, [P, P, I32, I64, ctypes.c_double, P,
+        "moe_dropout": (I32, [P, I32, P, I32, I64, ctypes.c_double, P,
                               ctypes.c_uint64, P, P]),
         "moe_ffn_fwd": (I32, [I32, P, P, P, P, I64, I64, I64, P, P, P, P, SZ,
                               P]),
@@ -669,41 +669,63 @@ def moe_mx_grouped_wgrad(aq, as_, bq, bs, offsets, Tk, c, stream=None,
 # one GPU, and the call runs on that GPU's current stream (or on `stream`,
 # which must be one of that GPU's) whichever device is current.
 
-def _enqueue(name, stream, tensors, fn, *args):
-    """fn(*args, stream) on the tensors' device; raises MoeError."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a GPU, got {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{name}: tensors on {dev}, stream on "
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+
+def _checked(name, specs):
+    """The device index and the pointers of the tensors of `specs`, a list of
+    (name, tensor or None, dtype, shape or None); one pass over them, since
+    the smallest calls cost little more than this."""
+    dev = None
+    mixed = False
+    ptrs = []
+    for tname, t, dtype, shape in specs:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype is not dtype or not t.is_contiguous() or (
+                shape is not None and t.shape != shape):
+            _want(t, f"{name}: {tname}", dtype, shape)
+        i = t.get_device()
+        if dev is None:
+            dev = i
+        elif i != dev:
+            mixed = True
+        ptrs.append(t.data_ptr())
+    if mixed:
+        raise ValueError(f"{name}: tensors on different devices: " + ", ".join(
+            f"{n} {t.device}" for n, t, _, _ in specs if t is not None))
+    if dev is None or dev < 0:
+        raise ValueError(f"{name}: tensors must be on a GPU")
+    return dev, ptrs
+
+
+def _enqueue(name, stream, dev, fn, *args):
+    """fn(*args, stream) on device `dev`; raises MoeError."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{name}: tensors on cuda:{dev}, stream on "
                          f"{stream.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(name, fn(*args, _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(name, fn(*args, _stream(stream)))
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream.cuda_stream)
+    if status:
+        _check(name, status)
 
 
-def _act_dtype(t, name):
-    """1 for fp32, 0 for bf16 (the types of the residual stream)."""
-    if t.dtype == torch.float32:
-        return 1
-    if t.dtype != torch.bfloat16:
+def _stream_dtype(t, name):
+    """The dtype of a residual-stream tensor: bf16 or fp32."""
+    if t.dtype is not _BF16 and t.dtype is not _F32:
         raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, "
                         f"got {t.dtype}")
-    return 0
+    return t.dtype
 
 
-def _want_ws(workspace):
-    """Bytes of a contiguous workspace tensor (0 for None)."""
-    if workspace is None:
-        return 0
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def moe_norm_fwd(kind, x, gamma, beta, eps, y, mean=None, rstd=None,
@@ -711,16 +733,13 @@ def moe_norm_fwd(kind, x, gamma, beta, eps, y, mean=None, rstd=None,
     """Layer norm or RMS norm of the rows of x (see include/moe.h); mean and
     rstd are written for moe_norm_bwd where given."""
     T, d = x.shape
-    x_fp32 = _act_dtype(x, "x")
-    _want(x, "x", x.dtype)
-    _want(gamma, "gamma", torch.float32, (d,))
-    _want(beta, "beta", torch.float32, (d,), allow_none=True)
-    _want(y, "y", torch.bfloat16, (T, d))
-    _want(mean, "mean", torch.float32, (T,), allow_none=True)
-    _want(rstd, "rstd", torch.float32, (T,), allow_none=True)
-    _enqueue("moe_norm_fwd", stream, (x, gamma, beta, y, mean, rstd),
-             lib.moe_norm_fwd, kind, _p(x), x_fp32, _p(gamma), _p(beta),
-             float(eps), T, d, _p(y), _p(mean), _p(rstd))
+    xt = _stream_dtype(x, "x")
+    dev, p = _checked("moe_norm_fwd", (
+        ("x", x, xt, None), ("gamma", gamma, _F32, (d,)),
+        ("beta", beta, _F32, (d,)), ("y", y, _BF16, (T, d)),
+        ("mean", mean, _F32, (T,)), ("rstd", rstd, _F32, (T,))))
+    _enqueue("moe_norm_fwd", stream, dev, lib.moe_norm_fwd, kind, p[0],
+             xt is _F32, p[1], p[2], eps, T, d, p[3], p[4], p[5])
 
 
 def moe_norm_bwd(kind, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta,
@@ -728,36 +747,32 @@ def moe_norm_bwd(kind, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta,
     """Gradient of moe_norm_fwd; dx = dres + the norm's (dres may be None,
     and dx may be dres)."""
     T, d = x.shape
-    x_fp32 = _act_dtype(x, "x")
-    _want(x, "x", x.dtype)
-    _want(dy, "dy", torch.bfloat16, (T, d))
-    _want(gamma, "gamma", torch.float32, (d,))
-    _want(mean, "mean", torch.float32, (T,), allow_none=True)
-    _want(rstd, "rstd", torch.float32, (T,))
-    _want(dres, "dres", x.dtype, (T, d), allow_none=True)
-    _want(dx, "dx", x.dtype, (T, d))
-    _want(dgamma, "dgamma", torch.float32, (d,), allow_none=True)
-    _want(dbeta, "dbeta", torch.float32, (d,), allow_none=True)
-    nbytes = _want_ws(workspace)
-    _enqueue("moe_norm_bwd", stream,
-             (x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace),
-             lib.moe_norm_bwd, kind, _p(dy), _p(x), x_fp32, _p(gamma),
-             _p(mean), _p(rstd), _p(dres), T, d, _p(dx), _p(dgamma),
-             _p(dbeta), _p(workspace), nbytes)
+    xt = _stream_dtype(x, "x")
+    dev, p = _checked("moe_norm_bwd", (
+        ("dy", dy, _BF16, (T, d)), ("x", x, xt, None),
+        ("gamma", gamma, _F32, (d,)), ("mean", mean, _F32, (T,)),
+        ("rstd", rstd, _F32, (T,)), ("dres", dres, xt, (T, d)),
+        ("dx", dx, xt, (T, d)), ("dgamma", dgamma, _F32, (d,)),
+        ("dbeta", dbeta, _F32, (d,)),
+        ("workspace", workspace, workspace.dtype if workspace is not None
+         else None, None)))
+    _enqueue("moe_norm_bwd", stream, dev, lib.moe_norm_bwd, kind, p[0], p[1],
+             xt is _F32, p[2], p[3], p[4], p[5], T, d, p[6], p[7], p[8],
+             p[9], _nbytes(workspace))
 
 
 def moe_dropout(x, res, p, rng, delta, out, stream=None):
-    """out = res + dropout(x) (res may be None; out may be x or res).  rng is
-    an int64 tensor {seed, offset} on the device; the call on the upstream
+    """out = res + dropout(x) (res may be None; out may be res, or x of its
+    dtype; x and out may differ in dtype, res has out's).  rng is an int64
+    tensor {seed, offset} on the device; the call on the upstream
     gradient with the same p, rng and delta is the backward pass."""
-    fp32 = _act_dtype(x, "x")
-    _want(x, "x", x.dtype)
-    _want(res, "res", x.dtype, x.shape, allow_none=True)
-    _want(rng, "rng", torch.int64, (2,))
-    _want(out, "out", x.dtype, x.shape)
-    _enqueue("moe_dropout", stream, (x, res, rng, out), lib.moe_dropout,
-             _p(x), _p(res), fp32, x.numel(), float(p), _p(rng),
-             int(delta) % (1 << 64), _p(out))
+    xt, ot = _stream_dtype(x, "x"), _stream_dtype(out, "out")
+    shape = x.shape
+    dev, q = _checked("moe_dropout", (
+        ("x", x, xt, None), ("res", res, ot, shape),
+        ("rng", rng, torch.int64, (2,)), ("out", out, ot, shape)))
+    _enqueue("moe_dropout", stream, dev, lib.moe_dropout, q[0], xt is _F32,
+             q[1], ot is _F32, x.numel(), p, q[2], delta % (1 << 64), q[3])
 
 
 def moe_ffn_fwd(act, x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace,
@@ -767,19 +782,14 @@ def moe_ffn_fwd(act, x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace,
     for moe_ffn_bwd where given."""
     T, d = x.shape
     f = w2.shape[1]
-    bf = torch.bfloat16
-    _want(x, "x", bf)
-    _want(w_gu, "w_gu", bf, (2 * f, d))
-    _want(w2, "w2", bf, (d, f))
-    _want(y_add, "y_add", bf, (T, d), allow_none=True)
-    _want(ab_saved, "ab_saved", bf, (T, 2 * f), allow_none=True)
-    _want(s_saved, "s_saved", bf, (T, f), allow_none=True)
-    _want(y, "y", bf, (T, d))
-    nbytes = _want_ws(workspace)
-    _enqueue("moe_ffn_fwd", stream,
-             (x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace),
-             lib.moe_ffn_fwd, act, _p(x), _p(w_gu), _p(w2), _p(y_add), T, d,
-             f, _p(ab_saved), _p(s_saved), _p(y), _p(workspace), nbytes)
+    dev, p = _checked("moe_ffn_fwd", (
+        ("x", x, _BF16, None), ("w_gu", w_gu, _BF16, (2 * f, d)),
+        ("w2", w2, _BF16, (d, f)), ("y_add", y_add, _BF16, (T, d)),
+        ("ab_saved", ab_saved, _BF16, (T, 2 * f)),
+        ("s_saved", s_saved, _BF16, (T, f)), ("y", y, _BF16, (T, d)),
+        ("workspace", workspace, workspace.dtype, None)))
+    _enqueue("moe_ffn_fwd", stream, dev, lib.moe_ffn_fwd, act, p[0], p[1],
+             p[2], p[3], T, d, f, p[4], p[5], p[6], p[7], _nbytes(workspace))
 
 
 def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
@@ -788,20 +798,14 @@ def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
     dx_add + the block's (dx_add may be None, and dx may be dx_add)."""
     T, d = dy.shape
     f = w2.shape[1]
-    bf = torch.bfloat16
-    _want(dy, "dy", bf)
-    _want(x, "x", bf, (T, d), allow_none=True)
-    _want(w_gu, "w_gu", bf, (2 * f, d))
-    _want(w2, "w2", bf, (d, f))
-    _want(ab_saved, "ab_saved", bf, (T, 2 * f))
-    _want(s_saved, "s_saved", bf, (T, f), allow_none=True)
-    _want(dx_add, "dx_add", bf, (T, d), allow_none=True)
-    _want(dx, "dx", bf, (T, d), allow_none=True)
-    _want(dw_gu, "dw_gu", bf, (2 * f, d), allow_none=True)
-    _want(dw2, "dw2", bf, (d, f), allow_none=True)
-    nbytes = _want_ws(workspace)
-    _enqueue("moe_ffn_bwd", stream,
-             (dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu, dw2,
-              workspace), lib.moe_ffn_bwd, act, _p(dy), _p(x), _p(w_gu),
-             _p(w2), _p(ab_saved), _p(s_saved), _p(dx_add), T, d, f, _p(dx),
-             _p(dw_gu), _p(dw2), _p(workspace), nbytes)
+    dev, p = _checked("moe_ffn_bwd", (
+        ("dy", dy, _BF16, None), ("x", x, _BF16, (T, d)),
+        ("w_gu", w_gu, _BF16, (2 * f, d)), ("w2", w2, _BF16, (d, f)),
+        ("ab_saved", ab_saved, _BF16, (T, 2 * f)),
+        ("s_saved", s_saved, _BF16, (T, f)),
+        ("dx_add", dx_add, _BF16, (T, d)), ("dx", dx, _BF16, (T, d)),
+        ("dw_gu", dw_gu, _BF16, (2 * f, d)), ("dw2", dw2, _BF16, (d, f)),
+        ("workspace", workspace, workspace.dtype, None)))
+    _enqueue("moe_ffn_bwd", stream, dev, lib.moe_ffn_bwd, act, p[0], p[1],
+             p[2], p[3], p[4], p[5], p[6], T, d, f, p[7], p[8],
+             p[9], p[10], _nbytes(workspace))

@@ -74,9 +74,9 @@ def test_norm_workspace_sizes():
     assert ws(1 << 20, 4096) == ws(1 << 30, 4096)
 
 
-def _drop(x=at(0), res=at(1), fp32=0, n=64, p=0.1, rng=at(2), delta=0,
+def _drop(x=at(0), xf=0, res=at(1), of=0, n=64, p=0.1, rng=at(2), delta=0,
           out=at(3)):
-    return L.moe_dropout(x, res, fp32, n, p, rng, delta, out, None)
+    return L.moe_dropout(x, xf, res, of, n, p, rng, delta, out, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -85,7 +85,8 @@ def _drop(x=at(0), res=at(1), fp32=0, n=64, p=0.1, rng=at(2), delta=0,
     (dict(x=None), INVALID), (dict(rng=None), INVALID),
     (dict(out=None), INVALID), (dict(x=at(0) + 2), INVALID),
     (dict(out=at(0) + 16), INVALID), (dict(out=at(1) - 16), INVALID),
-    (dict(rng=at(3) + 112), INVALID), (dict(out=at(2)), INVALID)])
+    (dict(rng=at(3) + 112), INVALID),
+    (dict(out=at(0), of=1), INVALID), (dict(out=at(0), xf=1), INVALID), (dict(out=at(2)), INVALID)])
 def test_dropout_refusals(kw, want):
     assert _drop(**kw) == want
     assert L.moe_last_error()

@@ -70,6 +70,32 @@ def test_dropout_parity(n, p, seed, off, delta, xt):
 
 
 @gpu
+@pytest.mark.parametrize("xt,ot", [(BF, F32), (F32, BF)],
+                         ids=["bf16_to_fp32", "fp32_to_bf16"])
+@pytest.mark.parametrize("n", [5, 4104, 100003])
+def test_dropout_between_types(n, xt, ot):
+    """A bf16 branch into an fp32 residual stream, and its gradient back."""
+    dev = torch.device("cuda:0")
+    x = I.make_tensor((n,), seed=n, dtype=xt, device=dev)
+    res = I.make_tensor((n,), seed=n + 1, dtype=ot, device=dev)
+    rng = _rng(21, 22)
+    for r in (res, None):
+        out = torch.empty(n, dtype=ot, device=dev)
+        moe.moe_dropout(x, r, 0.3, rng, 5, out)
+        ref, keep = B.dropout(h64(x), None if r is None else h64(r), 0.3, 21,
+                              27)
+        k = torch.from_numpy(keep).to(dev)
+        assert (out[~k] == (0 if r is None else r[~k])).all()
+        lin = 2 * U * np.abs(h64(x)) / 0.7
+        assert (np.abs(h64(out) - ref) <=
+                lin + HALF[ot] * (np.abs(ref) + lin)).all()
+    alias = res.clone()
+    moe.moe_dropout(x, alias, 0.3, rng, 5, alias)
+    moe.moe_dropout(x, res, 0.3, rng, 5, out)
+    assert torch.equal(alias, out)
+
+
+@gpu
 def test_dropped_nonfinite_values_vanish():
     dev = torch.device("cuda:0")
     n = 4096

@@ -150,7 +150,7 @@ def _check_bwd(act, N, add, ab, s, dx, dwg, dw2, T, d, f):
     _check("dw2", dw2, rd2, b + H * (np.abs(rd2) + b))
 
 
-# the weight-streaming form (T <= 64: one, two and four token blocks, each
+# the weight-streaming form (T <= 64, small weights: one, two and four token blocks, each
 # with its last block full and not), tiles of either width, split and whole
 # reductions, widths inside and across tiles and k-steps
 SIZES = [(1, 8, 8), (1, 2048, 1408), (2, 16, 24), (5, 264, 520),
@@ -158,7 +158,7 @@ SIZES = [(1, 8, 8), (1, 2048, 1408), (2, 16, 24), (5, 264, 520),
          (48, 4104, 136), (64, 256, 264), (64, 64, 4096), (65, 8, 8),
          (65, 40, 136), (100, 264, 72), (128, 128, 64), (130, 520, 392),
          (257, 1032, 776), (300, 2048, 1408), (1100, 520, 1416),
-         (1500, 2056, 136)]
+         (1500, 2056, 136), (20, 4096, 5632), (40, 2048, 2816)]
 
 
 @gpu
