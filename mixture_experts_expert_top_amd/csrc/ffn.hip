@@ -214,35 +214,41 @@ __device__ __forceinline__ void lds8(const float* p, float* v) {
 // of a W x W tile.  With two groups each runs half of the reduction out of
 // its own LDS stages and the second group's sums are added to the first's:
 // what a CU with a single tile needs to keep its matrix cores busy.
+//
+// The LDS of a tile: two stages of both operands a group, or the fp32 tile
+// of the epilogue (rows of W + 4).
+template <int W, int NG>
+constexpr int tile_smem() {
+  constexpr int k = NG * 4 * W * kBK * 2, e = W * (W + 4) * 4;
+  return k > e ? k : e;
+}
+
+// tile: index in the product's mtn x ntn tiles, already in XCD order.
 template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
-__global__ __launch_bounds__(256 * NG, NG == 1 ? 2 : 1) void ffn_tile_kernel(
-    TileParams P) {
+__device__ __forceinline__ void tile_product(const TileParams& P,
+                                             uint8_t* smem_all, int tile,
+                                             int split) {
   constexpr int BI = W / 64;                      // 32-blocks a wave and side
   constexpr int kTile = W * kBK * 2;              // bytes of one operand tile
   constexpr int kLd = W + 4;                      // fp32 stage stride
-  constexpr int kSmem =
-      NG * 4 * kTile > W * kLd * 4 ? NG * 4 * kTile : W * kLd * 4;
   constexpr bool kDual = EPI == kAct;
-  __shared__ __attribute__((aligned(16))) uint8_t smem_all[kSmem];
-
   const int grp = NG == 1 ? 0
                           : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
   uint8_t* const smem = smem_all + grp * 4 * kTile;
   const int wm = wave >> 1, wn = wave & 1;
-  // tiles an XCD gets are consecutive; blocks of 8 m-tiles, m fastest, so
-  // that they share B columns and A rows in its L2
-  const int id = xcd_remap(blockIdx.x, P.mtn * P.ntn);
+  // blocks of 8 m-tiles, m fastest: the consecutive tiles that an XCD gets
+  // share B columns and A rows in its L2
   const int per = 8 * P.ntn;
-  const int mb = id / per;
+  const int mb = tile / per;
   const int mh = min(8, P.mtn - mb * 8);
-  const int rem = id - mb * per;
+  const int rem = tile - mb * per;
   const int mt = mb * 8 + rem % mh, nt = rem / mh;
   const int m0 = mt * W;
   const int n0 = nt * (kDual ? W / 2 : W);
   // the workgroup's range of the reduction, then the group's; groups take
   // equally many steps (barriers are shared), empty past the range's end
-  const int kb0 = blockIdx.y * P.kchunk;
+  const int kb0 = split * P.kchunk;
   const int kend0 = min(P.K, kb0 + P.kchunk);
   const int nk = ((kend0 - kb0 + kBK - 1) / kBK + NG - 1) / NG;
   const int kbeg = kb0 + grp * nk * kBK;
@@ -430,11 +436,44 @@ __global__ __launch_bounds__(256 * NG, NG == 1 ? 2 : 1) void ffn_tile_kernel(
       }
       *reinterpret_cast<i32x4*>(P.C + ro * P.ldc + col) = pack8(x);
     } else {
-      float* o = P.Cf + (blockIdx.y * static_cast<int64_t>(P.M) + ro) * P.N +
-                 col;
+      float* o = P.Cf + (split * static_cast<int64_t>(P.M) + ro) * P.N + col;
       *reinterpret_cast<f32x4*>(o) = f32x4{x[0], x[1], x[2], x[3]};
       *reinterpret_cast<f32x4*>(o + 4) = f32x4{x[4], x[5], x[6], x[7]};
     }
+  }
+}
+
+template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
+__global__ __launch_bounds__(256 * NG, NG == 1 ? 2 : 1) void ffn_tile_kernel(
+    TileParams P) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_smem<W, NG>()];
+  tile_product<W, NG, AKC, BKC, EPI, ACT>(
+      P, smem, xcd_remap(blockIdx.x, P.mtn * P.ntn), blockIdx.y);
+}
+
+// Two independent products of the backward in one launch: a row product `a`
+// (dS with its activation, or dx) and a weight gradient `b`.  One's last
+// round of tiles runs beside the other's, and the gap of a launch is saved.
+struct PairParams {
+  TileParams a, b;
+  int splits_a;
+  int b_first;         // the product with the longer tiles goes first
+};
+
+template <int W, int EPI, int ACT>
+__global__ __launch_bounds__(256, 2) void ffn_pair_kernel(PairParams P) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_smem<W, 1>()];
+  const int ta = P.a.mtn * P.a.ntn, na = ta * P.splits_a;
+  const int nb = P.b.mtn * P.b.ntn;
+  const int id = blockIdx.x;
+  const int ia = P.b_first ? id - nb : id, ib = P.b_first ? id : id - na;
+  if (ia >= 0 && ia < na) {
+    const int split = ia / ta;
+    tile_product<W, 1, true, false, EPI, ACT>(
+        P.a, smem, xcd_remap(ia - split * ta, ta), split);
+  } else {
+    tile_product<W, 1, false, false, kRow, kActSilu>(P.b, smem,
+                                                     xcd_remap(ib, nb), 0);
   }
 }
 
@@ -638,6 +677,7 @@ hipError_t tile_w(TileParams P, int splits, hipStream_t s) {
 // `splits` ranges of kchunk.
 struct Plan {
   int width, groups, splits, kchunk;
+  double us;           // estimated time
 };
 
 template <bool AKC, bool BKC, int EPI, int ACT>
@@ -649,6 +689,22 @@ hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
                : tile_w<64, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
   return r.groups == 1 ? tile_w<128, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
                        : tile_w<128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
+}
+
+constexpr double kA[3] = {0.15, 0.08, 0.0}, kB[3] = {0.16, 0.43, 1.3};
+
+// Microseconds of moving the operands and the result of a product once.
+double move_us(int64_t M, int64_t N, int64_t K) {
+  const double m = static_cast<double>(M), n = static_cast<double>(N),
+               k = static_cast<double>(K);
+  return 2 * (m * k + n * k + m * n) / 4.5e6;
+}
+
+// Microseconds of summing `splits` fp32 planes of M x N.
+double planes_us(int64_t splits, int64_t M, int64_t N) {
+  return splits < 2 ? 0.0
+                    : 4 + static_cast<double>(splits * M) *
+                              static_cast<double>(N) * 8 / 4e6;
 }
 
 // The form with the least estimated time.  cols: output columns of a
@@ -668,7 +724,7 @@ hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
 Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
           bool allow256 = true) {
   const int64_t steps = (K + kBK - 1) / kBK;
-  constexpr double kA[3] = {0.15, 0.08, 0.0}, kB[3] = {0.16, 0.43, 1.3};
+  const double least = move_us(M, N * (256 / cols), K);
   Plan best{};
   double best_us = 1e30;
   for (int wi = 0; wi < (allow256 ? 3 : 2); ++wi) {
@@ -681,20 +737,81 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
       for (int g = 1; g <= 2; ++g) {
         if (g == 2 && (wi == 2 || n > 1)) break;
         double us = (kA[wi] + kB[wi] * g * n) *
-                        static_cast<double>((per + g - 1) / g) + 3 + g;
-        if (sp > 1)
-          us += 4 + static_cast<double>(sp * M) * static_cast<double>(N) *
-                        8 / 4e6;
+                        static_cast<double>((per + g - 1) / g) + 3 + g +
+                    planes_us(sp, M, N);
         if (us < best_us) {
           best_us = us;
           best = Plan{static_cast<int>(w), g,
                       static_cast<int>((steps + per - 1) / per),
-                      static_cast<int>(per * kBK)};
+                      static_cast<int>(per * kBK), us};
         }
       }
     }
   }
+  if (best.us < least) best.us = least;
   return best;
+}
+
+// The same for a row product a (M x Na over Ka; split: its reduction may be
+// cut) and a weight gradient b (Mb x Nb over M rows) in one launch of
+// `width`-wide tiles, which fill the CUs together: all k-steps at the full
+// CU's rate, and half of the longest tile for the ragged end.  Width 0: not
+// better than the two launches, which take `apart`; also where the pair
+// would be bound by memory, since interleaving two such streams costs more
+// than a launch.  (Backward of 64 x 2048 x 1408: 37 us apart, 31 us in
+// pairs; of 2000 x 2048 x 1408: 104 and 97 us; of 64 x 4096 x 14336, bound
+// by memory: 209 and 233 us.)
+Plan pair_plan(int64_t M, int64_t Na, int64_t Ka, bool split, int64_t Mb,
+               int64_t Nb, double apart) {
+  const double least = move_us(M, Na, Ka) + move_us(Mb, Nb, M);
+  Plan best{0, 1, 1, 0, apart};
+  const int64_t sa = (Ka + kBK - 1) / kBK, sb = (M + kBK - 1) / kBK;
+  for (int wi = 0; wi < 2; ++wi) {
+    const int64_t w = int64_t{64} << wi;
+    const double ta = static_cast<double>((M + w - 1) / w) *
+                      static_cast<double>((Na + w - 1) / w);
+    const double tb = static_cast<double>((Mb + w - 1) / w) *
+                      static_cast<double>((Nb + w - 1) / w);
+    for (int64_t sp = 1; sp <= (split ? 8 : 1); sp *= 2) {
+      if (sp > 1 && sp * 4 > sa) break;
+      const int64_t per = (sa + sp - 1) / sp;
+      const double work = (ta * static_cast<double>(sa) +
+                           tb * static_cast<double>(sb)) * kB[wi] / 256;
+      const double one = static_cast<double>(per > sb ? per : sb) *
+                         (kA[wi] + kB[wi]);
+      const double us = (work > one ? work : one) + 0.5 * one + 4 +
+                        planes_us(sp, M, Na);
+      if (us > least && us < best.us)
+        best = Plan{static_cast<int>(w), 1,
+                    static_cast<int>((sa + per - 1) / per),
+                    static_cast<int>(per * kBK), us};
+    }
+  }
+  return best;
+}
+
+template <int W, int EPI, int ACT>
+hipError_t pair_w(PairParams P, hipStream_t s) {
+  for (TileParams* t : {&P.a, &P.b}) {
+    t->mtn = (t->M + W - 1) / W;
+    t->ntn = (t->N + W - 1) / W;
+  }
+  P.b_first = P.b.kchunk > P.a.kchunk;
+  const uint32_t grid = static_cast<uint32_t>(P.a.mtn) * P.a.ntn *
+                            P.splits_a +
+                        static_cast<uint32_t>(P.b.mtn) * P.b.ntn;
+  hipLaunchKernelGGL((ffn_pair_kernel<W, EPI, ACT>), dim3(grid), dim3(256), 0,
+                     s, P);
+  return hipGetLastError();
+}
+
+template <int EPI, int ACT>
+hipError_t pair(const TileParams& a, const TileParams& b, const Plan& r,
+                hipStream_t s) {
+  PairParams P{a, b, r.splits, 0};
+  P.a.kchunk = r.kchunk;
+  return r.width == 64 ? pair_w<64, EPI, ACT>(P, s)
+                       : pair_w<128, EPI, ACT>(P, s);
 }
 
 hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
@@ -723,19 +840,25 @@ size_t up256(int64_t v) {
   return (static_cast<size_t>(v) + 255) & ~static_cast<size_t>(255);
 }
 
-// out[T][N] = add + A . B (B K-contiguous or not) by tiles.
-template <bool BKC>
-hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
-                       int64_t T, int64_t N, int64_t K, const bf16_t* add,
-                       bf16_t* out, float* planes, hipStream_t s) {
+TileParams row_params(const bf16_t* A, const bf16_t* B, int64_t ldb,
+                      int64_t T, int64_t N, int64_t K) {
   TileParams P{};
   P.A = A; P.lda = K;
   P.B = B; P.ldb = ldb; P.b_rows = N;
   P.M = static_cast<int>(T); P.N = static_cast<int>(N);
   P.K = static_cast<int>(K);
+  return P;
+}
+
+// out[T][N] = add + A . B (B K-contiguous or not).
+template <bool BKC>
+hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
+                       int64_t T, int64_t N, int64_t K, const bf16_t* add,
+                       bf16_t* out, float* planes, hipStream_t s) {
   const Plan r = plan(T, N, K, 256, true);
   if (r.width == 256)
     return gemm_dense_rows(A, B, BKC, T, N, K, add, out, s);
+  TileParams P = row_params(A, B, ldb, T, N, K);
   if (r.splits == 1) {
     P.C = out; P.ldc = N; P.AB = add;
     return tile<true, BKC, kRow, kActSilu>(P, r, s);
@@ -747,20 +870,28 @@ hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
 }
 
 // c[M][N] = sum_t a[t][m] b[t][n]
-hipError_t weight_product(const bf16_t* a, const bf16_t* b, int64_t T,
-                          int64_t M, int64_t N, bf16_t* c, hipStream_t s) {
+Plan weight_plan(int64_t T, int64_t M, int64_t N) {
   // the 256-wide kernel addresses an operand's rows with 32 bits
   const bool fits = T * (M > N ? M : N) * 2 <= kMaxResourceBytes;
-  const Plan r = plan(M, N, T, 256, false, fits);
-  if (r.width == 256)
-    return gemm_dense_wgrad(a, b, T, M, N, c, s);
+  return plan(M, N, T, 256, false, fits);
+}
+TileParams weight_params(const bf16_t* a, const bf16_t* b, int64_t T,
+                         int64_t M, int64_t N, bf16_t* c) {
   TileParams P{};
   P.A = a; P.lda = M;
   P.B = b; P.ldb = N;
   P.M = static_cast<int>(M); P.N = static_cast<int>(N);
   P.K = static_cast<int>(T);
+  P.kchunk = (P.K + kBK - 1) / kBK * kBK;
   P.C = c; P.ldc = N;
-  return tile<false, false, kRow, kActSilu>(P, r, s);
+  return P;
+}
+hipError_t weight_product(const bf16_t* a, const bf16_t* b, int64_t T,
+                          int64_t M, int64_t N, bf16_t* c, hipStream_t s) {
+  const Plan r = weight_plan(T, M, N);
+  if (r.width == 256) return gemm_dense_wgrad(a, b, T, M, N, c, s);
+  return tile<false, false, kRow, kActSilu>(
+      weight_params(a, b, T, M, N, c), r, s);
 }
 
 template <int ACT>
@@ -786,20 +917,64 @@ hipError_t fc1(const bf16_t* x, const bf16_t* w_gu, int64_t T, int64_t d,
   return tile<true, true, kAct, ACT>(P, r, s);
 }
 
+// A second launch costs about this much more than its kernel.
+constexpr double kLaunchUs = 2;
+
+// dAB, and dW2 unless it is null.
 template <int ACT>
-hipError_t dact(const bf16_t* dy, const bf16_t* w2, const bf16_t* ab,
-                int64_t T, int64_t d, int64_t f, bf16_t* dab,
-                hipStream_t s) {
+hipError_t dact_dw2(const bf16_t* dy, const bf16_t* w2, const bf16_t* ab,
+                    const bf16_t* s_saved, int64_t T, int64_t d, int64_t f,
+                    bf16_t* dab, bf16_t* dw2, hipStream_t s) {
   const Plan r = plan(T, f, d, 256, false);
+  TileParams P = row_params(dy, w2, f, T, f, d);
+  P.C = dab; P.ldc = 2 * f; P.AB = ab;
+  if (dw2) {
+    const double apart = r.us + weight_plan(T, d, f).us + kLaunchUs;
+    const Plan both = pair_plan(T, f, d, false, d, f, apart);
+    if (both.width)
+      return pair<kDAct, ACT>(P, weight_params(dy, s_saved, T, d, f, dw2),
+                              both, s);
+    hipError_t e = weight_product(dy, s_saved, T, d, f, dw2, s);
+    if (e != hipSuccess) return e;
+  }
   if (r.width == 256)
     return gemm_dense_fc2_dgrad(dy, w2, T, d, f, ACT, ab, dab, s);
-  TileParams P{};
-  P.A = dy; P.lda = d;
-  P.B = w2; P.ldb = f; P.b_rows = d;
-  P.M = static_cast<int>(T); P.N = static_cast<int>(f);
-  P.K = static_cast<int>(d);
-  P.C = dab; P.ldc = 2 * f; P.AB = ab;
   return tile<true, false, kDAct, ACT>(P, r, s);
+}
+
+// The launch of dx together with dW_gu (width 0: apart).
+Plan dx_pair(int64_t T, int64_t d, int64_t f) {
+  const double apart = plan(T, d, 2 * f, 256, true).us +
+                       weight_plan(T, 2 * f, d).us + kLaunchUs;
+  return pair_plan(T, d, 2 * f, true, 2 * f, d, apart);
+}
+
+// dx and dW_gu, either of them null to skip it.
+hipError_t dx_dw_gu(const bf16_t* dab, const bf16_t* x, const bf16_t* w_gu,
+                    const bf16_t* dx_add, int64_t T, int64_t d, int64_t f,
+                    bf16_t* dx, bf16_t* dw_gu, float* planes,
+                    hipStream_t s) {
+  if (dx && dw_gu) {
+    const Plan r = dx_pair(T, d, f);
+    if (r.width) {
+      TileParams P = row_params(dab, w_gu, d, T, d, 2 * f);
+      const TileParams Q = weight_params(dab, x, T, 2 * f, d, dw_gu);
+      if (r.splits == 1) {
+        P.C = dx; P.ldc = d; P.AB = dx_add;
+        return pair<kRow, kActSilu>(P, Q, r, s);
+      }
+      P.Cf = planes;
+      hipError_t e = pair<kPlane, kActSilu>(P, Q, r, s);
+      if (e != hipSuccess) return e;
+      return finish_rows(planes, r.splits, T * d, dx_add, dx, s);
+    }
+  }
+  if (dw_gu) {
+    hipError_t e = weight_product(dab, x, T, 2 * f, d, dw_gu, s);
+    if (e != hipSuccess || !dx) return e;
+  }
+  if (!dx) return hipSuccess;
+  return row_product<false>(dab, w_gu, d, T, d, 2 * f, dx_add, dx, planes, s);
 }
 
 // Workspaces.  Forward: S (when the caller keeps none), then the fp32
@@ -817,7 +992,10 @@ size_t ffn_fwd_workspace(int64_t T, int64_t d, int64_t f) {
 }
 
 size_t ffn_bwd_workspace(int64_t T, int64_t d, int64_t f) {
-  return up256(T * 2 * f * 2) + up256(plane_bytes(T, d, 2 * f));
+  const Plan r = dx_pair(T, d, f);
+  const int64_t alone = plane_bytes(T, d, 2 * f);
+  const int64_t both = r.width && r.splits > 1 ? r.splits * T * d * 4 : 0;
+  return up256(T * 2 * f * 2) + up256(alone > both ? alone : both);
 }
 
 hipError_t launch_ffn_fwd(int act, const bf16_t* x, const bf16_t* w_gu,
@@ -852,20 +1030,12 @@ hipError_t launch_ffn_bwd(int act, const bf16_t* dy, const bf16_t* x,
   bf16_t* dab = static_cast<bf16_t*>(ws);
   float* planes = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                            up256(T * 2 * f * 2));
-  hipError_t e = act == kActSilu
-                     ? dact<kActSilu>(dy, w2, ab, T, d, f, dab, s)
-                     : dact<kActGeluTanh>(dy, w2, ab, T, d, f, dab, s);
+  hipError_t e =
+      act == kActSilu
+          ? dact_dw2<kActSilu>(dy, w2, ab, s_saved, T, d, f, dab, dw2, s)
+          : dact_dw2<kActGeluTanh>(dy, w2, ab, s_saved, T, d, f, dab, dw2, s);
   if (e != hipSuccess) return e;
-  if (dw2) {
-    e = weight_product(dy, s_saved, T, d, f, dw2, s);
-    if (e != hipSuccess) return e;
-  }
-  if (dw_gu) {
-    e = weight_product(dab, x, T, 2 * f, d, dw_gu, s);
-    if (e != hipSuccess) return e;
-  }
-  if (!dx) return hipSuccess;
-  return row_product<false>(dab, w_gu, d, T, d, 2 * f, dx_add, dx, planes, s);
+  return dx_dw_gu(dab, x, w_gu, dx_add, T, d, f, dx, dw_gu, planes, s);
 }
 
 }  // namespace moe
