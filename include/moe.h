@@ -577,7 +577,8 @@ int64_t moe_mxfp8_padded_rows(int64_t rows, int32_t nseg);
  *   RMS).  Statistics are fp32, the variance is summed from centred values,
  *   y is rounded once.
  * d a multiple of 8 and at most 16384 (MOE_ERR_UNSUPPORTED above), T >= 1,
- * eps >= 0 and finite.  Outputs must overlap neither inputs nor each other.
+ * eps >= 0 and finite.  A row's squares must stay finite in fp32 (|x| below
+ * about 1e17 at any width).  Outputs must overlap neither inputs nor each other.
  * No workspace.
  */
 moe_status moe_norm_fwd(moe_norm kind, const void* x, int32_t x_fp32,
@@ -647,8 +648,8 @@ moe_status moe_dropout(const void* x, int32_t x_fp32, const void* res,
  * fp32 accumulation; S is computed from the fp32 sums and rounded to bf16
  * for the second product, y is rounded once.  One to a few tokens stream the
  * weights once; the bits of a row may differ between calls of different T.
- * d and f multiples of 8, 1 <= T < 2^30, the w_gu tensor at most
- * 4 GiB - 256 B (MOE_ERR_UNSUPPORTED above).  Workspace: MOE_ENTRY_FFN_FWD.
+ * d and f multiples of 8 and at most 2^21, 1 <= T < 2^30, the w_gu tensor
+ * at most 4 GiB - 256 B (MOE_ERR_UNSUPPORTED above).  Workspace: MOE_ENTRY_FFN_FWD.
  */
 moe_status moe_ffn_fwd(moe_act act, const void* x, const void* w_gu,
                        const void* w2, const void* y_add, int64_t T,

@@ -324,10 +324,14 @@ moe_status check_norm_dims(moe_norm kind, int64_t T, int64_t d) {
   return MOE_OK;
 }
 
+// A tile's 256 rows of the widest operand (dAB, 2f wide) stay inside a
+// buffer resource up to this width.
+constexpr int64_t kMaxFfnWidth = int64_t{1} << 21;
+
 bool ffn_dims_ok(int64_t T, int64_t d, int64_t f) {
   return T >= 1 && T < (int64_t{1} << 30) && d >= 8 && d % 8 == 0 &&
-         f >= 8 && f % 8 == 0 && f <= (int64_t{1} << 28) &&
-         d <= kMaxRange / (4 * f);
+         f >= 8 && f % 8 == 0 && d <= kMaxFfnWidth && f <= kMaxFfnWidth &&
+         4 * d * f <= kMaxRange;
 }
 
 moe_status check_ffn_dims(moe_act act, int64_t T, int64_t d, int64_t f) {
@@ -339,7 +343,8 @@ moe_status check_ffn_dims(moe_act act, int64_t T, int64_t d, int64_t f) {
   if (moe_status st = check_feature("d", d, MOE_BF16)) return st;
   if (moe_status st = check_feature("f", f, MOE_BF16)) return st;
   REQUIRE(ffn_dims_ok(T, d, f), MOE_ERR_UNSUPPORTED,
-          "T must be below 2^30 and w_gu at most 4 GiB - 256 B");
+          "T must be below 2^30, d and f at most 2^21 and w_gu at most "
+          "4 GiB - 256 B");
   return MOE_OK;
 }
 

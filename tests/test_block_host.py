@@ -128,7 +128,8 @@ def _ffn(act=0, x=at(0), w_gu=at(1), w2=at(2), y_add=None, T=4, d=64, f=128,
 @pytest.mark.parametrize("kw,want", [
     (dict(act=2), INVALID), (dict(T=0), INVALID), (dict(d=12), INVALID),
     (dict(f=12), INVALID), (dict(f=0), INVALID), (dict(T=1 << 30), UNSUP),
-    (dict(d=1 << 16, f=1 << 14), UNSUP), (dict(d=1 << 40, f=1 << 40), UNSUP),
+    (dict(d=1 << 16, f=1 << 14), UNSUP), (dict(d=(1 << 21) + 8), UNSUP),
+    (dict(d=8, f=(1 << 21) + 8), UNSUP), (dict(d=1 << 40, f=1 << 40), UNSUP),
     (dict(x=None), INVALID), (dict(w_gu=None), INVALID),
     (dict(w2=None), INVALID), (dict(y=None), INVALID),
     (dict(y=at(5) + 8), INVALID), (dict(ws=None), INVALID),

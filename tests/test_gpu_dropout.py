@@ -158,3 +158,19 @@ def test_dropout_masks_of_neighbouring_calls_are_independent():
                   base[n:]):
         agree = (base[:n] == other).double().mean().item()
         assert abs(agree - 0.5) < 0.0118
+
+
+@gpu
+def test_dropout_past_32_bit_offsets():
+    """More than 2^31 elements (4.3 GB): the kept set around 2^31 and at the
+    end is the generator's, counters past 2^28 among them."""
+    dev = torch.device("cuda:0")
+    n = (1 << 31) + 8 * 100003 + 5
+    x = torch.ones(n, dtype=BF, device=dev)
+    rng = _rng(8, 9)
+    moe.moe_dropout(x, None, 0.5, rng, 1, x)
+    for first in (0, (1 << 31) - 512, n // 8 * 8 - 4096):
+        m = min(8192, n - first)
+        keep = B.dropout_draws(m, 8, 10, first) >= 32768
+        got = x[first:first + m].float().cpu().numpy()
+        np.testing.assert_array_equal(got, np.where(keep, 2.0, 0.0))

@@ -336,3 +336,96 @@ def test_ffn_in_a_graph_and_on_another_stream(T):
         torch.cuda.synchronize()
         assert all(torch.equal(out[n], ref[n]) for n in ref)
     g.check()
+
+
+def _ref_rows(act, D, ab, s, sl):
+    """Float64 backward pieces of the rows sl, on the GPU."""
+    f = D["w2"].shape[1]
+    a, u = ab[sl, :f].double(), ab[sl, f:].double()
+    if act == "silu":
+        g = torch.sigmoid(a)
+        h, slope = a * g, g * (1 + a * (1 - g))
+    else:
+        c = (2 / np.pi) ** 0.5
+        th = torch.tanh(c * (a + 0.044715 * a ** 3))
+        h = 0.5 * a * (1 + th)
+        slope = 0.5 * (1 + th) + 0.5 * a * (1 - th * th) * c * (
+            1 + 3 * 0.044715 * a * a)
+    ds = D["dy"][sl].double() @ D["w2"].double()
+    return torch.cat((ds * u * slope, ds * h), dim=1), h * u
+
+
+def _close(name, got, ref):
+    """Mean-square and worst error in units of h and of the mean square: a
+    chain of roundings <= h in random order, as above; the worst of up to
+    2^30 nearly Gaussian errors stays within 8 of their standard
+    deviations, which is below 1.6 h of the output's."""
+    err = got.double() - ref
+    rms = float(ref.square().mean().sqrt())
+    q = float(err.square().mean().sqrt()) / rms / H
+    w = float((err.abs() - H * ref.abs()).max()) / rms / H
+    print(f"{name}: rms {q:.2f} h, worst {w:.2f} h")
+    assert q <= 1.6 and w <= 8 * 1.6, name
+
+
+# products at which the 256-wide tiles are the estimated best, rows and
+# columns ending inside a tile
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,d,f", [(4090, 4088, 1032), (2050, 4096, 4088),
+                                   (8192, 2048, 4096)])
+def test_ffn_large_products(T, d, f, act):
+    g = Guarded()
+    D = _data(T, d, f, seed=T)
+    y, ab, s = _run(act, D, T, d, f, True, g)
+    y2, _, _ = _run(act, D, T, d, f, True, g, save=False)
+    assert torch.equal(y, y2)
+    x, wg, w2 = (D[k].double() for k in ("x", "w_gu", "w2"))
+    rab = x @ wg.t()
+    _close("ab", ab, rab)
+    # S and y from the exact gate and up, dAB from the saved ones
+    _, hu = _ref_rows(act, D, rab, s, slice(None))
+    _close("s", s, hu)
+    _close("y", y, hu @ w2.t() + D["y_add"].double())
+    dab, _ = _ref_rows(act, D, ab, s, slice(None))
+    dx, dwg, dw2 = _bwd(act, D, T, d, f, True, g, ab, s)
+    # each gradient alone too: its product in a launch of its own
+    alone = (g.new(T, d), g.new(2 * f, d), g.new(d, f))
+    for i in range(3):
+        o = [t if j == i else None for j, t in enumerate(alone)]
+        moe.moe_ffn_bwd(_act(act), D["dy"], D["x"], D["w_gu"], D["w2"], ab,
+                        s, D["dx_add"] if i == 0 else None, *o,
+                        _ws(moe.MOE_ENTRY_FFN_BWD, T, d, f, g))
+    for got in ((dx, dwg, dw2), alone):
+        _close("dx", got[0], dab @ wg + D["dx_add"].double())
+        _close("dw_gu", got[1], dab.t() @ x)
+        _close("dw2", got[2], D["dy"].double().t() @ s.double())
+    g.check()
+
+
+@gpu
+def test_ffn_past_32_bit_offsets():
+    """dAB of 80000 x 28672 bf16 passes 4 GiB and 2^31 elements: the far rows
+    are right and the weight gradients sum all of them."""
+    T, d, f = 80000, 64, 14336
+    g = Guarded()
+    D = _data(T, d, f, seed=6)
+    y, ab, s = _run("silu", D, T, d, f, False, g)
+    dx, dwg, dw2 = _bwd("silu", D, T, d, f, False, g, ab, s)
+    wg, w2 = D["w_gu"].double(), D["w2"].double()
+    rwg, rw2 = torch.zeros_like(wg), torch.zeros_like(w2)
+    for r0 in range(0, T, 8000):
+        sl = slice(r0, r0 + 8000)
+        x = D["x"][sl].double()
+        dab, _ = _ref_rows("silu", D, ab, s, sl)
+        rwg += dab.t() @ x
+        rw2 += D["dy"][sl].double().t() @ s[sl].double()
+        if r0 in (0, 72000):
+            rab = x @ wg.t()
+            _close("ab", ab[sl], rab)
+            hu = rab[:, :f] * torch.sigmoid(rab[:, :f]) * rab[:, f:]
+            _close("y", y[sl], hu @ w2.t())
+            _close("dx", dx[sl], dab @ wg)
+    _close("dw_gu", dwg, rwg)
+    _close("dw2", dw2, rw2)
+    g.check()

@@ -289,3 +289,42 @@ def test_norm_on_another_stream_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(out[n], ref[n]) for n in ref)
+
+
+@gpu
+def test_norm_past_32_bit_offsets():
+    """600000 x 4096 passes 2^31 elements: the last rows equal those of a
+    small call bit for bit (rows do not depend on one another), and the
+    gradient of beta sums all rows."""
+    dev = torch.device("cuda:0")
+    T, d, n = 600000, 4096, 64
+    x = torch.empty(T, d, dtype=BF, device=dev)
+    for r in range(0, T, 50000):
+        x[r:r + 50000].normal_()
+    gamma, beta = _data(1, d, F32, 1)[1:3]
+    new = lambda *s, dt=F32: torch.empty(*s, dtype=dt, device=dev)  # noqa
+
+    def call(xs):
+        t = xs.shape[0]
+        o = dict(y=new(t, d, dt=BF), mean=new(t), rstd=new(t))
+        moe.moe_norm_fwd(0, xs, gamma, beta, EPS, o["y"], o["mean"],
+                         o["rstd"])
+        dx, db = new(t, d, dt=BF), new(d)
+        ws = new(moe.moe_workspace_bytes(moe.MOE_ENTRY_NORM_BWD, 0, t, 1, 1,
+                                         d, 0), dt=torch.uint8)
+        moe.moe_norm_bwd(0, o["y"], xs, gamma, o["mean"], o["rstd"], None,
+                         dx, None, db, ws)
+        return o["y"], o["mean"], o["rstd"], dx, db
+
+    big, small = call(x), call(x[-n:].clone())
+    for a, b in zip(big[:4], small[:4]):
+        assert torch.equal(a[-n:], b)
+    ref = torch.zeros(d, dtype=torch.float64, device=dev)
+    mag = torch.zeros_like(ref)
+    for r in range(0, T, 50000):
+        v = big[0][r:r + 50000].double()
+        ref += v.sum(dim=0)
+        mag += v.abs().sum(dim=0)
+    # chains: the rows of a workgroup, then the partials of a wave, then 16
+    chain = T / 1024 + 1024 / 16 + 16
+    assert ((big[4].double() - ref).abs() <= chain * U * mag).all()
