@@ -326,5 +326,5 @@ def test_norm_past_32_bit_offsets():
         ref += v.sum(dim=0)
         mag += v.abs().sum(dim=0)
     # chains: the rows of a workgroup, then the partials of a wave, then 16
-    chain = T / 1024 + 1024 / 16 + 16
+    chain = T / 512 + 512 / 16 + 16
     assert ((big[4].double() - ref).abs() <= chain * U * mag).all()
