@@ -322,15 +322,17 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               fra[set][k][i], frb[set][k][j], acc[i][j], 0, 0, 0);
   };
-  // Instruction order: a group's fragment reads right after its first
-  // product, so that they land while the others run from registers; LDS
-  // stores and global loads one after each product.
+  // Instruction order: the next group's fragment reads, the LDS stores and
+  // the global loads a few after each product, the reads first, so that they
+  // land while later products run from registers (reads all behind the
+  // first product: 5% slower in 128-wide tiles).
   constexpr int kRd = kG * BI * ((AKC ? 1 : 2) + (BKC ? 1 : 2));
   constexpr int kMv = TileMover<W, AKC>::NP + TileMover<W, BKC>::NP;
   constexpr int kMf = 2 * BI * BI;               // products a section
   constexpr int kSgMfma = 0x008, kSgVmem = 0x020, kSgRead = 0x100,
                 kSgWrite = 0x200;
   constexpr int kPer = (kMv + kMf - 1) / kMf;    // moves a product
+  constexpr int kSpread = kMf < 4 ? kMf : 4;     // products with reads
   read_group(0, 0, 0);
   // step kt with kt % kDepth == q, a compile-time constant
   auto step = [&](int q, int kt) {
@@ -348,8 +350,8 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
 #pragma unroll
     for (int i = 0; i < kMf; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-      if (kGroups > 1 && i == 0)
-        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd, 0);
+      if (kGroups > 1 && i < kSpread)
+        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd / kSpread, 0);
       __builtin_amdgcn_sched_group_barrier(kSgWrite, kPer, 0);
       __builtin_amdgcn_sched_group_barrier(kSgVmem, kPer, 0);
     }
@@ -360,7 +362,8 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
 #pragma unroll
     for (int i = 0; i < kMf; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
-      if (i == 0) __builtin_amdgcn_sched_group_barrier(kSgRead, kRd, 0);
+      if (i < kSpread)
+        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd / kSpread, 0);
     }
   };
   int kt0 = 0;
@@ -508,7 +511,11 @@ __global__ __launch_bounds__(256) void ffn_rows_kernel(
 // MFMA's A operand (16 rows x 32 k, one 16-byte load a lane straight from
 // global memory) and tokens its B operand; the next chunk's loads are in
 // flight during the current chunk's products.  The waves' sums are added
-// in wave order through LDS.
+// in wave order through LDS.  With more than 16 tokens their traffic counts:
+// a wave then loads its chunk of x as whole 256-byte rows and turns it into
+// fragments through its own piece of LDS, in place of 16 rows x 64 bytes a
+// load (64 tokens over 2048 x 1408: 20.9 -> 16.7 us, 24 tokens 13.2 -> 12.4;
+// up to 16 tokens the turn only adds its latency: 8.9 -> 10.7 us for one).
 //   RT = 16: kAct has a gate and an up tile; RT = 8: kAct packs 8 gate and
 //   8 up rows into one tile, kRow leaves half of its tile empty.  8 doubles
 //   the workgroups where 16 would leave CUs without one.
@@ -524,7 +531,12 @@ struct ThinParams {
 template <int NTB, int NWV, int RT, int EPI, int ACT>
 __global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
   constexpr int NWT = (EPI == kAct && RT == 16) ? 2 : 1;   // weight tiles
-  __shared__ float red[NWV][NWT][NTB][256];
+  constexpr bool kStageX = NTB > 1;
+  constexpr int kRedBytes = NWV * NWT * NTB * 1024;
+  constexpr int kXBytes = kStageX ? NWV * NTB * 4096 : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t
+      smem[kRedBytes > kXBytes ? kRedBytes : kXBytes];
+  auto red = reinterpret_cast<float (*)[NWT][NTB][256]>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int fr = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * RT;
@@ -550,18 +562,19 @@ __global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
                       static_cast<uint32_t>(nr) * ld2);
     wv = fr < nr ? fr * ld2 : kOob;
   }
-  __amdgpu_buffer_rsrc_t rx[NTB];
-  uint32_t xv[NTB];
+  const auto rx = make_rsrc(P.X, static_cast<uint32_t>(P.T) * ld2);
+  uint8_t* const xs = smem + wave * NTB * 4096;
+  const int xp = lane & 15;                      // staged: 16-byte piece
+  uint32_t xv[kStageX ? NTB * 4 : NTB];
 #pragma unroll
-  for (int b = 0; b < NTB; ++b) {
-    const int nt = max(0, min(16, P.T - 16 * b));
-    rx[b] = make_rsrc(P.X + static_cast<int64_t>(16 * b) * P.K,
-                      static_cast<uint32_t>(nt) * ld2);
-    xv[b] = fr < nt ? fr * ld2 : kOob;
+  for (int i = 0; i < (kStageX ? NTB * 4 : NTB); ++i) {
+    const int t = kStageX ? 4 * i + g : 16 * i + fr;
+    xv[i] = t < P.T ? static_cast<uint32_t>(t) * ld2 : kOob;
   }
 
+  // x: fragment b of k-slice s (4 b + s), or staged the rows 4 i + lane / 16
   struct Chunk {
-    i32x4 w[NWT][4], x[NTB][4];
+    i32x4 w[NWT][4], x[NTB * 4];
   };
   Chunk cur, nxt;
   auto load = [&](Chunk& c, int kc) {
@@ -573,11 +586,26 @@ __global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
 #pragma unroll
       for (int i = 0; i < NWT; ++i)
         c.w[i][s] = buf_load16(rw[i], ok && wv != kOob ? wv + kb : kOob);
+      if constexpr (!kStageX)
 #pragma unroll
-      for (int b = 0; b < NTB; ++b)
-        c.x[b][s] = buf_load16(rx[b], ok && xv[b] != kOob ? xv[b] + kb
-                                                          : kOob);
+        for (int b = 0; b < NTB; ++b)
+          c.x[4 * b + s] =
+              buf_load16(rx, ok && xv[b] != kOob ? xv[b] + kb : kOob);
     }
+    if constexpr (kStageX) {
+      const int k = kc * 128 + xp * 8;
+#pragma unroll
+      for (int i = 0; i < NTB * 4; ++i)
+        c.x[i] = buf_load16(rx, k < P.K && xv[i] != kOob
+                                    ? xv[i] + static_cast<uint32_t>(k) * 2
+                                    : kOob);
+    }
+  };
+  // orders a wave's LDS writes before its own reads, and the reverse
+  auto wave_sync = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
   f32x4 acc[NWT][NTB];
 #pragma unroll
@@ -589,17 +617,35 @@ __global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
   if (kc < nkc) load(cur, kc);
   for (; kc < nkc; kc += NWV) {
     if (kc + NWV < nkc) load(nxt, kc + NWV);
+    if constexpr (kStageX) {
+      // piece p of row t in slot p ^ (t % 16): both the row-wise stores and
+      // the fragment reads (one piece of 16 rows) meet every bank once
+#pragma unroll
+      for (int i = 0; i < NTB * 4; ++i) {
+        const int t = 4 * i + g;
+        *reinterpret_cast<i32x4*>(xs + t * 256 + ((xp ^ (t & 15)) << 4)) =
+            cur.x[i];
+      }
+      wave_sync();
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int i = 0; i < NWT; ++i)
+      for (int b = 0; b < NTB; ++b) {
+        const i32x4 xf =
+            kStageX ? *reinterpret_cast<const i32x4*>(
+                          xs + (16 * b + fr) * 256 + (((4 * s + g) ^ fr) << 4))
+                    : cur.x[4 * b + s];
 #pragma unroll
-        for (int b = 0; b < NTB; ++b)
+        for (int i = 0; i < NWT; ++i)
           acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8_v, cur.w[i][s]),
-              __builtin_bit_cast(bf16x8_v, cur.x[b][s]), acc[i][b], 0, 0, 0);
+              __builtin_bit_cast(bf16x8_v, xf), acc[i][b], 0, 0, 0);
+      }
+    if constexpr (kStageX) wave_sync();
     cur = nxt;
   }
+  if constexpr (kStageX) __syncthreads();   // red takes the stages' place
 #pragma unroll
   for (int i = 0; i < NWT; ++i)
 #pragma unroll
@@ -656,8 +702,8 @@ hipError_t thin(const ThinParams& P, hipStream_t s) {
   if (ntb == 2)
     return narrow ? thin_rt<2, 8, EPI, ACT>(P, s)
                   : thin_rt<2, 16, EPI, ACT>(P, s);
-  return narrow ? thin_rt<4, 8, EPI, ACT>(P, s)
-                : thin_rt<4, 16, EPI, ACT>(P, s);
+  // four token blocks leave no registers for a second weight tile
+  return thin_rt<4, 8, EPI, ACT>(P, s);
 }
 
 // ---------------------------------------------------------- tile launches
@@ -827,8 +873,8 @@ hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
 // (every workgroup reads all of them), the tiles' hardly does up to 64, but
 // tiles of narrow blocks leave CUs idle.  Forward on MI355X, thin and tiles,
 // us: 16 tokens 11 and 18 (d 2048, f 1408), 18 and 21 (2048, 2816), 28 and
-// 35 (4096, 4096), 84 and 78 (4096, 14336); 24 tokens 13 and 19, 21 and 20,
-// 31 and 33, 101 and 76; 64 tokens 21 and 23, 38 and 23, 48 and 38, 163 and
+// 35 (4096, 4096), 84 and 78 (4096, 14336); 24 tokens 12 and 19, 20 and 20,
+// 32 and 33, 97 and 76; 64 tokens 17 and 23, 31 and 23, 50 and 38, 159 and
 // 82.
 bool thin_form(int64_t T, int64_t d, int64_t f) {
   const int64_t bytes = 6 * d * f;
