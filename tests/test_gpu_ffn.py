@@ -368,12 +368,12 @@ def _close(name, got, ref):
     assert q <= 1.6 and w <= 8 * 1.6, name
 
 
-# products at which the 256-wide tiles are the estimated best, rows and
-# columns ending inside a tile
+# products at which the 256-wide tiles are the estimated best: rows and
+# columns ending inside a tile, a last round that is half empty
 @gpu
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T,d,f", [(4090, 4088, 1032), (2050, 4096, 4088),
-                                   (8192, 2048, 4096)])
+                                   (8192, 2048, 4096), (4100, 4096, 6136)])
 def test_ffn_large_products(T, d, f, act):
     g = Guarded()
     D = _data(T, d, f, seed=T)
