@@ -26,7 +26,8 @@
  *  - All tensor pointers are DEVICE pointers owned by the caller; the
  *    library never allocates or frees memory.  Scratch memory is the
  *    caller's `workspace` (size from moe_workspace_bytes); it need not be
- *    zeroed.  The one exception, moe_permute_noalloc, uses a fixed
+ *    zeroed, and calls that may run at the same time (streams, graphs)
+ *    need one each.  The one exception, moe_permute_noalloc, uses a fixed
  *    per-GPU scratch array of the library instead (see there).
  *  - Row-major layouts.  bf16 tensors are passed as `void*` holding IEEE
  *    bfloat16 bit patterns.  Every tensor pointer must be 16-byte aligned.

@@ -375,7 +375,8 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     if (kt0 + q < nk) step(q, kt0 + q);
 
   // The whole tile goes through LDS as fp32 (after the K-loop's last barrier
-  // only fragments that no product uses are read there), then each thread takes 8 columns of a row at a time.
+  // only fragments that no product uses are read there), then each thread
+  // takes 8 columns of a row at a time.
   float* st = reinterpret_cast<float*>(smem_all);
 #pragma unroll
   for (int h = NG - 1; h >= 0; --h) {
@@ -737,6 +738,11 @@ hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
                        : tile_w<128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
 }
 
+// Workgroups of 256 threads that one launch holds (2^32 threads).
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+
+// Microseconds of a k-step on a CU with n tiles of 64, 128 or 256: kA + kB n
+// (see plan).
 constexpr double kA[3] = {0.15, 0.08, 0.0}, kB[3] = {0.16, 0.43, 1.3};
 
 // Microseconds of moving the operands and the result of a product once.
@@ -778,6 +784,7 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
     const int64_t tiles = ((M + w - 1) / w) * ((N + c - 1) / c);
     for (int64_t sp = 1; sp <= (split && wi < 2 ? 8 : 1); sp *= 2) {
       if (sp > 1 && sp * 4 > steps) break;       // at least 4 steps a split
+      if (tiles * sp > kMaxGroups / 2) break;
       const int64_t per = (steps + sp - 1) / sp;
       const double n = static_cast<double>((tiles * sp + 255) / 256);
       for (int g = 1; g <= 2; ++g) {
@@ -820,6 +827,7 @@ Plan pair_plan(int64_t M, int64_t Na, int64_t Ka, bool split, int64_t Mb,
                       static_cast<double>((Nb + w - 1) / w);
     for (int64_t sp = 1; sp <= (split ? 8 : 1); sp *= 2) {
       if (sp > 1 && sp * 4 > sa) break;
+      if (ta * static_cast<double>(sp) + tb > kMaxGroups) break;
       const int64_t per = (sa + sp - 1) / sp;
       const double work = (ta * static_cast<double>(sa) +
                            tb * static_cast<double>(sb)) * kB[wi] / 256;
@@ -1073,6 +1081,7 @@ hipError_t launch_ffn_bwd(int act, const bf16_t* dy, const bf16_t* x,
                           const bf16_t* dx_add, int64_t T, int64_t d,
                           int64_t f, bf16_t* dx, bf16_t* dw_gu, bf16_t* dw2,
                           void* ws, hipStream_t s) {
+  if (!dx && !dw_gu) return weight_product(dy, s_saved, T, d, f, dw2, s);
   bf16_t* dab = static_cast<bf16_t*>(ws);
   float* planes = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                            up256(T * 2 * f * 2));
