@@ -2,7 +2,9 @@
  * moe.h -- C-ABI of libmoe.so: the mixture-of-experts expert-MLP hot path
  * (top-k routing, permutation by expert, grouped GEMM with fused SwiGLU and
  * routing-weight scaling, optional MXFP8 block quantization, un-permute
- * combine; forward and backward) as hand-written HIP kernels for gfx950.
+ * combine; forward and backward) and the residual block around it (norm,
+ * dense gated feed-forward block, dropout) as hand-written HIP kernels for
+ * gfx950.
  *
  * Sources, cited by page title and section:
  *  [P1] "Efficient MoE Training for Biological Foundation Models" (NVIDIA

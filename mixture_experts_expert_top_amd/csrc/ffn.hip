@@ -16,6 +16,10 @@
 //    with the reduction split over workgroups.
 //  * large: bound by the matrix cores.  The grouped GEMM's 256 x 256 kernel
 //    without its routing plan (gemm.hip, gemm_dense_*).
+// On MI355X: 1 token through d 4096, f 14336 forward 66 us (5.3 TB/s of
+// weights); 24 through 2048 x 1408 10.3 us; 777 through 2048 x 2816 51 us
+// (520 TFLOP/s); 2000 through it forward and backward 248 us (840 TFLOP/s);
+// 8192 through 4096 x 14336 6.8 to 7.0 ms (1240 to 1280 TFLOP/s).
 
 #include "common.cuh"
 #include "internal.h"
