@@ -516,11 +516,11 @@ __global__ __launch_bounds__(256) void ffn_rows_kernel(
 // MFMA's A operand (16 rows x 32 k, one 16-byte load a lane straight from
 // global memory) and tokens its B operand; the next chunk's loads are in
 // flight during the current chunk's products.  The waves' sums are added
-// in wave order through LDS.  With more than 16 tokens their traffic counts:
-// a wave then loads its chunk of x as whole 256-byte rows and turns it into
-// fragments through its own piece of LDS, in place of 16 rows x 64 bytes a
-// load (64 tokens over 2048 x 1408: 20.9 -> 16.7 us, 24 tokens 13.2 -> 12.4;
-// up to 16 tokens the turn only adds its latency: 8.9 -> 10.7 us for one).
+// in wave order through LDS.  Past a few tokens (kStageX) a wave loads its
+// chunk of x as whole 256-byte rows and turns it into fragments through its
+// own piece of LDS, in place of 16 rows x 64 bytes a load (2048 x 1408: 64
+// tokens 20.9 -> 16.7 us, 24 tokens 13.2 -> 12.4, 16 tokens 11.1 -> 10.3; one
+// token, where the turn only adds its latency, 8.7 -> 9.6).
 //   RT = 16: kAct has a gate and an up tile; RT = 8: kAct packs 8 gate and
 //   8 up rows into one tile, kRow leaves half of its tile empty.  8 doubles
 //   the workgroups where 16 would leave CUs without one.
@@ -533,10 +533,10 @@ struct ThinParams {
   const bf16_t* add;   // kRow: [T][N] or null
 };
 
-template <int NTB, int NWV, int RT, int EPI, int ACT>
-__global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
+template <int NTB, bool kStageX, int RT, int EPI, int ACT>
+__global__ __launch_bounds__(512) void ffn_thin_kernel(ThinParams P) {
+  constexpr int NWV = 8;
   constexpr int NWT = (EPI == kAct && RT == 16) ? 2 : 1;   // weight tiles
-  constexpr bool kStageX = NTB > 1;
   constexpr int kRedBytes = NWV * NWT * NTB * 1024;
   constexpr int kXBytes = kStageX ? NWV * NTB * 4096 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t
@@ -689,26 +689,31 @@ __global__ __launch_bounds__(64 * NWV) void ffn_thin_kernel(ThinParams P) {
   }
 }
 
-template <int NTB, int RT, int EPI, int ACT>
+template <int NTB, bool kStageX, int RT, int EPI, int ACT>
 hipError_t thin_rt(const ThinParams& P, hipStream_t s) {
-  constexpr int NWV = 8;
-  hipLaunchKernelGGL((ffn_thin_kernel<NTB, NWV, RT, EPI, ACT>),
-                     dim3((P.N + RT - 1) / RT), dim3(64 * NWV), 0, s, P);
+  hipLaunchKernelGGL((ffn_thin_kernel<NTB, kStageX, RT, EPI, ACT>),
+                     dim3((P.N + RT - 1) / RT), dim3(512), 0, s, P);
   return hipGetLastError();
 }
+
+// Tokens whose fragments are loaded straight from x (see above).
+constexpr int kDirectTokens = 4;
 
 template <int EPI, int ACT>
 hipError_t thin(const ThinParams& P, hipStream_t s) {
   const int ntb = (P.T + 15) / 16;
   const bool narrow = P.N < 16 * 256;
+  if (P.T <= kDirectTokens)
+    return narrow ? thin_rt<1, false, 8, EPI, ACT>(P, s)
+                  : thin_rt<1, false, 16, EPI, ACT>(P, s);
   if (ntb == 1)
-    return narrow ? thin_rt<1, 8, EPI, ACT>(P, s)
-                  : thin_rt<1, 16, EPI, ACT>(P, s);
+    return narrow ? thin_rt<1, true, 8, EPI, ACT>(P, s)
+                  : thin_rt<1, true, 16, EPI, ACT>(P, s);
   if (ntb == 2)
-    return narrow ? thin_rt<2, 8, EPI, ACT>(P, s)
-                  : thin_rt<2, 16, EPI, ACT>(P, s);
+    return narrow ? thin_rt<2, true, 8, EPI, ACT>(P, s)
+                  : thin_rt<2, true, 16, EPI, ACT>(P, s);
   // four token blocks leave no registers for a second weight tile
-  return thin_rt<4, 8, EPI, ACT>(P, s);
+  return thin_rt<4, true, 8, EPI, ACT>(P, s);
 }
 
 // ---------------------------------------------------------- tile launches
@@ -884,8 +889,8 @@ hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
 // Whether the weight-streaming form runs.  Its time grows with the tokens
 // (every workgroup reads all of them), the tiles' hardly does up to 64, but
 // tiles of narrow blocks leave CUs idle.  Forward on MI355X, thin and tiles,
-// us: 16 tokens 11 and 18 (d 2048, f 1408), 18 and 21 (2048, 2816), 28 and
-// 35 (4096, 4096), 84 and 78 (4096, 14336); 24 tokens 12 and 19, 20 and 20,
+// us: 16 tokens 10 and 18 (d 2048, f 1408), 15 and 21 (2048, 2816), 26 and
+// 35 (4096, 4096), 75 and 78 (4096, 14336); 24 tokens 12 and 19, 20 and 20,
 // 32 and 33, 97 and 76; 64 tokens 17 and 23, 31 and 23, 50 and 38, 159 and
 // 82.
 bool thin_form(int64_t T, int64_t d, int64_t f) {

@@ -158,7 +158,8 @@ SIZES = [(1, 8, 8), (1, 2048, 1408), (2, 16, 24), (5, 264, 520),
          (48, 4104, 136), (64, 256, 264), (64, 64, 4096), (65, 8, 8),
          (65, 40, 136), (100, 264, 72), (128, 128, 64), (130, 520, 392),
          (257, 1032, 776), (300, 2048, 1408), (1100, 520, 1416),
-         (1500, 2056, 136), (20, 4096, 5632), (40, 2048, 2816)]
+         (1500, 2056, 136), (4, 264, 136), (8, 4104, 4104), (12, 136, 520),
+         (20, 4096, 5632), (40, 2048, 2816)]
 
 
 @gpu
