@@ -700,10 +700,13 @@ def _checked(name, specs):
     return dev, ptrs
 
 
-# The handle of a device's current stream, without building a Stream object
-# where torch offers that (1.2 us less of a 7 us call).
+# The handle of a device's current stream without building a Stream object,
+# and the current device's index, where torch offers them directly (1.4 us
+# less of a 7 us call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice",
+                          torch.cuda.current_device)
 
 
 def _enqueue(name, stream, dev, fn, *args):
@@ -715,7 +718,7 @@ def _enqueue(name, stream, dev, fn, *args):
             raise ValueError(f"{name}: tensors on cuda:{dev}, stream on "
                              f"{stream.device}")
         handle = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):

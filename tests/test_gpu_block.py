@@ -219,3 +219,68 @@ def test_block_refusals():
         blk.forward(D["x"], D["gamma"], D["w_gu"], D["w2"], w_g=D["w_g"])
     with pytest.raises(ValueError, match="bf16"):
         MoEBlock(MoEPath(16, 64, 64, 4, 2, device=dev, y_fp32=True))
+
+
+@gpu
+def test_tensors_on_different_devices_are_refused():
+    dev = torch.device("cuda:0")
+    x = torch.zeros(4, 64, dtype=BF, device=dev)
+    y, gamma = torch.empty_like(x), torch.ones(64)
+    with pytest.raises(ValueError, match="different devices"):
+        moe.moe_norm_fwd(0, x, gamma, None, 1e-5, y)
+    with pytest.raises(ValueError, match="different devices"):
+        moe.moe_dropout(x, None, 0.1, torch.zeros(2, dtype=torch.int64), 0, y)
+    # a view that starts off a 16-byte boundary is refused by the library
+    flat = torch.zeros(4 * 64 + 8, dtype=BF, device=dev)
+    with pytest.raises(moe.MoeError, match="aligned"):
+        moe.moe_norm_fwd(0, flat[4:4 + 256].view(4, 64), gamma.to(dev), None,
+                         1e-5, y)
+
+
+@gpu
+def test_calls_at_the_same_time_on_two_streams():
+    """Two steps of different data, each with its own buffers and workspaces,
+    issued in turn on two streams: the bits of each run alone."""
+    dev = torch.device("cuda:0")
+    T, d, f = 200, 264, 1032
+    sets = []
+    for seed in (1, 2):
+        mk = lambda shape, k, s=1.0, dt=BF: I.make_tensor(  # noqa: E731
+            shape, seed=seed * 17 + k, scale=s, dtype=dt, device=dev)
+        new = lambda *s, dt=BF: torch.empty(*s, dtype=dt, device=dev)  # noqa
+        ws = lambda e: new(max(16, moe.moe_workspace_bytes(  # noqa: E731
+            e, 0, T, 1, 1, d, f)), dt=torch.uint8)
+        sets.append(dict(
+            x=mk((T, d), 0), gamma=mk((d,), 1, dt=F32), dy=mk((T, d), 2),
+            wg=mk((2 * f, d), 3, d ** -0.5), w2=mk((d, f), 4, f ** -0.5),
+            n=new(T, d), rstd=new(T, dt=F32), ab=new(T, 2 * f), s=new(T, f),
+            y=new(T, d), dn=new(T, d), dwg=new(2 * f, d), dw2=new(d, f),
+            dx=new(T, d), dg=new(d, dt=F32), wf=ws(moe.MOE_ENTRY_FFN_FWD),
+            wb=ws(moe.MOE_ENTRY_FFN_BWD), wn=ws(moe.MOE_ENTRY_NORM_BWD),
+            rng=torch.tensor([seed, 3], dtype=torch.int64, device=dev)))
+
+    def step(b, st=None):
+        moe.moe_norm_fwd(1, b["x"], b["gamma"], None, 1e-5, b["n"], None,
+                         b["rstd"], stream=st)
+        moe.moe_ffn_fwd(0, b["n"], b["wg"], b["w2"], None, b["ab"], b["s"],
+                        b["y"], b["wf"], stream=st)
+        moe.moe_dropout(b["y"], b["x"], 0.2, b["rng"], 1, b["y"], stream=st)
+        moe.moe_ffn_bwd(0, b["dy"], b["n"], b["wg"], b["w2"], b["ab"],
+                        b["s"], None, b["dn"], b["dwg"], b["dw2"], b["wb"],
+                        stream=st)
+        moe.moe_norm_bwd(1, b["dn"], b["x"], b["gamma"], None, b["rstd"],
+                         b["dy"], b["dx"], b["dg"], None, b["wn"], stream=st)
+
+    outs = ["y", "dn", "dwg", "dw2", "dx", "dg"]
+    for b in sets:
+        step(b)
+    torch.cuda.synchronize()
+    refs = [[b[n].clone() for n in outs] for b in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, st in zip(sets, streams):
+            step(b, st)
+    torch.cuda.synchronize()
+    for b, ref in zip(sets, refs):
+        assert all(torch.equal(b[n], r) for n, r in zip(outs, ref))
