@@ -12,13 +12,13 @@
 //  * thin (few tokens): bound by reading the weights once.  ffn_thin_kernel
 //    streams them from global memory straight into MFMA fragments.
 //  * tile: bound by the latency of the K-loop and by how many CUs have a
-//    tile.  ffn_tile_kernel, 128 x 128 or 64 x 64 output tiles, optionally
-//    with the reduction split over workgroups.
+//    tile.  ffn_tile_kernel, 128 x 128, 128 x 64 or 64 x 64 output tiles,
+//    optionally with the reduction split over workgroups.
 //  * large: bound by the matrix cores.  The grouped GEMM's 256 x 256 kernel
 //    without its routing plan (gemm.hip, gemm_dense_*).
 // On MI355X: 1 token through d 4096, f 14336 forward 66 us (5.3 TB/s of
-// weights); 24 through 2048 x 1408 10.3 us; 777 through 2048 x 2816 51 us
-// (520 TFLOP/s); 2000 through it forward and backward 248 us (840 TFLOP/s);
+// weights); 24 through 2048 x 1408 10.3 us; 777 through 2048 x 2816 49 us
+// (550 TFLOP/s); 2000 through it forward and backward 248 us (840 TFLOP/s);
 // 8192 through 4096 x 14336 6.8 to 7.0 ms (1240 to 1280 TFLOP/s).
 
 #include "common.cuh"
@@ -56,7 +56,7 @@ struct TileParams {
 };
 
 constexpr int kBK = 64;
-// tiles in flight from global memory, 128- and 64-wide
+// tiles in flight from global memory, in 128 x 128 and in smaller tiles
 constexpr int kDepthWide = 2;
 constexpr int kDepthNarrow = 4;
 
@@ -214,32 +214,33 @@ __device__ __forceinline__ void lds8(const float* p, float* v) {
   }
 }
 
-// NG groups of 256 threads; a group is 2 x 2 waves, each (W / 2) x (W / 2)
-// of a W x W tile.  With two groups each runs half of the reduction out of
+// NG groups of 256 threads; a group is 2 x 2 waves, each (WM / 2) x (WN / 2)
+// of a WM x WN tile.  With two groups each runs half of the reduction out of
 // its own LDS stages and the second group's sums are added to the first's:
 // what a CU with a single tile needs to keep its matrix cores busy.
 //
 // The LDS of a tile: two stages of both operands a group, or the fp32 tile
-// of the epilogue (rows of W + 4).
-template <int W, int NG>
+// of the epilogue (rows of WN + 4).
+template <int WM, int WN, int NG>
 constexpr int tile_smem() {
-  constexpr int k = NG * 4 * W * kBK * 2, e = W * (W + 4) * 4;
+  constexpr int k = NG * 2 * (WM + WN) * kBK * 2, e = WM * (WN + 4) * 4;
   return k > e ? k : e;
 }
 
 // tile: index in the product's mtn x ntn tiles, already in XCD order.
-template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
+template <int WM, int WN, int NG, bool AKC, bool BKC, int EPI, int ACT>
 __device__ __forceinline__ void tile_product(const TileParams& P,
                                              uint8_t* smem_all, int tile,
                                              int split) {
-  constexpr int BI = W / 64;                      // 32-blocks a wave and side
-  constexpr int kTile = W * kBK * 2;              // bytes of one operand tile
-  constexpr int kLd = W + 4;                      // fp32 stage stride
+  constexpr int BM = WM / 64, BN = WN / 64;       // 32-blocks a wave and side
+  constexpr int kTileA = WM * kBK * 2;            // bytes of an operand's tile
+  constexpr int kTileB = WN * kBK * 2;
+  constexpr int kLd = WN + 4;                     // fp32 stage stride
   constexpr bool kDual = EPI == kAct;
   const int grp = NG == 1 ? 0
                           : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
-  uint8_t* const smem = smem_all + grp * 4 * kTile;
+  uint8_t* const smem = smem_all + grp * 2 * (kTileA + kTileB);
   const int wm = wave >> 1, wn = wave & 1;
   // blocks of 8 m-tiles, m fastest: the consecutive tiles that an XCD gets
   // share B columns and A rows in its L2
@@ -248,8 +249,8 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   const int mh = min(8, P.mtn - mb * 8);
   const int rem = tile - mb * per;
   const int mt = mb * 8 + rem % mh, nt = rem / mh;
-  const int m0 = mt * W;
-  const int n0 = nt * (kDual ? W / 2 : W);
+  const int m0 = mt * WM;
+  const int n0 = nt * (kDual ? WN / 2 : WN);
   // the workgroup's range of the reduction, then the group's; groups take
   // equally many steps (barriers are shared), empty past the range's end
   const int kb0 = split * P.kchunk;
@@ -258,20 +259,20 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   const int kbeg = kb0 + grp * nk * kBK;
   const int kend = min(kend0, kbeg + nk * kBK);
 
-  TileMover<W, AKC> ma;
-  TileMover<W, BKC> mb_;
+  TileMover<WM, AKC> ma;
+  TileMover<WN, BKC> mb_;
   ma.init(tid, P.A, P.lda, m0, P.M, false, 0);
   mb_.init(tid, P.B, P.ldb, n0, BKC ? P.b_rows : P.N, kDual, P.N);
-  TileFrag<W, AKC> fa;
-  TileFrag<W, BKC> fb;
+  TileFrag<WM, AKC> fa;
+  TileFrag<WN, BKC> fb;
   fa.init(lane);
   fb.init(lane);
 
-  f32x16 acc[BI][BI];
+  f32x16 acc[BM][BN];
 #pragma unroll
-  for (int i = 0; i < BI; ++i)
+  for (int i = 0; i < BM; ++i)
 #pragma unroll
-    for (int j = 0; j < BI; ++j) acc[i][j] = f32x16{};
+    for (int j = 0; j < BN; ++j) acc[i][j] = f32x16{};
 
   // LDS: [A 0][A 1][B 0][B 1], tile kt in stage kt & 1.  The registers hold
   // the next kDepth tiles from global memory and two sets of fragments:
@@ -281,11 +282,11 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   // refills the freed registers with tile kt + 1 + kDepth, and before its
   // last group's products passes the barrier that completes tile kt + 1 and
   // reads the first group of it.
-  constexpr int kDepth = W == 128 ? kDepthWide : kDepthNarrow;
+  constexpr int kDepth = WM + WN > 192 ? kDepthWide : kDepthNarrow;
   static_assert(kDepth % 2 == 0, "the LDS stage is a compile-time constant");
-  i32x4 va[kDepth][TileMover<W, AKC>::NP], vb[kDepth][TileMover<W, BKC>::NP];
+  i32x4 va[kDepth][TileMover<WM, AKC>::NP], vb[kDepth][TileMover<WN, BKC>::NP];
   {
-    i32x4 fa0[TileMover<W, AKC>::NP], fb0[TileMover<W, BKC>::NP];
+    i32x4 fa0[TileMover<WM, AKC>::NP], fb0[TileMover<WN, BKC>::NP];
     ma.load(fa0, kbeg, kend);
     mb_.load(fb0, kbeg, kend);
 #pragma unroll
@@ -297,32 +298,32 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     }
     __builtin_amdgcn_sched_barrier(0);
     ma.store(fa0, smem);
-    mb_.store(fb0, smem + 2 * kTile);
+    mb_.store(fb0, smem + 2 * kTileA);
   }
   __syncthreads();
-  constexpr int kG = W == 128 ? 2 : 4;           // k-slices a group
+  constexpr int kG = WM + WN > 128 ? 2 : 4;      // k-slices a group
   constexpr int kGroups = 4 / kG;
-  bf16x8_v fra[2][kG][BI], frb[2][kG][BI];
+  bf16x8_v fra[2][kG][BM], frb[2][kG][BN];
   auto read_group = [&](int set, int stage, int group) {
-    const uint8_t* ta = smem + stage * kTile;
-    const uint8_t* tb = smem + 2 * kTile + stage * kTile;
+    const uint8_t* ta = smem + stage * kTileA;
+    const uint8_t* tb = smem + 2 * kTileA + stage * kTileB;
 #pragma unroll
     for (int k = 0; k < kG; ++k) {
 #pragma unroll
-      for (int i = 0; i < BI; ++i)
-        fra[set][k][i] = fa.read(ta, wm * BI + i, group * kG + k);
+      for (int i = 0; i < BM; ++i)
+        fra[set][k][i] = fa.read(ta, wm * BM + i, group * kG + k);
 #pragma unroll
-      for (int j = 0; j < BI; ++j)
-        frb[set][k][j] = fb.read(tb, wn * BI + j, group * kG + k);
+      for (int j = 0; j < BN; ++j)
+        frb[set][k][j] = fb.read(tb, wn * BN + j, group * kG + k);
     }
   };
   auto products = [&](int set, int k0, int k1) {
 #pragma unroll
     for (int k = k0; k < k1; ++k)
 #pragma unroll
-      for (int i = 0; i < BI; ++i)
+      for (int i = 0; i < BM; ++i)
 #pragma unroll
-        for (int j = 0; j < BI; ++j)
+        for (int j = 0; j < BN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               fra[set][k][i], frb[set][k][j], acc[i][j], 0, 0, 0);
   };
@@ -330,13 +331,14 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   // the global loads a few after each product, the reads first, so that they
   // land while later products run from registers (reads all behind the
   // first product: 5% slower in 128-wide tiles).
-  constexpr int kRd = kG * BI * ((AKC ? 1 : 2) + (BKC ? 1 : 2));
-  constexpr int kMv = TileMover<W, AKC>::NP + TileMover<W, BKC>::NP;
-  constexpr int kMf = 2 * BI * BI;               // products a section
+  constexpr int kRd = kG * (BM * (AKC ? 1 : 2) + BN * (BKC ? 1 : 2));
+  constexpr int kMv = TileMover<WM, AKC>::NP + TileMover<WN, BKC>::NP;
+  constexpr int kMf = 2 * BM * BN;               // products a section
   constexpr int kSgMfma = 0x008, kSgVmem = 0x020, kSgRead = 0x100,
                 kSgWrite = 0x200;
   constexpr int kPer = (kMv + kMf - 1) / kMf;    // moves a product
   constexpr int kSpread = kMf < 4 ? kMf : 4;     // products with reads
+  constexpr int kRdPer = (kRd + kSpread - 1) / kSpread;
   read_group(0, 0, 0);
   // step kt with kt % kDepth == q, a compile-time constant
   auto step = [&](int q, int kt) {
@@ -345,8 +347,8 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     const int s2 = kGroups == 1 ? cs : 1;      // and after it
     __builtin_amdgcn_sched_barrier(0);
     if (kGroups > 1) read_group(1, cs, 1);
-    ma.store(va[q], smem + ns * kTile);
-    mb_.store(vb[q], smem + 2 * kTile + ns * kTile);
+    ma.store(va[q], smem + ns * kTileA);
+    mb_.store(vb[q], smem + 2 * kTileA + ns * kTileB);
     const int k2 = kbeg + (kt + 1 + kDepth) * kBK;
     ma.load(va[q], k2, kend);
     mb_.load(vb[q], k2, kend);
@@ -355,7 +357,7 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     for (int i = 0; i < kMf; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
       if (kGroups > 1 && i < kSpread)
-        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd / kSpread, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgRead, kRdPer, 0);
       __builtin_amdgcn_sched_group_barrier(kSgWrite, kPer, 0);
       __builtin_amdgcn_sched_group_barrier(kSgVmem, kPer, 0);
     }
@@ -367,7 +369,7 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     for (int i = 0; i < kMf; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSgMfma, 1, 0);
       if (i < kSpread)
-        __builtin_amdgcn_sched_group_barrier(kSgRead, kRd / kSpread, 0);
+        __builtin_amdgcn_sched_group_barrier(kSgRead, kRdPer, 0);
     }
   };
   int kt0 = 0;
@@ -386,25 +388,25 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   for (int h = NG - 1; h >= 0; --h) {
     if (grp == h)
 #pragma unroll
-      for (int i = 0; i < BI; ++i)
+      for (int i = 0; i < BM; ++i)
 #pragma unroll
-        for (int j = 0; j < BI; ++j)
+        for (int j = 0; j < BN; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
-            const int r = (wm * BI + i) * 32 + (v >> 2) * 8 +
+            const int r = (wm * BM + i) * 32 + (v >> 2) * 8 +
                           (lane >> 5) * 4 + (v & 3);
-            float* p = st + r * kLd + (wn * BI + j) * 32 + (lane & 31);
+            float* p = st + r * kLd + (wn * BN + j) * 32 + (lane & 31);
             *p = h == NG - 1 ? acc[i][j][v] : acc[i][j][v] + *p;
           }
     __syncthreads();
   }
-  constexpr int kCols = kDual ? W / 2 : W;
+  constexpr int kCols = kDual ? WN / 2 : WN;
   constexpr int kCh = kCols / 8;                  // chunks a row
   constexpr int kThr = 256 * NG;
 #pragma unroll
-  for (int it = 0; it < (W * kCh + kThr - 1) / kThr; ++it) {
+  for (int it = 0; it < (WM * kCh + kThr - 1) / kThr; ++it) {
     const int idx = static_cast<int>(threadIdx.x) + kThr * it;
-    if (W * kCh < kThr && idx >= W * kCh) continue;
+    if (WM * kCh < kThr && idx >= WM * kCh) continue;
     const int r = idx / kCh, c = (idx % kCh) * 8;
     const int row = m0 + r, col = n0 + c;
     if (row >= P.M || col >= P.N) continue;
@@ -413,7 +415,7 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
     const int64_t ro = static_cast<int64_t>(row);
     if constexpr (EPI == kAct) {
       float u[8], s[8];
-      lds8(st + r * kLd + W / 2 + c, u);
+      lds8(st + r * kLd + WN / 2 + c, u);
 #pragma unroll
       for (int q = 0; q < 8; ++q) s[q] = act_val<ACT>(x[q]) * u[q];
       if (P.C) {
@@ -451,11 +453,12 @@ __device__ __forceinline__ void tile_product(const TileParams& P,
   }
 }
 
-template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
+template <int WM, int WN, int NG, bool AKC, bool BKC, int EPI, int ACT>
 __global__ __launch_bounds__(256 * NG, NG == 1 ? 2 : 1) void ffn_tile_kernel(
     TileParams P) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_smem<W, NG>()];
-  tile_product<W, NG, AKC, BKC, EPI, ACT>(
+  __shared__ __attribute__((aligned(16))) uint8_t
+      smem[tile_smem<WM, WN, NG>()];
+  tile_product<WM, WN, NG, AKC, BKC, EPI, ACT>(
       P, smem, xcd_remap(blockIdx.x, P.mtn * P.ntn), blockIdx.y);
 }
 
@@ -470,17 +473,17 @@ struct PairParams {
 
 template <int W, int EPI, int ACT>
 __global__ __launch_bounds__(256, 2) void ffn_pair_kernel(PairParams P) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_smem<W, 1>()];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[tile_smem<W, W, 1>()];
   const int ta = P.a.mtn * P.a.ntn, na = ta * P.splits_a;
   const int nb = P.b.mtn * P.b.ntn;
   const int id = blockIdx.x;
   const int ia = P.b_first ? id - nb : id, ib = P.b_first ? id : id - na;
   if (ia >= 0 && ia < na) {
     const int split = ia / ta;
-    tile_product<W, 1, true, false, EPI, ACT>(
+    tile_product<W, W, 1, true, false, EPI, ACT>(
         P.a, smem, xcd_remap(ia - split * ta, ta), split);
   } else {
-    tile_product<W, 1, false, false, kRow, kActSilu>(P.b, smem,
+    tile_product<W, W, 1, false, false, kRow, kActSilu>(P.b, smem,
                                                      xcd_remap(ib, nb), 0);
   }
 }
@@ -717,42 +720,55 @@ hipError_t thin(const ThinParams& P, hipStream_t s) {
 }
 
 // ---------------------------------------------------------- tile launches
-template <int W, int NG, bool AKC, bool BKC, int EPI, int ACT>
+template <int WM, int WN, int NG, bool AKC, bool BKC, int EPI, int ACT>
 hipError_t tile_w(TileParams P, int splits, hipStream_t s) {
-  constexpr int wn = EPI == kAct ? W / 2 : W;
-  P.mtn = (P.M + W - 1) / W;
+  constexpr int wn = EPI == kAct ? WN / 2 : WN;
+  P.mtn = (P.M + WM - 1) / WM;
   P.ntn = (P.N + wn - 1) / wn;
-  hipLaunchKernelGGL((ffn_tile_kernel<W, NG, AKC, BKC, EPI, ACT>),
+  hipLaunchKernelGGL((ffn_tile_kernel<WM, WN, NG, AKC, BKC, EPI, ACT>),
                      dim3(static_cast<uint32_t>(P.mtn) * P.ntn, splits),
                      dim3(256 * NG), 0, s, P);
   return hipGetLastError();
 }
 
-// The form of one product: output tiles of `width` (64, 128, or 256 for the
-// grouped GEMM's kernel), `groups` of 256 threads a tile, the reduction in
+// The form of one product: output tiles of `height` x `width` (256 x 256 for
+// the grouped GEMM's kernel), `groups` of 256 threads a tile, the reduction in
 // `splits` ranges of kchunk.
 struct Plan {
-  int width, groups, splits, kchunk;
+  int height, width, groups, splits, kchunk;
   double us;           // estimated time
 };
 
 template <bool AKC, bool BKC, int EPI, int ACT>
 hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
   P.kchunk = r.kchunk;
+  if (r.width == 64 && r.height == 64)
+    return r.groups == 1
+               ? tile_w<64, 64, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
+               : tile_w<64, 64, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
   if (r.width == 64)
     return r.groups == 1
-               ? tile_w<64, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
-               : tile_w<64, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
-  return r.groups == 1 ? tile_w<128, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
-                       : tile_w<128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
+               ? tile_w<128, 64, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
+               : tile_w<128, 64, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
+  return r.groups == 1
+             ? tile_w<128, 128, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
+             : tile_w<128, 128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
 }
 
 // Workgroups of 256 threads that one launch holds (2^32 threads).
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
 
-// Microseconds of a k-step on a CU with n tiles of 64, 128 or 256: kA + kB n
+// A form's output tile, and the microseconds that a CU with n such tiles
+// takes: a + b n for a k-step of all of them, c n for what no k-step covers
 // (see plan).
-constexpr double kA[3] = {0.15, 0.08, 0.0}, kB[3] = {0.16, 0.43, 1.3};
+struct TileCost {
+  int height, width;
+  double a, b, c;
+};
+constexpr TileCost kTiles[] = {{64, 64, 0.15, 0.16, 0.6},
+                               {128, 64, 0.05, 0.31, 1.25},
+                               {128, 128, 0.08, 0.43, 2.5},
+                               {256, 256, 0.0, 1.3, 6.0}};
 
 // Microseconds of moving the operands and the result of a product once.
 double move_us(int64_t M, int64_t N, int64_t K) {
@@ -772,38 +788,48 @@ double planes_us(int64_t splits, int64_t M, int64_t N) {
 // width-256 tile (128 where a tile holds gate and up).  split: the reduction
 // may be cut over workgroups (row outputs, through fp32 planes).
 //
-// A CU with n tiles of a width takes a + b n microseconds for a k-step of
-// all of them, measured on MI355X over T = 65..4096, d = 2048 and 4096, f =
-// 1408..14336: (0.15, 0.16) at 64, (0.08, 0.43) at 128, (0, 1.3) at 256 --
-// per output the wide tile costs half of the narrow one, but 88 tiles of
-// 256 leave two thirds of the CUs idle (dS of 2000 x 2816 over 2048: 43,
-// 38 and 49 us).  Two groups act as twice the tiles for half the steps (45
-// to 128-wide tiles: 23.7 -> 20.2 us).  Cutting the reduction adds a pass
-// over the planes at about 4 TB/s and a launch; it pays where few tiles
-// meet a long reduction (128 x 4096 over 14336: 70 -> 47 us) and costs
-// where the tiles fill the CUs (2000 x 2048 over 2816: 27 -> 37 us).
+// A CU with n tiles of a form takes a + b n microseconds for a k-step of all
+// of them, and c n to fill the pipeline and to write the results (about 3.4
+// TB/s, hardly overlapped); n lies between the mean and the fullest CU's
+// tiles.  kTiles holds the values measured on MI355X over T = 65..4096, d =
+// 2048 and 4096, f = 1408..14336.  Per output the 128-wide tile costs half
+// of the 64-wide one, but 88 tiles of 256 leave two thirds of the CUs idle
+// (dS of 2000 x 2816 over 2048: 43, 38 and 49 us at 64, 128 and 256).  128 x
+// 64 stands between where its tiles just fill the CUs: 777 x 2048 over 2816,
+// of 416, 224 and 112 tiles, 21.4, 18.8 and 22.9 us; 128 x 14336 over 4096
+// 44, 36 and 44 us (64 x 128 is within 3% of it).  Two groups act as twice
+// the tiles for half the steps (45 128-wide tiles: 23.7 -> 20.2 us).
+// Cutting the reduction adds a pass over the planes at about 4 TB/s and a
+// launch; it pays where few tiles meet a long reduction (128 x 4096 over
+// 14336: 70 -> 47 us) and costs where the tiles fill the CUs (2000 x 2048
+// over 2816: 27 -> 37 us).
 Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
           bool allow256 = true) {
   const int64_t steps = (K + kBK - 1) / kBK;
   const double least = move_us(M, N * (256 / cols), K);
   Plan best{};
   double best_us = 1e30;
-  for (int wi = 0; wi < (allow256 ? 3 : 2); ++wi) {
-    const int64_t w = int64_t{64} << wi, c = cols * w / 256;
-    const int64_t tiles = ((M + w - 1) / w) * ((N + c - 1) / c);
-    for (int64_t sp = 1; sp <= (split && wi < 2 ? 8 : 1); sp *= 2) {
+  for (const TileCost& t : kTiles) {
+    const bool large = t.width == 256;
+    if (large && !allow256) break;
+    const int64_t h = t.height, c = cols * t.width / 256;
+    const int64_t tiles = ((M + h - 1) / h) * ((N + c - 1) / c);
+    for (int64_t sp = 1; sp <= (split && !large ? 8 : 1); sp *= 2) {
       if (sp > 1 && sp * 4 > steps) break;       // at least 4 steps a split
       if (tiles * sp > kMaxGroups / 2) break;
       const int64_t per = (steps + sp - 1) / sp;
-      const double n = static_cast<double>((tiles * sp + 255) / 256);
+      const int64_t full = (tiles * sp + 255) / 256;
+      const double n = full == 1 ? 1.0
+                                 : 0.5 * static_cast<double>(full) +
+                                       static_cast<double>(tiles * sp) / 512;
       for (int g = 1; g <= 2; ++g) {
-        if (g == 2 && (wi == 2 || n > 1)) break;
-        double us = (kA[wi] + kB[wi] * g * n) *
-                        static_cast<double>((per + g - 1) / g) + 3 + g +
-                    planes_us(sp, M, N);
+        if (g == 2 && (large || full > 1)) break;
+        double us = (t.a + t.b * g * n) *
+                        static_cast<double>((per + g - 1) / g) +
+                    t.c * n + 1 + g + planes_us(sp, M, N);
         if (us < best_us) {
           best_us = us;
-          best = Plan{static_cast<int>(w), g,
+          best = Plan{t.height, t.width, g,
                       static_cast<int>((steps + per - 1) / per),
                       static_cast<int>(per * kBK), us};
         }
@@ -817,19 +843,21 @@ Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
 // The same for a row product a (M x Na over Ka; split: its reduction may be
 // cut) and a weight gradient b (Mb x Nb over M rows) in one launch of
 // `width`-wide tiles, which fill the CUs together: all k-steps at the full
-// CU's rate, and half of the longest tile for the ragged end.  Width 0: not
-// better than the two launches, which take `apart`; also where the pair
-// would be bound by memory, since interleaving two such streams costs more
-// than a launch.  (Backward of 64 x 2048 x 1408: 37 us apart, 31 us in
-// pairs; of 2000 x 2048 x 1408: 104 and 97 us; of 64 x 4096 x 14336, bound
-// by memory: 209 and 233 us.)
+// CU's rate, half of the longest tile for the ragged end, and a quarter of
+// the writes (the rest overlaps other tiles' k-steps).  Width 0: not better
+// than the two launches, which take `apart`; also where the pair would be
+// bound by memory (within a quarter of it), since interleaving two such
+// streams costs more than a launch.  (Backward of 64 x 2048 x 1408: 37 us
+// apart, 31 us in pairs; of 2000 x 2048 x 1408: 104 and 97 us; of 64 x 4096
+// x 14336, bound by memory: 209 and 233 us.)
 Plan pair_plan(int64_t M, int64_t Na, int64_t Ka, bool split, int64_t Mb,
                int64_t Nb, double apart) {
   const double least = move_us(M, Na, Ka) + move_us(Mb, Nb, M);
-  Plan best{0, 1, 1, 0, apart};
+  Plan best{0, 0, 1, 1, 0, apart};
   const int64_t sa = (Ka + kBK - 1) / kBK, sb = (M + kBK - 1) / kBK;
-  for (int wi = 0; wi < 2; ++wi) {
-    const int64_t w = int64_t{64} << wi;
+  for (const TileCost& t : kTiles) {
+    if (t.width != t.height || t.width == 256) continue;
+    const int64_t w = t.width;
     const double ta = static_cast<double>((M + w - 1) / w) *
                       static_cast<double>((Na + w - 1) / w);
     const double tb = static_cast<double>((Mb + w - 1) / w) *
@@ -839,13 +867,14 @@ Plan pair_plan(int64_t M, int64_t Na, int64_t Ka, bool split, int64_t Mb,
       if (ta * static_cast<double>(sp) + tb > kMaxGroups) break;
       const int64_t per = (sa + sp - 1) / sp;
       const double work = (ta * static_cast<double>(sa) +
-                           tb * static_cast<double>(sb)) * kB[wi] / 256;
+                           tb * static_cast<double>(sb)) * t.b / 256;
       const double one = static_cast<double>(per > sb ? per : sb) *
-                         (kA[wi] + kB[wi]);
-      const double us = (work > one ? work : one) + 0.5 * one + 4 +
+                         (t.a + t.b);
+      const double us = (work > one ? work : one) + 0.5 * one + 2 +
+                        t.c * (ta * static_cast<double>(sp) + tb) / 1024 +
                         planes_us(sp, M, Na);
-      if (us > least && us < best.us)
-        best = Plan{static_cast<int>(w), 1,
+      if (us > 1.25 * least && us < best.us)
+        best = Plan{static_cast<int>(w), static_cast<int>(w), 1,
                     static_cast<int>((sa + per - 1) / per),
                     static_cast<int>(per * kBK), us};
     }

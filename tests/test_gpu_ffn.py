@@ -430,3 +430,16 @@ def test_ffn_past_32_bit_offsets():
     _close("dw_gu", dwg, rwg)
     _close("dw2", dw2, rw2)
     g.check()
+
+
+# the 128 x 64 tiles: fc1 with one group a tile; y over a split reduction;
+# [dA dU]; dx; dw2; y and [dA dU] with two groups
+TALL = [(137, 264, 3720), (65, 1160, 3208), (2420, 264, 520),
+        (2420, 520, 136), (65, 4232, 392), (326, 3720, 4232)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T,d,f", TALL)
+def test_ffn_tall_tiles(T, d, f, act):
+    test_ffn_parity(T, d, f, act)
