@@ -475,6 +475,7 @@ class MoEBlock:
         if f_shared:
             self.ab, self.s = z(T, 2 * f_shared), z(T, f_shared)
             self.ws_ffn = self._ws(MOE_ENTRY_FFN_FWD, f_shared)
+        self._x = None
         self._bwd_ready = False
 
     def _ws(self, entry, f):
@@ -510,6 +511,9 @@ class MoEBlock:
             raise ValueError("dropout (p > 0) needs rng")
         if self.f_shared and (sw_gu is None or sw2 is None):
             raise ValueError("f_shared > 0 needs sw_gu and sw2")
+        if x.data_ptr() == self.path.y.data_ptr():
+            raise ValueError("x is the path's y, which this call replaces "
+                             "before it adds x")
         with _around(timers, "norm_fwd"):
             moe.moe_norm_fwd(self.norm, x, gamma, beta, self.eps, self.n,
                              self.mean, self.rstd)
@@ -520,7 +524,8 @@ class MoEBlock:
                 moe.moe_ffn_fwd(self.act, self.n, sw_gu, sw2, z, self.ab,
                                 self.s, z, self.ws_ffn)
         self._drop = (p, self._no_rng if rng is None else rng, delta)
-        self._x = x
+        # x may be the last call's y, which this call's y then replaces
+        self._x = None if x.data_ptr() == self.y.data_ptr() else x
         with _around(timers, "dropout_fwd"):
             moe.moe_dropout(z, x, *self._drop, self.y)
         return self.y
@@ -528,7 +533,12 @@ class MoEBlock:
     def backward(self, dy, gamma, w_gu, w2, sw_gu=None, sw2=None,
                  timers=None):
         """dx; the weights' gradients are left in dgamma, dbeta, dsw_gu and
-        dsw2, and in the path (dw_gu, dw2, and the router's)."""
+        dsw2, and in the path (dw_gu, dw2, and the router's).  It reads the
+        forward's x again, so that must be as it was and not the block's own
+        y."""
+        if self._x is None:
+            raise ValueError("backward needs a forward whose x was not this "
+                             "block's y")
         if not self._bwd_ready:
             self._alloc_bwd()
         with _around(timers, "dropout_bwd"):

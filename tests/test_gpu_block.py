@@ -284,3 +284,36 @@ def test_calls_at_the_same_time_on_two_streams():
     torch.cuda.synchronize()
     for b, ref in zip(sets, refs):
         assert all(torch.equal(b[n], r) for n, r in zip(outs, ref))
+
+
+@gpu
+def test_block_on_its_own_output():
+    """x may be the block's last y: the forward is that of a copy; the
+    backward, whose x is gone, is refused, as is one without a forward, and
+    an x in the path's own output."""
+    dev = torch.device("cuda:0")
+    path = MoEPath(33, 64, 64, 4, 2, device=dev)
+    D = _inputs(33, 64, 64, 4, 64, BF, 1, True)
+    blk = MoEBlock(path, f_shared=64)
+
+    def fwd(x):
+        return blk.forward(x, D["gamma"], D["w_gu"], D["w2"], w_g=D["w_g"],
+                           sw_gu=D["sw_gu"], sw2=D["sw2"], p=0.25,
+                           rng=D["rng"])
+
+    def bwd():
+        return blk.backward(D["dy"], D["gamma"], D["w_gu"], D["w2"],
+                            sw_gu=D["sw_gu"], sw2=D["sw2"])
+    with pytest.raises(ValueError, match="forward"):
+        bwd()
+    once = fwd(D["x"]).clone()
+    twice = fwd(once).clone()
+    bwd()
+    assert torch.equal(fwd(D["x"]), once)
+    assert torch.equal(fwd(blk.y), twice)
+    with pytest.raises(ValueError, match="this block's y"):
+        bwd()
+    with pytest.raises(ValueError, match="path's y"):
+        fwd(path.y)
+    fwd(D["x"])
+    bwd()
