@@ -438,6 +438,27 @@ class MoEPathMX(MoEPath):
         return self.dx, self.dw_gu, self.dw2, self.dp
 
 
+def _extent(t):
+    """First byte of a contiguous tensor and the byte past its last."""
+    lo = t.data_ptr()
+    return lo, lo + t.numel() * t.element_size()
+
+
+def _buffers(owner, label, but=()):
+    """(name, first byte, end) of the tensors that owner allocated for its
+    calls; names with an underscore hold a caller's."""
+    return [(f"{label} {n}", *_extent(t)) for n, t in vars(owner).items()
+            if isinstance(t, torch.Tensor) and n[0] != "_" and n not in but]
+
+
+def _refuse_overlap(name, t, buffers):
+    lo, hi = _extent(t)
+    for n, b, e in buffers:
+        if lo < e and b < hi:
+            raise ValueError(f"{name} overlaps {n}, which the block replaces "
+                             f"before it has read {name} for the last time")
+
+
 class MoEBlock:
     """Pre-norm residual block around an expert layer (a ``MoEPath`` or
     ``MoEPathMX`` with bf16 output):
@@ -475,6 +496,9 @@ class MoEBlock:
         if f_shared:
             self.ab, self.s = z(T, 2 * f_shared), z(T, f_shared)
             self.ws_ffn = self._ws(MOE_ENTRY_FFN_FWD, f_shared)
+        # what a forward replaces; dx is a backward's alone
+        self._fwd_bufs = (_buffers(path, "the path's", ("dx",)) +
+                          _buffers(self, "the block's", ("y",)))
         self._x = None
         self._bwd_ready = False
 
@@ -497,6 +521,12 @@ class MoEBlock:
         if f:
             self.dsw_gu, self.dsw2 = z(2 * f, d), z(d, f)
             self.ws_ffn_bwd = self._ws(MOE_ENTRY_FFN_BWD, f)
+        if not self.path._bwd_ready:
+            self.path._alloc_bwd()
+        # what stands between a backward's two reads of dy, and of x
+        self._bwd_bufs = (_buffers(self.path, "the path's", ("y",)) +
+                          _buffers(self, "the block's", ("y", "dx")))
+        self._dx_buf = [("the block's dx", *_extent(self.dx))]
         self._bwd_ready = True
 
     def forward(self, x, gamma, w_gu, w2, beta=None, w_g=None, bias=None,
@@ -511,9 +541,7 @@ class MoEBlock:
             raise ValueError("dropout (p > 0) needs rng")
         if self.f_shared and (sw_gu is None or sw2 is None):
             raise ValueError("f_shared > 0 needs sw_gu and sw2")
-        if x.data_ptr() == self.path.y.data_ptr():
-            raise ValueError("x is the path's y, which this call replaces "
-                             "before it adds x")
+        _refuse_overlap("x", x, self._fwd_bufs)
         with _around(timers, "norm_fwd"):
             moe.moe_norm_fwd(self.norm, x, gamma, beta, self.eps, self.n,
                              self.mean, self.rstd)
@@ -541,6 +569,8 @@ class MoEBlock:
                              "block's y")
         if not self._bwd_ready:
             self._alloc_bwd()
+        _refuse_overlap("dy", dy, self._bwd_bufs)
+        _refuse_overlap("x", self._x, self._bwd_bufs + self._dx_buf)
         with _around(timers, "dropout_bwd"):
             moe.moe_dropout(dy, None, *self._drop, self.dz)
         dn = self.path.backward(self.dz, w_gu, w2, timers=timers)[0]
