@@ -542,6 +542,7 @@ class MoEBlock:
         if self.f_shared and (sw_gu is None or sw2 is None):
             raise ValueError("f_shared > 0 needs sw_gu and sw2")
         _refuse_overlap("x", x, self._fwd_bufs)
+        self._x = None      # until every call below has been made
         with _around(timers, "norm_fwd"):
             moe.moe_norm_fwd(self.norm, x, gamma, beta, self.eps, self.n,
                              self.mean, self.rstd)
@@ -552,10 +553,11 @@ class MoEBlock:
                 moe.moe_ffn_fwd(self.act, self.n, sw_gu, sw2, z, self.ab,
                                 self.s, z, self.ws_ffn)
         self._drop = (p, self._no_rng if rng is None else rng, delta)
-        # x may be the last call's y, which this call's y then replaces
-        self._x = None if x.data_ptr() == self.y.data_ptr() else x
         with _around(timers, "dropout_fwd"):
             moe.moe_dropout(z, x, *self._drop, self.y)
+        # x may be the last call's y, which this call's y has replaced
+        if x.data_ptr() != self.y.data_ptr():
+            self._x = x
         return self.y
 
     def backward(self, dy, gamma, w_gu, w2, sw_gu=None, sw2=None,
@@ -565,8 +567,8 @@ class MoEBlock:
         forward's x again, so that must be as it was and not the block's own
         y."""
         if self._x is None:
-            raise ValueError("backward needs a forward whose x was not this "
-                             "block's y")
+            raise ValueError("backward needs a forward that has ended and "
+                             "whose x was not this block's y")
         if not self._bwd_ready:
             self._alloc_bwd()
         _refuse_overlap("dy", dy, self._bwd_bufs)

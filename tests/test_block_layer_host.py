@@ -107,3 +107,34 @@ def test_dy_in_the_blocks_results_is_taken(calls):
     blk = _block(stream_fp32=True, f_shared=0)
     _fwd(blk, _rows(blk))
     assert _bwd(blk, _rows(blk)) is blk.dx
+
+
+@pytest.mark.parametrize("at", ["moe_permute", "moe_ffn_fwd", "moe_dropout"])
+def test_no_backward_after_a_forward_that_failed(calls, monkeypatch, at):
+    """A forward that ends half way has replaced n and the norm's statistics:
+    the backward of the forward before it is gone too."""
+    blk = _block()
+    _fwd(blk, _rows(blk))
+
+    def fail(*a, **k):
+        raise moe.MoeError(at, 1, "MOE_ERR_INVALID_ARG", "refused")
+
+    with monkeypatch.context() as m:
+        m.setattr(moe, at, fail)
+        with pytest.raises(moe.MoeError):
+            _fwd(blk, _rows(blk))
+    with pytest.raises(ValueError, match="backward needs a forward"):
+        _bwd(blk, _rows(blk))
+    _fwd(blk, _rows(blk))
+    _bwd(blk, _rows(blk))
+
+
+def test_a_refused_forward_leaves_the_one_before(calls):
+    blk = _block()
+    _fwd(blk, _rows(blk))
+    for kw in (dict(p=0.5), dict(sw2=None)):
+        with pytest.raises(ValueError):
+            _fwd(blk, _rows(blk), **kw)
+    with pytest.raises(ValueError):
+        _fwd(blk, blk.path.y)
+    _bwd(blk, _rows(blk))
