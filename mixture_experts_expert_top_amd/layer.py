@@ -83,6 +83,7 @@ class MoEPath:
         self.renorm = renorm
         self.aux_coef = aux_coef
         self._router = None
+        self._forwards = 0      # tells whose forward the buffers hold
         self.prec = prec
         Tk = T * k
         dev = torch.device(device)
@@ -137,6 +138,7 @@ class MoEPath:
 
     # ------------------------------------------------------------------
     def route(self, x=None, w_g=None, bias=None, logits=None, timers=None):
+        self._forwards += 1
         if logits is None:
             with _around(timers, "router_logits"):
                 moe.moe_router_logits(x, w_g, bias, self.logits)
@@ -558,6 +560,7 @@ class MoEBlock:
         # x may be the last call's y, which this call's y has replaced
         if x.data_ptr() != self.y.data_ptr():
             self._x = x
+        self._path_forward = self.path._forwards
         return self.y
 
     def backward(self, dy, gamma, w_gu, w2, sw_gu=None, sw2=None,
@@ -569,6 +572,9 @@ class MoEBlock:
         if self._x is None:
             raise ValueError("backward needs a forward that has ended and "
                              "whose x was not this block's y")
+        if self.path._forwards != self._path_forward:
+            raise ValueError("the path has run another forward since this "
+                             "block's")
         if not self._bwd_ready:
             self._alloc_bwd()
         _refuse_overlap("dy", dy, self._bwd_bufs)

@@ -138,3 +138,28 @@ def test_a_refused_forward_leaves_the_one_before(calls):
     with pytest.raises(ValueError):
         _fwd(blk, blk.path.y)
     _bwd(blk, _rows(blk))
+
+
+def test_no_backward_after_the_path_ran_for_another(calls):
+    """The path keeps one forward: two blocks around one path, or a call of
+    the path itself, replace what the first block's backward would read."""
+    blk = _block()
+    other = layer.MoEBlock(blk.path)
+    _fwd(blk, _rows(blk))
+    _fwd(other, _rows(blk))
+    calls.clear()
+    with pytest.raises(ValueError, match="another forward"):
+        _bwd(blk, _rows(blk))
+    assert calls == []
+    _bwd(other, _rows(blk))
+    w = _weights(blk)
+    x = torch.zeros(T, D, dtype=BF)
+    for use in (lambda: blk.path.forward(x, w["w_gu"], w["w2"], w_g=x[:E]),
+                lambda: blk.path.route(x, x[:E])):
+        _fwd(blk, _rows(blk))
+        use()
+        with pytest.raises(ValueError, match="another forward"):
+            _bwd(blk, _rows(blk))
+    _fwd(blk, _rows(blk))
+    _bwd(blk, _rows(blk))
+    _bwd(blk, _rows(blk))
