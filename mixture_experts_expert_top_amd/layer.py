@@ -35,6 +35,7 @@ No arithmetic happens here: every step runs in the library's kernels.
 """
 
 import contextlib
+import functools
 
 import torch
 
@@ -461,6 +462,17 @@ def _refuse_overlap(name, t, buffers):
                              f"before it has read {name} for the last time")
 
 
+def _on_its_device(call):
+    """Runs a block's call with its path's device as the current one: the
+    path's entries launch on the current device's stream, those around it on
+    their tensors', and the two have to be one stream."""
+    @functools.wraps(call)
+    def run(self, *args, **kw):
+        with torch.cuda.device(self.path.y.device):
+            return call(self, *args, **kw)
+    return run
+
+
 class MoEBlock:
     """Pre-norm residual block around an expert layer (a ``MoEPath`` or
     ``MoEPathMX`` with bf16 output):
@@ -531,6 +543,7 @@ class MoEBlock:
         self._dx_buf = [("the block's dx", *_extent(self.dx))]
         self._bwd_ready = True
 
+    @_on_its_device
     def forward(self, x, gamma, w_gu, w2, beta=None, w_g=None, bias=None,
                 logits=None, sw_gu=None, sw2=None, p=0.0, rng=None, delta=0,
                 timers=None):
@@ -563,6 +576,7 @@ class MoEBlock:
         self._path_forward = self.path._forwards
         return self.y
 
+    @_on_its_device
     def backward(self, dy, gamma, w_gu, w2, sw_gu=None, sw2=None,
                  timers=None):
         """dx; the weights' gradients are left in dgamma, dbeta, dsw_gu and

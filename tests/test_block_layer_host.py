@@ -163,3 +163,28 @@ def test_no_backward_after_the_path_ran_for_another(calls):
     _fwd(blk, _rows(blk))
     _bwd(blk, _rows(blk))
     _bwd(blk, _rows(blk))
+
+
+def test_calls_run_on_the_paths_device(calls, monkeypatch):
+    """The path's calls take the current device's stream, the others their
+    tensors' device: both are the path's device while the block runs."""
+    on = []
+
+    @contextlib.contextmanager
+    def device(d):
+        on.append(d)
+        yield
+        on.pop()
+
+    where = {}
+    for name in LAUNCHES:
+        monkeypatch.setattr(moe, name, lambda *a, _n=name, **k:
+                            where.setdefault(_n, list(on)))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    blk = _block()
+    _fwd(blk, _rows(blk))
+    _bwd(blk, _rows(blk))
+    assert {"moe_norm_fwd", "moe_permute", "moe_grouped_mlp_bwd",
+            "moe_ffn_bwd", "moe_norm_bwd"} <= set(where)
+    assert all(w == [torch.device("cpu")] for w in where.values()), where
+    assert on == []
