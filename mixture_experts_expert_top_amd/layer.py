@@ -482,7 +482,11 @@ class MoEBlock:
     f_shared > 0 adds the dense feed-forward block (the "shared expert") of
     that width.  x, y and their gradients are the residual stream, bf16 or
     (stream_fp32) fp32.  The buffers belong to the block and the path; y, dx
-    and the gradients are overwritten by the next call.
+    and the gradients are overwritten by the next call, and a backward is
+    that of the path's last forward.  x and dy are read twice, first and
+    last, so neither may lie in a buffer of the block or the path, but for
+    the block's own results: a forward takes its y (and then has no
+    backward), a backward its y or its dx as dy.
 
     forward:  moe_norm_fwd -> the path's calls -> moe_ffn_fwd (into the
               path's y) -> moe_dropout
@@ -586,6 +590,8 @@ class MoEBlock:
         if self._x is None:
             raise ValueError("backward needs a forward that has ended and "
                              "whose x was not this block's y")
+        if self.f_shared and (sw_gu is None or sw2 is None):
+            raise ValueError("f_shared > 0 needs sw_gu and sw2")
         if self.path._forwards != self._path_forward:
             raise ValueError("the path has run another forward since this "
                              "block's")

@@ -188,3 +188,14 @@ def test_calls_run_on_the_paths_device(calls, monkeypatch):
             "moe_ffn_bwd", "moe_norm_bwd"} <= set(where)
     assert all(w == [torch.device("cpu")] for w in where.values()), where
     assert on == []
+
+
+@pytest.mark.parametrize("missing", ["sw_gu", "sw2"])
+def test_backward_needs_the_feed_forward_weights(calls, missing):
+    """Refused before the path's backward has run, as in the forward."""
+    blk = _block()
+    _fwd(blk, _rows(blk))
+    calls.clear()
+    with pytest.raises(ValueError, match="sw_gu and sw2"):
+        _bwd(blk, _rows(blk), **{missing: None})
+    assert calls == []
