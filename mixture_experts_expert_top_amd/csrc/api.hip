@@ -419,7 +419,7 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
     case MOE_ENTRY_ROUTER_BWD:
       return moe::router_backward_workspace(T, E, d < 1 ? 1 : d);
     case MOE_ENTRY_NORM_BWD:
-      if (d < 8 || d > moe::kMaxNormWidth) return 0;
+      if (d < 8 || d % 8 || d > moe::kMaxNormWidth) return 0;
       return moe::norm_bwd_workspace(T, d);
     case MOE_ENTRY_FFN_FWD:
     case MOE_ENTRY_FFN_BWD:

@@ -1,0 +1,17 @@
+"""Further argument checks of the norm and feed-forward entries that need no
+GPU (fake device pointers; every call is refused before a launch)."""
+
+import pytest
+import torch
+
+from mixture_experts_expert_top_amd import moe
+
+L = moe.lib
+
+
+@pytest.mark.parametrize("d", [9, 12, 20, 4100, 16380])
+def test_norm_workspace_of_a_refused_width_is_0(d):
+    """The width's own call is refused, so it has no workspace either."""
+    assert L.moe_workspace_bytes(moe.MOE_ENTRY_NORM_BWD, 0, 4, 1, 1, d, 0) == 0
+    assert L.moe_workspace_bytes(moe.MOE_ENTRY_NORM_BWD, 0, 4, 1, 1,
+                                 d // 8 * 8, 0) > 0
