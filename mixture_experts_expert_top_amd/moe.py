@@ -735,6 +735,10 @@ def _stream_dtype(t, name):
     return t.dtype
 
 
+def _dtype(t):
+    return None if t is None else t.dtype
+
+
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -765,8 +769,7 @@ def moe_norm_bwd(kind, dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta,
         ("rstd", rstd, _F32, (T,)), ("dres", dres, xt, (T, d)),
         ("dx", dx, xt, (T, d)), ("dgamma", dgamma, _F32, (d,)),
         ("dbeta", dbeta, _F32, (d,)),
-        ("workspace", workspace, workspace.dtype if workspace is not None
-         else None, None)))
+        ("workspace", workspace, _dtype(workspace), None)))
     _enqueue("moe_norm_bwd", stream, dev, lib.moe_norm_bwd, kind, p[0], p[1],
              xt is _F32, p[2], p[3], p[4], p[5], T, d, p[6], p[7], p[8],
              p[9], _nbytes(workspace))
@@ -798,7 +801,7 @@ def moe_ffn_fwd(act, x, w_gu, w2, y_add, ab_saved, s_saved, y, workspace,
         ("w2", w2, _BF16, (d, f)), ("y_add", y_add, _BF16, (T, d)),
         ("ab_saved", ab_saved, _BF16, (T, 2 * f)),
         ("s_saved", s_saved, _BF16, (T, f)), ("y", y, _BF16, (T, d)),
-        ("workspace", workspace, workspace.dtype, None)))
+        ("workspace", workspace, _dtype(workspace), None)))
     _enqueue("moe_ffn_fwd", stream, dev, lib.moe_ffn_fwd, act, p[0], p[1],
              p[2], p[3], T, d, f, p[4], p[5], p[6], p[7], _nbytes(workspace))
 
@@ -816,7 +819,7 @@ def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
         ("s_saved", s_saved, _BF16, (T, f)),
         ("dx_add", dx_add, _BF16, (T, d)), ("dx", dx, _BF16, (T, d)),
         ("dw_gu", dw_gu, _BF16, (2 * f, d)), ("dw2", dw2, _BF16, (d, f)),
-        ("workspace", workspace, workspace.dtype, None)))
+        ("workspace", workspace, _dtype(workspace), None)))
     _enqueue("moe_ffn_bwd", stream, dev, lib.moe_ffn_bwd, act, p[0], p[1],
              p[2], p[3], p[4], p[5], p[6], T, d, f, p[7], p[8],
              p[9], p[10], _nbytes(workspace))
