@@ -22,6 +22,7 @@
 // 8192 through 4096 x 14336 6.8 to 7.0 ms (1240 to 1280 TFLOP/s).
 
 #include "common.cuh"
+#include "ffn_plan.h"
 #include "internal.h"
 
 namespace moe {
@@ -55,7 +56,6 @@ struct TileParams {
   float* Cf;           // kPlane: [split][M][N]
 };
 
-constexpr int kBK = 64;
 // tiles in flight from global memory, in 128 x 128 and in smaller tiles
 constexpr int kDepthWide = 2;
 constexpr int kDepthNarrow = 4;
@@ -699,23 +699,19 @@ hipError_t thin_rt(const ThinParams& P, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tokens whose fragments are loaded straight from x (see above).
-constexpr int kDirectTokens = 4;
-
 template <int EPI, int ACT>
 hipError_t thin(const ThinParams& P, hipStream_t s) {
-  const int ntb = (P.T + 15) / 16;
-  const bool narrow = P.N < 16 * 256;
-  if (P.T <= kDirectTokens)
+  const ThinPlan r = thin_plan(P.T, P.N);
+  const bool narrow = r.rows == 8;
+  if (!r.staged)
     return narrow ? thin_rt<1, false, 8, EPI, ACT>(P, s)
                   : thin_rt<1, false, 16, EPI, ACT>(P, s);
-  if (ntb == 1)
+  if (r.blocks == 1)
     return narrow ? thin_rt<1, true, 8, EPI, ACT>(P, s)
                   : thin_rt<1, true, 16, EPI, ACT>(P, s);
-  if (ntb == 2)
+  if (r.blocks == 2)
     return narrow ? thin_rt<2, true, 8, EPI, ACT>(P, s)
                   : thin_rt<2, true, 16, EPI, ACT>(P, s);
-  // four token blocks leave no registers for a second weight tile
   return thin_rt<4, true, 8, EPI, ACT>(P, s);
 }
 
@@ -731,14 +727,6 @@ hipError_t tile_w(TileParams P, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The form of one product: output tiles of `height` x `width` (256 x 256 for
-// the grouped GEMM's kernel), `groups` of 256 threads a tile, the reduction in
-// `splits` ranges of kchunk.
-struct Plan {
-  int height, width, groups, splits, kchunk;
-  double us;           // estimated time
-};
-
 template <bool AKC, bool BKC, int EPI, int ACT>
 hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
   P.kchunk = r.kchunk;
@@ -753,133 +741,6 @@ hipError_t tile(TileParams P, const Plan& r, hipStream_t s) {
   return r.groups == 1
              ? tile_w<128, 128, 1, AKC, BKC, EPI, ACT>(P, r.splits, s)
              : tile_w<128, 128, 2, AKC, BKC, EPI, ACT>(P, r.splits, s);
-}
-
-// Workgroups of 256 threads that one launch holds (2^32 threads).
-constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
-
-// A form's output tile, and the microseconds that a CU with n such tiles
-// takes: a + b n for a k-step of all of them, c n for what no k-step covers
-// (see plan).
-struct TileCost {
-  int height, width;
-  double a, b, c;
-};
-constexpr TileCost kTiles[] = {{64, 64, 0.15, 0.16, 0.6},
-                               {128, 64, 0.05, 0.31, 1.25},
-                               {128, 128, 0.08, 0.43, 2.5},
-                               {256, 256, 0.0, 1.3, 6.0}};
-
-// Microseconds of moving the operands and the result of a product once.
-double move_us(int64_t M, int64_t N, int64_t K) {
-  const double m = static_cast<double>(M), n = static_cast<double>(N),
-               k = static_cast<double>(K);
-  return 2 * (m * k + n * k + m * n) / 4.5e6;
-}
-
-// Microseconds of summing `splits` fp32 planes of M x N.
-double planes_us(int64_t splits, int64_t M, int64_t N) {
-  return splits < 2 ? 0.0
-                    : 4 + static_cast<double>(splits * M) *
-                              static_cast<double>(N) * 8 / 4e6;
-}
-
-// The form with the least estimated time.  cols: output columns of a
-// width-256 tile (128 where a tile holds gate and up).  split: the reduction
-// may be cut over workgroups (row outputs, through fp32 planes).
-//
-// A CU with n tiles of a form takes a + b n microseconds for a k-step of all
-// of them, and c n to fill the pipeline and to write the results (about 3.4
-// TB/s, hardly overlapped); n lies between the mean and the fullest CU's
-// tiles.  kTiles holds the values measured on MI355X over T = 65..4096, d =
-// 2048 and 4096, f = 1408..14336.  Per output the 128-wide tile costs half
-// of the 64-wide one, but 88 tiles of 256 leave two thirds of the CUs idle
-// (dS of 2000 x 2816 over 2048: 43, 38 and 49 us at 64, 128 and 256).  128 x
-// 64 stands between where its tiles just fill the CUs: 777 x 2048 over 2816,
-// of 416, 224 and 112 tiles, 21.4, 18.8 and 22.9 us; 128 x 14336 over 4096
-// 44, 36 and 44 us (64 x 128 is within 3% of it).  Two groups act as twice
-// the tiles for half the steps (45 128-wide tiles: 23.7 -> 20.2 us).
-// Cutting the reduction adds a pass over the planes at about 4 TB/s and a
-// launch; it pays where few tiles meet a long reduction (128 x 4096 over
-// 14336: 70 -> 47 us) and costs where the tiles fill the CUs (2000 x 2048
-// over 2816: 27 -> 37 us).
-Plan plan(int64_t M, int64_t N, int64_t K, int64_t cols, bool split,
-          bool allow256 = true) {
-  const int64_t steps = (K + kBK - 1) / kBK;
-  const double least = move_us(M, N * (256 / cols), K);
-  Plan best{};
-  double best_us = 1e30;
-  for (const TileCost& t : kTiles) {
-    const bool large = t.width == 256;
-    if (large && !allow256) break;
-    const int64_t h = t.height, c = cols * t.width / 256;
-    const int64_t tiles = ((M + h - 1) / h) * ((N + c - 1) / c);
-    for (int64_t sp = 1; sp <= (split && !large ? 8 : 1); sp *= 2) {
-      if (sp > 1 && sp * 4 > steps) break;       // at least 4 steps a split
-      if (tiles * sp > kMaxGroups / 2) break;
-      const int64_t per = (steps + sp - 1) / sp;
-      const int64_t full = (tiles * sp + 255) / 256;
-      const double n = full == 1 ? 1.0
-                                 : 0.5 * static_cast<double>(full) +
-                                       static_cast<double>(tiles * sp) / 512;
-      for (int g = 1; g <= 2; ++g) {
-        if (g == 2 && (large || full > 1)) break;
-        double us = (t.a + t.b * g * n) *
-                        static_cast<double>((per + g - 1) / g) +
-                    t.c * n + 1 + g + planes_us(sp, M, N);
-        if (us < best_us) {
-          best_us = us;
-          best = Plan{t.height, t.width, g,
-                      static_cast<int>((steps + per - 1) / per),
-                      static_cast<int>(per * kBK), us};
-        }
-      }
-    }
-  }
-  if (best.us < least) best.us = least;
-  return best;
-}
-
-// The same for a row product a (M x Na over Ka; split: its reduction may be
-// cut) and a weight gradient b (Mb x Nb over M rows) in one launch of
-// `width`-wide tiles, which fill the CUs together: all k-steps at the full
-// CU's rate, half of the longest tile for the ragged end, and a quarter of
-// the writes (the rest overlaps other tiles' k-steps).  Width 0: not better
-// than the two launches, which take `apart`; also where the pair would be
-// bound by memory (within a quarter of it), since interleaving two such
-// streams costs more than a launch.  (Backward of 64 x 2048 x 1408: 37 us
-// apart, 31 us in pairs; of 2000 x 2048 x 1408: 104 and 97 us; of 64 x 4096
-// x 14336, bound by memory: 209 and 233 us.)
-Plan pair_plan(int64_t M, int64_t Na, int64_t Ka, bool split, int64_t Mb,
-               int64_t Nb, double apart) {
-  const double least = move_us(M, Na, Ka) + move_us(Mb, Nb, M);
-  Plan best{0, 0, 1, 1, 0, apart};
-  const int64_t sa = (Ka + kBK - 1) / kBK, sb = (M + kBK - 1) / kBK;
-  for (const TileCost& t : kTiles) {
-    if (t.width != t.height || t.width == 256) continue;
-    const int64_t w = t.width;
-    const double ta = static_cast<double>((M + w - 1) / w) *
-                      static_cast<double>((Na + w - 1) / w);
-    const double tb = static_cast<double>((Mb + w - 1) / w) *
-                      static_cast<double>((Nb + w - 1) / w);
-    for (int64_t sp = 1; sp <= (split ? 8 : 1); sp *= 2) {
-      if (sp > 1 && sp * 4 > sa) break;
-      if (ta * static_cast<double>(sp) + tb > kMaxGroups) break;
-      const int64_t per = (sa + sp - 1) / sp;
-      const double work = (ta * static_cast<double>(sa) +
-                           tb * static_cast<double>(sb)) * t.b / 256;
-      const double one = static_cast<double>(per > sb ? per : sb) *
-                         (t.a + t.b);
-      const double us = (work > one ? work : one) + 0.5 * one + 2 +
-                        t.c * (ta * static_cast<double>(sp) + tb) / 1024 +
-                        planes_us(sp, M, Na);
-      if (us > 1.25 * least && us < best.us)
-        best = Plan{static_cast<int>(w), static_cast<int>(w), 1,
-                    static_cast<int>((sa + per - 1) / per),
-                    static_cast<int>(per * kBK), us};
-    }
-  }
-  return best;
 }
 
 template <int W, int EPI, int ACT>
@@ -915,19 +776,6 @@ hipError_t finish_rows(const float* planes, int n_planes, int64_t n,
   return hipGetLastError();
 }
 
-// Whether the weight-streaming form runs.  Its time grows with the tokens
-// (every workgroup reads all of them), the tiles' hardly does up to 64, but
-// tiles of narrow blocks leave CUs idle.  Forward on MI355X, thin and tiles,
-// us: 16 tokens 10 and 18 (d 2048, f 1408), 15 and 21 (2048, 2816), 26 and
-// 35 (4096, 4096), 75 and 78 (4096, 14336); 24 tokens 12 and 19, 20 and 20,
-// 32 and 33, 97 and 76; 64 tokens 17 and 23, 31 and 23, 50 and 38, 159 and
-// 82.
-bool thin_form(int64_t T, int64_t d, int64_t f) {
-  const int64_t bytes = 6 * d * f;
-  return T <= 16 || (T <= 32 && bytes <= (int64_t{128} << 20)) ||
-         (T <= 64 && bytes <= (int64_t{24} << 20));
-}
-
 size_t up256(int64_t v) {
   return (static_cast<size_t>(v) + 255) & ~static_cast<size_t>(255);
 }
@@ -947,7 +795,7 @@ template <bool BKC>
 hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
                        int64_t T, int64_t N, int64_t K, const bf16_t* add,
                        bf16_t* out, float* planes, hipStream_t s) {
-  const Plan r = plan(T, N, K, 256, true);
+  const Plan r = row_plan(T, N, K);
   if (r.width == 256)
     return gemm_dense_rows(A, B, BKC, T, N, K, add, out, s);
   TileParams P = row_params(A, B, ldb, T, N, K);
@@ -962,11 +810,6 @@ hipError_t row_product(const bf16_t* A, const bf16_t* B, int64_t ldb,
 }
 
 // c[M][N] = sum_t a[t][m] b[t][n]
-Plan weight_plan(int64_t T, int64_t M, int64_t N) {
-  // the 256-wide kernel addresses an operand's rows with 32 bits
-  const bool fits = T * (M > N ? M : N) * 2 <= kMaxResourceBytes;
-  return plan(M, N, T, 256, false, fits);
-}
 TileParams weight_params(const bf16_t* a, const bf16_t* b, int64_t T,
                          int64_t M, int64_t N, bf16_t* c) {
   TileParams P{};
@@ -997,7 +840,7 @@ hipError_t fc1(const bf16_t* x, const bf16_t* w_gu, int64_t T, int64_t d,
     P.C = ab; P.S = s_out;
     return thin<kAct, ACT>(P, s);
   }
-  const Plan r = plan(T, f, d, 128, false);
+  const Plan r = fc1_plan(T, d, f);
   if (r.width == 256)
     return gemm_dense_fc1_fwd(x, w_gu, T, d, f, ACT, ab, s_out, s);
   TileParams P{};
@@ -1009,36 +852,25 @@ hipError_t fc1(const bf16_t* x, const bf16_t* w_gu, int64_t T, int64_t d,
   return tile<true, true, kAct, ACT>(P, r, s);
 }
 
-// A second launch costs about this much more than its kernel.
-constexpr double kLaunchUs = 2;
-
 // dAB, and dW2 unless it is null.
 template <int ACT>
 hipError_t dact_dw2(const bf16_t* dy, const bf16_t* w2, const bf16_t* ab,
                     const bf16_t* s_saved, int64_t T, int64_t d, int64_t f,
                     bf16_t* dab, bf16_t* dw2, hipStream_t s) {
-  const Plan r = plan(T, f, d, 256, false);
   TileParams P = row_params(dy, w2, f, T, f, d);
   P.C = dab; P.ldc = 2 * f; P.AB = ab;
   if (dw2) {
-    const double apart = r.us + weight_plan(T, d, f).us + kLaunchUs;
-    const Plan both = pair_plan(T, f, d, false, d, f, apart);
+    const Plan both = dact_pair(T, d, f);
     if (both.width)
       return pair<kDAct, ACT>(P, weight_params(dy, s_saved, T, d, f, dw2),
                               both, s);
     hipError_t e = weight_product(dy, s_saved, T, d, f, dw2, s);
     if (e != hipSuccess) return e;
   }
+  const Plan r = dact_plan(T, d, f);
   if (r.width == 256)
     return gemm_dense_fc2_dgrad(dy, w2, T, d, f, ACT, ab, dab, s);
   return tile<true, false, kDAct, ACT>(P, r, s);
-}
-
-// The launch of dx together with dW_gu (width 0: apart).
-Plan dx_pair(int64_t T, int64_t d, int64_t f) {
-  const double apart = plan(T, d, 2 * f, 256, true).us +
-                       weight_plan(T, 2 * f, d).us + kLaunchUs;
-  return pair_plan(T, d, 2 * f, true, 2 * f, d, apart);
 }
 
 // dx and dW_gu, either of them null to skip it.
@@ -1072,7 +904,7 @@ hipError_t dx_dw_gu(const bf16_t* dab, const bf16_t* x, const bf16_t* w_gu,
 // Workspaces.  Forward: S (when the caller keeps none), then the fp32
 // planes of y.  Backward: dAB, then the planes of dx.
 int64_t plane_bytes(int64_t T, int64_t N, int64_t K) {
-  const Plan r = plan(T, N, K, 256, true);
+  const Plan r = row_plan(T, N, K);
   return r.splits > 1 ? r.splits * T * N * 4 : 0;
 }
 
