@@ -15,12 +15,13 @@
 // kept exactly for the probability that is drawn.  16 bits a draw are half
 // the integer work of 32-bit draws (20 widening multiplies a counter); both
 // hide behind the memory traffic on MI355X (8192 x 4096 bf16 with a
-// residual: 36.6 and 36.5 us).
+// residual: 37.5 us, and 37.1 with 32-bit draws).
 // A dropped element adds exactly 0, whatever x holds there.
 //
 // Bound by memory: x, res and out once, 16-byte accesses, a chunk a thread
-// (8192 x 4096 bf16: 36.0 us with a residual and 23.7 us without, 5.6 TB/s;
-// 8 chunks a thread 38.5 and 25.2 us).
+// (8192 x 4096 bf16: 37.5 us with a residual, 5.4 TB/s, and 23.9 without, 5.6
+// TB/s; 8 chunks a thread 39.3 and 25.8 us).  All times: calls in a captured
+// sequence over data that leaves the caches.
 
 #include "common.cuh"
 #include "internal.h"

@@ -16,10 +16,20 @@
 //    optionally with the reduction split over workgroups.
 //  * large: bound by the matrix cores.  The grouped GEMM's 256 x 256 kernel
 //    without its routing plan (gemm.hip, gemm_dense_*).
-// On MI355X: 1 token through d 4096, f 14336 forward 66 us (5.3 TB/s of
-// weights); 24 through 2048 x 1408 10.3 us; 777 through 2048 x 2816 49 us
-// (550 TFLOP/s); 2000 through it forward and backward 248 us (840 TFLOP/s);
-// 8192 through 4096 x 14336 6.8 to 7.0 ms (1240 to 1280 TFLOP/s).
+// On MI355X, a pass among others: 1 token through d 4096, f 14336 forward 66
+// us (5.3 TB/s of weights); 24 through 2048 x 1408 10.3 us; 777 through 2048 x
+// 2816 49 us (550 TFLOP/s); 2000 through it forward and backward 248 to 252 us
+// (820 to 840 TFLOP/s); 8192 through 4096 x 14336 6.8 to 7.0 ms (1240 to 1280
+// TFLOP/s).
+//
+// What is rounded to bf16, and why: S and [dA dU], since they are operands of
+// bf16 matrix products (their fp32 form would need the products in two parts
+// or at the fp32 rate, a sixteenth); AB as saved for the backward, since it is
+// the largest tensor of the block (fp32 would double it), as in the expert
+// layer; y, dx and the weight gradients once, from fp32 sums.  S is computed
+// from the fp32 sums, not from the saved AB.  Against 64 bits y is off by
+// 0.0018 to 0.0023 of its norm and the gradients by 0.0030, where the last
+// rounding alone is 0.0017; without AB's the gradients would be at 0.0024.
 
 #include "common.cuh"
 #include "ffn_plan.h"
@@ -521,9 +531,10 @@ __global__ __launch_bounds__(256) void ffn_rows_kernel(
 // flight during the current chunk's products.  The waves' sums are added
 // in wave order through LDS.  Past a few tokens (kStageX) a wave loads its
 // chunk of x as whole 256-byte rows and turns it into fragments through its
-// own piece of LDS, in place of 16 rows x 64 bytes a load (2048 x 1408: 64
-// tokens 20.9 -> 16.7 us, 24 tokens 13.2 -> 12.4, 16 tokens 11.1 -> 10.3; one
-// token, where the turn only adds its latency, 8.7 -> 9.6).
+// own piece of LDS, in place of 16 rows x 64 bytes a load (2048 x 1408, whole
+// forwards in a captured sequence over data that leaves the caches: 64 tokens
+// 20.0 -> 14.9 us, 24 tokens 12.5 -> 10.7, 16 tokens 10.6 -> 9.1, 5 tokens 8.7
+// -> 9.0; one token, where the turn only adds its latency, 8.2 -> 8.9).
 //   RT = 16: kAct has a gate and an up tile; RT = 8: kAct packs 8 gate and
 //   8 up rows into one tile, kRow leaves half of its tile empty.  8 doubles
 //   the workgroups where 16 would leave CUs without one.

@@ -187,11 +187,11 @@ inline Plan dx_pair(int64_t T, int64_t d, int64_t f) {
 
 // Whether the weight-streaming form runs.  Its time grows with the tokens
 // (every workgroup reads all of them), the tiles' hardly does up to 64, but
-// tiles of narrow blocks leave CUs idle.  Forward on MI355X, thin and tiles,
-// us: 16 tokens 10 and 18 (d 2048, f 1408), 15 and 21 (2048, 2816), 26 and
-// 35 (4096, 4096), 75 and 78 (4096, 14336); 24 tokens 12 and 19, 20 and 20,
-// 32 and 33, 97 and 76; 64 tokens 17 and 23, 31 and 23, 50 and 38, 159 and
-// 82.
+// tiles of narrow blocks leave CUs idle.  Forward on MI355X in a captured
+// sequence over data that leaves the caches, thin and tiles, us: 16 tokens 9
+// and 16 (d 2048, f 1408), 15 and 20 (2048, 2816), 27 and 32 (4096, 4096), 80
+// and 78 (4096, 14336); 24 tokens 11 and 17, 20 and 20, 31 and 33, 97 and 76;
+// 64 tokens 15 and 18, 28 and 23, 58 and 39, 176 and 85.
 inline bool thin_form(int64_t T, int64_t d, int64_t f) {
   const int64_t bytes = 6 * d * f;
   return T <= 16 || (T <= 32 && bytes <= (int64_t{128} << 20)) ||

@@ -21,8 +21,16 @@
 // rounded once.
 //
 // On MI355X, 8192 x 4096 bf16 RMS: forward 24.6 us (5.5 TB/s), backward 48.6
-// (5.7 TB/s) and 4.6 us for the weight gradient's second kernel; 16384 x 2048
-// fp32 layer norm: 38.6, 83.2 and 4.8 us.  A copy moves 5.1 TB/s.
+// (5.7 TB/s) and 4.7 us for the weight gradient's second kernel; 16384 x 2048
+// fp32 layer norm: 38.4, 82.5 and 4.7 us (kernel times; as calls in a captured
+// sequence over data that leaves the caches 27 and 57 us, 41 and 89 us).  A
+// copy moves 5.1 TB/s.
+//
+// Above d = 8192 a row takes 16 waves, which leave a lane 128 registers, and
+// the backward of layer norm with its two column sums spills: 35 registers
+// for fp32, 4 for bf16; RMS norm none.  2048 x 16384, backward calls in a
+// captured sequence: layer norm fp32 138 us (its bytes at a copy's rate are
+// 92), bf16 72 (52); RMS norm fp32 98, bf16 61.
 
 #include "common.cuh"
 #include "internal.h"
@@ -387,9 +395,10 @@ auto with_map(int64_t d, F&& f) {
 // Workgroups of the two passes, by the threads they put on a CU, and no more
 // than there are rows.  The backward takes few: every workgroup leaves two
 // rows of partial sums, and with the next row's loads in flight 8 waves a CU
-// keep up with the memory (8192 x 4096 bf16 RMS: 57 us with 512 threads a
-// CU, 63 with 1024, 69 with 2048, 61 with 256; 1003 x 2056: 15, 20, 20 and
-// 14 us).  The forward is within 2% from 1024 to 16384.
+// keep up with the memory (both kernels of the backward, calls in a captured
+// sequence, 8192 x 4096 bf16 RMS: 57 us with 512 threads a CU, 63 with 1024,
+// 68 with 2048, 59 with 256; 1003 x 2056: 12.4, 17.2, 17.2 and 11.3 us).  The
+// forward is within 2% from 1024 to 16384.
 template <class M>
 int64_t blocks(int64_t T, int per_cu_threads) {
   const int per_cu = per_cu_threads / M::kThreads;
