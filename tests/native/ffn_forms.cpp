@@ -1,7 +1,6 @@
 // The kernel instances that a dense feed-forward call launches, as text, from
 // the plan the library itself uses.
 #include <stdio.h>
-#include <string.h>
 
 #include "ffn_plan.h"
 
@@ -12,28 +11,25 @@ namespace {
 struct Out {
   char* p;
   int left;
-  void add(const char* fmt, const char* name, int a, int b, int c,
-           const char* tail) {
-    const int n = snprintf(p, left, fmt, name, a, b, c, tail);
+  template <class... A>
+  void add(const char* fmt, A... a) {
+    const int n = snprintf(p, left, fmt, a...);
     if (n > 0 && n < left) {
       p += n;
       left -= n;
     }
   }
+  // sums: a row product, whose reduction may be split
   void tile(const char* name, const Plan& r, bool sums) {
     if (r.width == 256)
-      add("%s %dx%dx%d%s;", name, 256, 256, 1, "");
+      add("%s 256x256x1;", name);
     else
       add("%s %dx%dx%d%s;", name, r.height, r.width, r.groups,
           !sums ? "" : r.splits > 1 ? " split" : " whole");
   }
   void thin(const char* name, const ThinPlan& r) {
-    add("%s thin %d blocks %d rows%.0d%s;", name, r.blocks, r.rows, 0,
+    add("%s thin %d blocks %d rows%s;", name, r.blocks, r.rows,
         r.staged ? " staged" : "");
-  }
-  void pair(const char* name, const Plan& r, bool sums) {
-    add("%s %dx%dx%d%s;", name, r.width, r.width, 1,
-        !sums ? "" : r.splits > 1 ? " split" : " whole");
   }
 };
 
@@ -60,13 +56,13 @@ extern "C" void ffn_forms(int64_t T, int64_t d, int64_t f, int want,
     return;
   }
   if (dw2 && dact_pair(T, d, f).width) {
-    o.pair("dact+dw2", dact_pair(T, d, f), false);
+    o.tile("dact+dw2", dact_pair(T, d, f), false);
   } else {
     if (dw2) o.tile("dw", weight_plan(T, d, f), false);
     o.tile("dact", dact_plan(T, d, f), false);
   }
   if (dx && dw_gu && dx_pair(T, d, f).width) {
-    o.pair("dx+dw_gu", dx_pair(T, d, f), true);
+    o.tile("dx+dw_gu", dx_pair(T, d, f), true);
     return;
   }
   if (dw_gu) o.tile("dw", weight_plan(T, 2 * f, d), false);
