@@ -38,6 +38,8 @@
 namespace moe {
 namespace {
 
+static_assert(kMaxOperandBytes == kMaxResourceBytes, "one limit");
+
 enum Epi { kAct = 0, kDAct = 1, kRow = 2, kPlane = 3 };
 
 // ------------------------------------------------------------ activations

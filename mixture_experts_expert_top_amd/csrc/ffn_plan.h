@@ -5,11 +5,11 @@
 
 #include <stdint.h>
 
-#include "limits.h"
-
 namespace moe {
 
 constexpr int kBK = 64;      // reduction length of a k-step
+// bytes of a buffer resource (kMaxResourceBytes of internal.h)
+constexpr int64_t kMaxOperandBytes = 0xffffff00;
 
 // The form of one product: output tiles of `height` x `width` (256 x 256 for
 // the grouped GEMM's kernel), `groups` of 256 threads a tile, the reduction in
@@ -165,7 +165,7 @@ inline Plan dact_plan(int64_t T, int64_t d, int64_t f) {
 // A weight gradient [M][N], a sum over T.
 inline Plan weight_plan(int64_t T, int64_t M, int64_t N) {
   // the 256-wide kernel addresses an operand's rows with 32 bits
-  const bool fits = T * (M > N ? M : N) * 2 <= kMaxResourceBytes;
+  const bool fits = T * (M > N ? M : N) * 2 <= kMaxOperandBytes;
   return plan(M, N, T, 256, false, fits);
 }
 // A second launch costs about this much more than its kernel.

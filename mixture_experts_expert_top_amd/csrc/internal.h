@@ -5,14 +5,18 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "limits.h"
-
 namespace moe {
 
 typedef uint16_t bf16_t;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+// Buffer resources address their range with 32-bit byte offsets, and a
+// load at an offset at or past the range returns zero (tile masking).
+// kOob is the offset the kernels give a masked load; every resource range
+// is at most kOob bytes, so a masked load never reads memory.
+constexpr uint32_t kOob = 0xffffff00u;
+constexpr int64_t kMaxResourceBytes = kOob;
 // Partial-sum planes of the fp32 row outputs (fc2's O and fc1's data
 // gradient dXp), laid out [planes][T*k][d]; the combine adds them in plane
 // order.  Their reductions (over f and 2f) are cut in two when f is at
