@@ -2,8 +2,9 @@
  * moe.h -- C-ABI of libmoe.so: the mixture-of-experts expert-MLP hot path
  * (top-k routing, permutation by expert, grouped GEMM with fused SwiGLU and
  * routing-weight scaling, optional MXFP8 block quantization, un-permute
- * combine; forward and backward) and the residual block around it (norm,
- * dense gated feed-forward block, dropout) as hand-written HIP kernels for
+ * combine; forward and backward), the residual block around it (norm,
+ * dense gated feed-forward block, dropout) and the optimizer step that uses
+ * its gradients (gradient norm, AdamW) as hand-written HIP kernels for
  * gfx950.
  *
  * Sources, cited by page title and section:
@@ -85,7 +86,8 @@ typedef enum moe_entry {
   MOE_ENTRY_ROUTER_BWD = 3,
   MOE_ENTRY_NORM_BWD = 4,
   MOE_ENTRY_FFN_FWD = 5,
-  MOE_ENTRY_FFN_BWD = 6
+  MOE_ENTRY_FFN_BWD = 6,
+  MOE_ENTRY_GRAD_NORM = 7
 } moe_entry;
 
 /* Gate activation of moe_ffn_fwd and moe_ffn_bwd. */
@@ -682,11 +684,100 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
                        void* dx, void* dw_gu, void* dw2, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
 
+/* One gradient of moe_grad_norm: n values at g (device memory), bf16 or
+ * (g_fp32 != 0) fp32.  With n == 0 the pointer is not looked at. */
+typedef struct moe_grad {
+  const void* g;
+  int64_t n;
+  int32_t g_fp32;
+  int32_t reserved;        /* 0 */
+} moe_grad;
+
+/*
+ * moe_grad_norm -- the 2-norm of all gradients of a step taken together:
+ *   norm[0] = sqrt(sum over the tensors and their values of g^2)
+ * grads: count descriptors in HOST memory, read before the call returns;
+ * norm: one fp32 in device memory.  Squares and sums are fp64 in a fixed
+ * order, rounded once.  An infinite or NaN value makes the norm so.  The
+ * gradients may overlap each other, the norm and the workspace nothing.
+ * count >= 1, 0 <= n <= 2^34 each (MOE_ERR_UNSUPPORTED above); tensors
+ * 16-byte aligned.  Workspace: MOE_ENTRY_GRAD_NORM (its size depends on
+ * nothing).
+ */
+moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm,
+                         void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* How moe_adamw holds the two moments. */
+typedef enum moe_moments {
+  MOE_MOMENTS_FP32 = 0,  /* m and v in fp32                               */
+  MOE_MOMENTS_FP8 = 1    /* E4M3 codes of m and of sqrt(v), one fp32      */
+                         /* scale for each MOE_ADAMW_BLOCK values         */
+} moe_moments;
+
+#define MOE_ADAMW_BLOCK 256
+
+/* One tensor of moe_adamw; every pointer is device memory.  With n == 0 no
+ * pointer is looked at. */
+typedef struct moe_adamw_tensor {
+  void* p;                 /* [n] parameter, bf16 or (p_fp32 != 0) fp32   */
+  float* master;           /* [n] fp32 copy that a bf16 p is the rounding
+                              of, or NULL (always NULL for an fp32 p)     */
+  const void* g;           /* [n] gradient, bf16 or (g_fp32 != 0) fp32    */
+  void* m;                 /* [n] first moment                            */
+  void* v;                 /* [n] second moment (FP8: of its square root) */
+  float* m_scale;          /* FP8: [ceil(n / MOE_ADAMW_BLOCK)], else NULL */
+  float* v_scale;
+  int64_t n;
+  float weight_decay;      /* of this tensor, finite and >= 0             */
+  int32_t p_fp32, g_fp32;
+  int32_t reserved;        /* 0 */
+} moe_adamw_tensor;
+
+/*
+ * moe_adamw -- one AdamW step over many tensors (Loshchilov and Hutter,
+ * "Decoupled weight decay regularization"), in place:
+ *   c = 1, or with grad_norm: min(1, max_norm / (grad_norm[0] + 1e-6))
+ *   g' = c g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p - lr wd p - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * with t = step[0] >= 1 (the first step is 1) and lr = lr[0].  The new p is
+ * computed from master where there is one, which is replaced too; p is
+ * rounded to bf16 once.
+ *   tensors: count descriptors in HOST memory, read before the call returns.
+ *   step (int64), lr (fp32), grad_norm (fp32, or NULL: no clipping) are read
+ *   on the DEVICE when the kernel runs, so a captured step can be replayed
+ *   while its caller advances step and lr.  An infinite or NaN grad_norm
+ *   leaves every tensor as it was (the caller sees it in grad_norm).
+ * MOE_MOMENTS_FP8: code q of value i stands for q * scale[i / 256].  The
+ *   moments are updated in fp32, every operation rounded by itself, from
+ *   m = q_m s_m and r = q_v s_v, v = r^2; r' = sqrt(beta2 r^2 +
+ *   (1 - beta2) g'^2) is held in place of v and also used as it is for p.  A
+ *   block's scale is its largest |m| or r over 256 (0, with codes 0, where
+ *   that is below 1e-30); a value over its scale, y, is given u 2^-20ths of
+ *   its fourth significant bit (u = (t * 0x9E3779B1 mod 2^32) >> 12, in the
+ *   bits of the fp32 value), cut to four significant bits, and rounded to
+ *   the nearest E4M3 value; an r above 0 keeps at least the smallest code.
+ *   Codes and scales are exact (bit-identical to this definition).
+ * Moments of a tensor that was never stepped are all zero bytes, scales
+ * included.  Gradients are finite, g'^2 too, unless grad_norm leaves the step
+ * out; the fp32 arithmetic of p uses the hardware reciprocal.
+ * count >= 1, 0 <= n <= 2^34 each (MOE_ERR_UNSUPPORTED above), 0 <= beta < 1,
+ * 1e-20 <= eps <= 1, max_norm > 0 with grad_norm.  Tensors 16-byte aligned,
+ * step, lr and grad_norm aligned to their own size; what is written overlaps nothing else of the call
+ * (MOE_ERR_INVALID_ARG), gradients may overlap each other.  No workspace.
+ */
+moe_status moe_adamw(moe_moments moments, const moe_adamw_tensor* tensors,
+                     int32_t count, const int64_t* step, const float* lr,
+                     double beta1, double beta2, double eps,
+                     const float* grad_norm, double max_norm,
+                     hipStream_t stream);
+
 /*
  * moe_workspace_bytes -- workspace size an entry point needs for the given
  * problem (0 when none).  Returns 0 for invalid arguments.  The norm and
  * the dense feed-forward block have neither experts nor slots: E = k = 1
- * and prec MOE_BF16 (the norm ignores f).
+ * and prec MOE_BF16 (the norm ignores f).  MOE_ENTRY_GRAD_NORM ignores
+ * every size.
  */
 size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
                            int32_t E, int32_t k, int64_t d, int64_t f);

@@ -1,14 +1,19 @@
 // C-ABI of libmoe: argument validation, workspace layout and launch order.
 // Semantics of every entry point are documented in include/moe.h.
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "optim.h"
 
 using moe::bf16_t;
 
@@ -324,6 +329,116 @@ moe_status check_norm_dims(moe_norm kind, int64_t T, int64_t d) {
   return MOE_OK;
 }
 
+// The same for the many tensors of a table: a span is written or read, and
+// one that is written may overlap no other.
+struct Span {
+  uintptr_t lo, hi;
+  bool written;
+  int tensor;          // its index in the table, or -1
+};
+
+class Spans {
+ public:
+  // room for `most` spans, on the heap past what most steps need; ok() is
+  // false without the memory
+  explicit Spans(size_t most) {
+    if (most > kHere) {
+      heap_.reset(new (std::nothrow) Span[most]);
+      at_ = heap_.get();
+    }
+  }
+  bool ok() const { return at_ != nullptr; }
+  void add(const void* p, int64_t bytes, bool written, int tensor) {
+    if (!p || bytes <= 0) return;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    at_[n_++] = Span{lo, lo + static_cast<uintptr_t>(bytes), written, tensor};
+  }
+  // whether some written span overlaps another; *a and *b are then the two
+  // tensors
+  bool clash(int* a, int* b) {
+    std::sort(at_, at_ + n_,
+              [](const Span& x, const Span& y) { return x.lo < y.lo; });
+    // the spans so far that reach furthest, of all and of the written ones
+    const Span* any = nullptr;
+    const Span* written = nullptr;
+    for (size_t i = 0; i < n_; ++i) {
+      const Span* const s = at_ + i;
+      const Span* const o = s->written ? any : written;
+      if (o && s->lo < o->hi) {
+        *a = o->tensor;
+        *b = s->tensor;
+        return true;
+      }
+      if (!any || s->hi > any->hi) any = s;
+      if (s->written && (!written || s->hi > written->hi)) written = s;
+    }
+    return false;
+  }
+
+ private:
+  static constexpr size_t kHere = 512;
+  Span here_[kHere];
+  std::unique_ptr<Span[]> heap_;
+  Span* at_ = here_;
+  size_t n_ = 0;
+};
+
+moe_status check_scalar(const char* name, const void* p, size_t size) {
+  REQUIRE(p != nullptr, MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  REQUIRE(reinterpret_cast<uintptr_t>(p) % size == 0, MOE_ERR_INVALID_ARG,
+          "%s is not %zu-byte aligned", name, size);
+  return MOE_OK;
+}
+
+moe_status check_table(const void* table, const char* name, int32_t count) {
+  REQUIRE(table != nullptr, MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  REQUIRE(count >= 1, MOE_ERR_INVALID_ARG, "count must be >= 1 (got %d)",
+          count);
+  return MOE_OK;
+}
+
+moe_status check_length(int i, int64_t n) {
+  REQUIRE(n >= 0, MOE_ERR_INVALID_ARG, "tensor %d: n must be >= 0 (got %lld)",
+          i, static_cast<long long>(n));
+  REQUIRE(n <= moe::kMaxTensor, MOE_ERR_UNSUPPORTED,
+          "tensor %d: n must be at most 2^34 (got %lld)", i,
+          static_cast<long long>(n));
+  return MOE_OK;
+}
+
+moe_status check_member(int i, const char* name, const void* p) {
+  REQUIRE(p != nullptr, MOE_ERR_INVALID_ARG, "tensor %d: %s is NULL", i,
+          name);
+  REQUIRE(aligned16(p), MOE_ERR_INVALID_ARG,
+          "tensor %d: %s is not 16-byte aligned", i, name);
+  return MOE_OK;
+}
+
+moe_status check_adamw_tensor(int i, const moe_adamw_tensor& t, bool fp8) {
+  if (moe_status st = check_length(i, t.n)) return st;
+  if (t.n == 0) return MOE_OK;
+  if (moe_status st = check_member(i, "p", t.p)) return st;
+  if (moe_status st = check_member(i, "g", t.g)) return st;
+  if (moe_status st = check_member(i, "m", t.m)) return st;
+  if (moe_status st = check_member(i, "v", t.v)) return st;
+  if (t.master) {
+    REQUIRE(!t.p_fp32, MOE_ERR_INVALID_ARG,
+            "tensor %d: an fp32 parameter takes no master", i);
+    if (moe_status st = check_member(i, "master", t.master)) return st;
+  }
+  if (fp8) {
+    if (moe_status st = check_member(i, "m_scale", t.m_scale)) return st;
+    if (moe_status st = check_member(i, "v_scale", t.v_scale)) return st;
+  } else {
+    REQUIRE(!t.m_scale && !t.v_scale, MOE_ERR_INVALID_ARG,
+            "tensor %d: fp32 moments take no scales", i);
+  }
+  REQUIRE(t.weight_decay >= 0.0f && t.weight_decay <= 3.4e38f,
+          MOE_ERR_INVALID_ARG,
+          "tensor %d: weight_decay must be finite and >= 0", i);
+  return MOE_OK;
+}
+
 // A tile's 256 rows of the widest operand (dAB, 2f wide) stay inside a
 // buffer resource up to this width.
 constexpr int64_t kMaxFfnWidth = int64_t{1} << 21;
@@ -407,6 +522,7 @@ const char* moe_version(void) { return "libmoe 0.1 gfx950"; }
 
 size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
                            int32_t E, int32_t k, int64_t d, int64_t f) {
+  if (entry == MOE_ENTRY_GRAD_NORM) return moe::grad_norm_workspace();
   if (T < 1 || E < 1 || E > moe::kMaxExperts || k < 1 || k > E) return 0;
   if (prec != MOE_BF16 && !is_mx(prec)) return 0;
   const int64_t Tk = T * k;
@@ -430,6 +546,8 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       if (f < 1 || d < 1) return 0;
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
       return mx_bwd_layout(Tk, E, d, f, mx_bwd_base(Tk, f)).total;
+    default:
+      break;
   }
   return 0;
 }
@@ -1391,6 +1509,95 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
           static_cast<bf16_t*>(dx), static_cast<bf16_t*>(dw_gu),
           static_cast<bf16_t*>(dw2), workspace, stream),
       "moe_ffn_bwd");
+}
+
+moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm,
+                         void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+  if (moe_status st = check_table(grads, "grads", count)) return st;
+  if (moe_status st = check_scalar("norm", norm, 4)) return st;
+  REQUIRE_PTR(workspace);
+  const size_t need = moe::grad_norm_workspace();
+  REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE,
+          "workspace too small: %zu < %zu", workspace_bytes, need);
+  const Range outs[] = {{"norm", norm, 4},
+                        {"workspace", workspace, static_cast<int64_t>(need)}};
+  const Range none[] = {{"", nullptr, 0}};
+  if (moe_status st = check_disjoint(outs, none)) return st;
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_grad& t = grads[i];
+    if (moe_status st = check_length(i, t.n)) return st;
+    if (t.n == 0) continue;
+    if (moe_status st = check_member(i, "g", t.g)) return st;
+    const Range g{"", t.g, t.n * (t.g_fp32 ? 4 : 2)};
+    REQUIRE(!overlap(outs[0], g) && !overlap(outs[1], g), MOE_ERR_INVALID_ARG,
+            "tensor %d: g overlaps the norm or the workspace", i);
+  }
+  return hip_status(
+      moe::launch_grad_norm(grads, count, norm, workspace, stream),
+      "moe_grad_norm");
+}
+
+moe_status moe_adamw(moe_moments moments, const moe_adamw_tensor* tensors,
+                     int32_t count, const int64_t* step, const float* lr,
+                     double beta1, double beta2, double eps,
+                     const float* grad_norm, double max_norm,
+                     hipStream_t stream) {
+  REQUIRE(moments == MOE_MOMENTS_FP32 || moments == MOE_MOMENTS_FP8,
+          MOE_ERR_INVALID_ARG, "unknown form of the moments %d",
+          static_cast<int>(moments));
+  if (moe_status st = check_table(tensors, "tensors", count)) return st;
+  if (moe_status st = check_scalar("step", step, 8)) return st;
+  if (moe_status st = check_scalar("lr", lr, 4)) return st;
+  REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0,
+          MOE_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  REQUIRE(eps >= 1e-20 && eps <= 1.0, MOE_ERR_INVALID_ARG,
+          "eps must be in [1e-20, 1]");
+  if (grad_norm) {
+    if (moe_status st = check_scalar("grad_norm", grad_norm, 4)) return st;
+    REQUIRE(max_norm > 0.0 && max_norm <= 3.4e38, MOE_ERR_INVALID_ARG,
+            "max_norm must be finite and > 0");
+  }
+  const bool fp8 = moments == MOE_MOMENTS_FP8;
+  Spans spans(static_cast<size_t>(count) * 7 + 3);
+  REQUIRE(spans.ok(), MOE_ERR_UNSUPPORTED,
+          "no host memory for a table of %d tensors", count);
+  spans.add(step, 8, false, -1);
+  spans.add(lr, 4, false, -1);
+  spans.add(grad_norm, 4, false, -1);
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (moe_status st = check_adamw_tensor(i, t, fp8)) return st;
+    const int64_t blocks = (t.n + moe::kStateBlock - 1) / moe::kStateBlock;
+    if (t.n == 0) continue;
+    spans.add(t.p, t.n * (t.p_fp32 ? 4 : 2), true, i);
+    spans.add(t.master, t.n * 4, true, i);
+    spans.add(t.g, t.n * (t.g_fp32 ? 4 : 2), false, i);
+    spans.add(t.m, t.n * (fp8 ? 1 : 4), true, i);
+    spans.add(t.v, t.n * (fp8 ? 1 : 4), true, i);
+    if (fp8) {
+      spans.add(t.m_scale, blocks * 4, true, i);
+      spans.add(t.v_scale, blocks * 4, true, i);
+    }
+  }
+  int a = 0, b = 0;
+  REQUIRE(!spans.clash(&a, &b), MOE_ERR_INVALID_ARG,
+          "tensors %d and %d: what the step writes overlaps (-1: step, lr or "
+          "grad_norm)", a, b);
+  moe::AdamwHyper h;
+  h.b1 = static_cast<float>(beta1);
+  h.c1 = static_cast<float>(1.0 - beta1);
+  h.b2 = static_cast<float>(beta2);
+  h.c2 = static_cast<float>(1.0 - beta2);
+  h.log_b1 = log(beta1);
+  h.log_b2 = log(beta2);
+  h.eps = static_cast<float>(eps);
+  h.max_norm = static_cast<float>(max_norm);
+  h.step = step;
+  h.lr = lr;
+  h.norm = grad_norm;
+  return hip_status(moe::launch_adamw(fp8, tensors, count, h, stream),
+                    "moe_adamw");
 }
 
 }  // extern "C"

@@ -1,0 +1,456 @@
+// The step that uses the gradients: their global norm, and AdamW over many
+// tensors in one launch.
+//
+//   norm = sqrt(sum over all tensors of g^2)
+//   g' = g min(1, max_norm / (norm + 1e-6))
+//   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
+//   p = p - lr wd p - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Both kernels are bound by memory: a value's gradient, parameter and moments
+// are read once and the parameter and moments written once.  The table of
+// tensors travels in the kernel's arguments (kTensors a launch), so a call
+// copies nothing to the device and can be captured.
+//
+// 8-bit moments.  m and r = sqrt(v) are held as E4M3 codes with an fp32 scale
+// for each 256 values (the block's largest magnitude stands at 256, so nothing
+// reaches the format's end).  Rounding to nearest would hold a moment that
+// moves by less than half a code a step where it is for good (sqrt(v) falls by
+// 0.05% a step at b2 = 0.999, a code is 6 to 12%), so before a value is cut to
+// four significant bits a fraction of the last of them is added that depends
+// on the step alone (multiples of the golden ratio modulo 1): over the steps
+// the cuts average out, and no random numbers are read.  r is held rather
+// than v because it spans half the exponents: 2^17 from the scale's top to the
+// smallest code, which is also the least that a second moment above zero is
+// held as, so that it never divides as zero.
+
+#include "optim.h"
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+// every fp32 operation of the moments is rounded by itself, so that codes and
+// scales are defined to the bit
+#pragma clang fp contract(off)
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;                         // values a thread and pass
+constexpr int kChunk = kThreads * kVec;         // values a workgroup
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p);
+  const f32x4 b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = a[i];
+    v[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void load8(const bf16_t* p, float* v) {
+  const i32x4 r = *reinterpret_cast<const i32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf_lo(static_cast<uint32_t>(r[i]));
+    v[2 * i + 1] = bf_hi(static_cast<uint32_t>(r[i]));
+  }
+}
+__device__ __forceinline__ void store8(bf16_t* p, const float* v) {
+  i32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = static_cast<int>(pack_bf16x2(v[2 * i], v[2 * i + 1]));
+  *reinterpret_cast<i32x4*>(p) = o;
+}
+// E4M3 codes
+__device__ __forceinline__ void load8(const uint8_t* p, float* v) {
+  const i32x2 r = *reinterpret_cast<const i32x2*>(p);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(r[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(r[i], true);
+    v[4 * i] = lo[0];
+    v[4 * i + 1] = lo[1];
+    v[4 * i + 2] = hi[0];
+    v[4 * i + 3] = hi[1];
+  }
+}
+__device__ __forceinline__ void store8(uint8_t* p, const float* v) {
+  i32x2 o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0,
+                                                  false);
+    o[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], w,
+                                           true);
+  }
+  *reinterpret_cast<i32x2*>(p) = o;
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const bf16_t* p) { return bf2f(*p); }
+__device__ __forceinline__ float load1(const uint8_t* p) {
+  return __builtin_amdgcn_cvt_f32_fp8(*p, 0);
+}
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(bf16_t* p, float v) { *p = f2bf(v); }
+__device__ __forceinline__ void store1(uint8_t* p, float v) {
+  *p = static_cast<uint8_t>(
+      __builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+}
+
+// `left` values of 8 (8 or more: all), the rest zero
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int64_t left, float* v) {
+  if (left >= kVec) {
+    load8(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) v[i] = i < left ? load1(p + i) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int64_t left,
+                                           const float* v) {
+  if (left >= kVec) {
+    store8(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+    if (i < left) store1(p + i, v[i]);
+}
+
+// The last entry of first[0 .. count) that is not above `chunk`.
+__device__ __forceinline__ int find_tensor(const uint32_t* first, int count,
+                                           uint32_t chunk) {
+  int lo = 0, n = count;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (first[lo + half] <= chunk) lo += half;
+    n -= half;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------- norm
+// fp64 sums of squares: the vector units add doubles at the rate of floats,
+// and the clip factor then depends on no order of summation.
+constexpr int kNormTensors = 160;
+constexpr int kNormGroups = 1024;
+
+struct NormTable {
+  const void* g[kNormTensors];
+  int64_t n[kNormTensors];
+  uint32_t first[kNormTensors];       // first chunk
+  uint8_t fp32[kNormTensors];
+  int count;
+  uint32_t chunks;
+  int add;                            // to what an earlier launch left
+};
+
+// The sum over a wave's lanes, in a fixed order, in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, kWave);
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ double sum8(const T* g, int64_t left) {
+  float v[kVec];
+  load_some(g, left, v);
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const double x = v[i];
+    s = fma(x, x, s);
+  }
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(
+    NormTable P, double* __restrict__ part) {
+  __shared__ double red[kThreads / kWave];
+  double s = 0.0;
+  for (uint32_t c = blockIdx.x; c < P.chunks; c += gridDim.x) {
+    const int i = find_tensor(P.first, P.count, c);
+    const int64_t at = static_cast<int64_t>(c - P.first[i]) * kChunk +
+                       threadIdx.x * kVec;
+    const int64_t left = P.n[i] - at;
+    if (left <= 0) continue;
+    s += P.fp32[i] ? sum8(static_cast<const float*>(P.g[i]) + at, left)
+                   : sum8(static_cast<const bf16_t*>(P.g[i]) + at, left);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = P.add ? part[blockIdx.x] : 0.0;
+    for (int w = 0; w < kThreads / kWave; ++w) s += red[w];
+    part[blockIdx.x] = s;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_finish_kernel(
+    const double* __restrict__ part, int count, float* __restrict__ norm) {
+  __shared__ double red[kThreads / kWave];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += kThreads) s += part[i];
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int w = 0; w < kThreads / kWave; ++w) s += red[w];
+    norm[0] = static_cast<float>(sqrt(s));
+  }
+}
+
+// ------------------------------------------------------------------ AdamW
+constexpr int kTensors = 48;
+
+struct AdamwTable {
+  void* p[kTensors];
+  float* master[kTensors];
+  const void* g[kTensors];
+  void* m[kTensors];
+  void* v[kTensors];
+  float* ms[kTensors];
+  float* vs[kTensors];
+  int64_t n[kTensors];
+  uint32_t first[kTensors];           // first chunk
+  float decay[kTensors];
+  uint8_t p_fp32[kTensors], g_fp32[kTensors];
+  int count;
+  AdamwHyper h;
+};
+static_assert(sizeof(AdamwTable) <= 4096, "kernel arguments");
+static_assert(sizeof(NormTable) <= 4096, "kernel arguments");
+
+// What every value of a step shares.
+struct Shared {
+  float b1, c1, b2, c2, coef, size, root, eps, lr;
+  uint32_t dither;
+  bool clip;
+};
+
+// 1 - b^t, to about an ulp for every t (t log b is rounded once, and expm1
+// keeps its relative precision)
+__device__ __forceinline__ float one_minus_power(double log_b, int64_t t) {
+  return -expm1f(static_cast<float>(static_cast<double>(t) * log_b));
+}
+
+// a moment, cut to what E4M3 holds: `y` in units of the block's scale
+__device__ __forceinline__ float cut(float y, uint32_t dither) {
+  return __uint_as_float((__float_as_uint(y) + dither) & ~0xfffffu);
+}
+
+// The largest of 32 lanes' values, in each of them.
+__device__ __forceinline__ float max32(float v) {
+  v = dpp_group_max<16>(v);
+  return fmaxf(v, shfl_xor(v, 16));
+}
+
+// Eight values of one tensor from `at` on.  kBits8: the 32 lanes of half a
+// wave hold a block, and lanes past the tensor's end hold zeros.
+template <bool kBits8, typename TP, bool kMaster, typename TG>
+__device__ __forceinline__ void update(const AdamwTable& P, int i, int64_t at,
+                                       const Shared& S) {
+  const int64_t left = P.n[i] - at;
+  if (!kBits8 && left <= 0) return;
+  TP* const p = static_cast<TP*>(P.p[i]) + at;
+  float* const master = P.master[i] + at;
+  float g[kVec], x[kVec], m[kVec], r[kVec];
+  load_some(static_cast<const TG*>(P.g[i]) + at, left, g);
+  if constexpr (kMaster)
+    load_some(master, left, x);
+  else
+    load_some(p, left, x);
+  using TS = typename std::conditional<kBits8, uint8_t, float>::type;
+  TS* const pm = static_cast<TS*>(P.m[i]) + at;
+  TS* const pv = static_cast<TS*>(P.v[i]) + at;
+  load_some(pm, left, m);
+  load_some(pv, left, r);
+  if (S.clip)
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) g[q] *= S.coef;
+  if constexpr (kBits8) {
+    const int64_t b = at / kStateBlock;
+    const float sm = left > 0 ? P.ms[i][b] : 0.0f;
+    const float sv = left > 0 ? P.vs[i][b] : 0.0f;
+    float tm = 0.0f, tr = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) {
+      m[q] = m[q] * sm * S.b1 + g[q] * S.c1;
+      const float ro = r[q] * sv;
+      r[q] = sqrtf(ro * ro * S.b2 + g[q] * g[q] * S.c2);
+      tm = fmaxf(tm, fabsf(m[q]));
+      tr = fmaxf(tr, r[q]);
+    }
+    tm = max32(tm);
+    tr = max32(tr);
+    const float im = tm >= 1e-30f ? 256.0f / tm : 0.0f;
+    const float ir = tr >= 1e-30f ? 256.0f / tr : 0.0f;
+    float ym[kVec], yr[kVec];
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) {
+      ym[q] = cut(m[q] * im, S.dither);
+      yr[q] = r[q] > 0.0f ? cut(fmaxf(r[q] * ir, 0x1p-9f), S.dither) : 0.0f;
+    }
+    if (left > 0) {
+      store_some(pm, left, ym);
+      store_some(pv, left, yr);
+      if ((threadIdx.x & 31) == 0) {
+        P.ms[i][b] = tm >= 1e-30f ? tm * 0x1p-8f : 0.0f;
+        P.vs[i][b] = tr >= 1e-30f ? tr * 0x1p-8f : 0.0f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) {
+      m[q] = m[q] * S.b1 + g[q] * S.c1;
+      r[q] = r[q] * S.b2 + g[q] * g[q] * S.c2;
+    }
+    store_some(pm, left, m);
+    store_some(pv, left, r);
+#pragma unroll
+    for (int q = 0; q < kVec; ++q) r[q] = sqrtf(r[q]);
+  }
+  if (left <= 0) return;
+  const float shrink = S.lr * P.decay[i];
+#pragma unroll
+  for (int q = 0; q < kVec; ++q) {
+    const float d = fmaf(r[q], S.root, S.eps);
+    const float u = m[q] * __builtin_amdgcn_rcpf(d);
+    x[q] = fmaf(-S.size, u, fmaf(-shrink, x[q], x[q]));
+  }
+  if constexpr (kMaster) store_some(master, left, x);
+  store_some(p, left, x);
+}
+
+template <bool kBits8>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable P) {
+  Shared S;
+  S.clip = P.h.norm != nullptr;
+  S.coef = 1.0f;
+  if (S.clip) {
+    const float norm = *P.h.norm;
+    // an infinite or NaN norm: the step is left out
+    if (!(fabsf(norm) < INFINITY)) return;
+    S.coef = fminf(P.h.max_norm / (norm + 1e-6f), 1.0f);
+  }
+  const int64_t t = *P.h.step;
+  S.b1 = P.h.b1;
+  S.c1 = P.h.c1;
+  S.b2 = P.h.b2;
+  S.c2 = P.h.c2;
+  S.eps = P.h.eps;
+  S.lr = *P.h.lr;
+  S.size = S.lr / one_minus_power(P.h.log_b1, t);
+  S.root = 1.0f / sqrtf(one_minus_power(P.h.log_b2, t));
+  S.dither = (static_cast<uint32_t>(t) * 0x9e3779b1u) >> 12;
+  const int i = find_tensor(P.first, P.count, blockIdx.x);
+  const int64_t at = static_cast<int64_t>(blockIdx.x - P.first[i]) * kChunk +
+                     threadIdx.x * kVec;
+  if (P.p_fp32[i]) {
+    if (P.g_fp32[i])
+      update<kBits8, float, false, float>(P, i, at, S);
+    else
+      update<kBits8, float, false, bf16_t>(P, i, at, S);
+  } else if (P.master[i]) {
+    if (P.g_fp32[i])
+      update<kBits8, bf16_t, true, float>(P, i, at, S);
+    else
+      update<kBits8, bf16_t, true, bf16_t>(P, i, at, S);
+  } else {
+    if (P.g_fp32[i])
+      update<kBits8, bf16_t, false, float>(P, i, at, S);
+    else
+      update<kBits8, bf16_t, false, bf16_t>(P, i, at, S);
+  }
+}
+
+}  // namespace
+
+size_t grad_norm_workspace() { return kNormGroups * sizeof(double); }
+
+hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
+                            void* ws, hipStream_t s) {
+  double* part = static_cast<double*>(ws);
+  int64_t all = 0;
+  for (int i = 0; i < count; ++i) all += (grads[i].n + kChunk - 1) / kChunk;
+  const int groups = static_cast<int>(
+      all < 1 ? 1 : all < kNormGroups ? all : kNormGroups);
+  int i = 0;
+  bool first = true;
+  do {
+    NormTable P{};
+    int64_t chunks = 0;
+    for (; i < count && P.count < kNormTensors; ++i) {
+      if (grads[i].n == 0) continue;
+      const int64_t c = (grads[i].n + kChunk - 1) / kChunk;
+      if (chunks + c > 0xffffffff) break;
+      const int q = P.count++;
+      P.g[q] = grads[i].g;
+      P.n[q] = grads[i].n;
+      P.fp32[q] = grads[i].g_fp32 != 0;
+      P.first[q] = static_cast<uint32_t>(chunks);
+      chunks += c;
+    }
+    P.chunks = static_cast<uint32_t>(chunks);
+    P.add = !first;
+    first = false;
+    hipLaunchKernelGGL(grad_norm_kernel, dim3(groups), dim3(kThreads), 0, s,
+                       P, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } while (i < count);
+  hipLaunchKernelGGL(grad_norm_finish_kernel, dim3(1), dim3(kThreads), 0, s,
+                     part, groups, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(bool bits8, const moe_adamw_tensor* t, int count,
+                        const AdamwHyper& h, hipStream_t s) {
+  int i = 0;
+  while (i < count) {
+    AdamwTable P{};
+    P.h = h;
+    int64_t chunks = 0;
+    for (; i < count && P.count < kTensors; ++i) {
+      if (t[i].n == 0) continue;
+      const int64_t c = (t[i].n + kChunk - 1) / kChunk;
+      if (chunks + c > kMaxGroups) break;
+      const int q = P.count++;
+      P.p[q] = t[i].p;
+      P.master[q] = t[i].master;
+      P.g[q] = t[i].g;
+      P.m[q] = t[i].m;
+      P.v[q] = t[i].v;
+      P.ms[q] = t[i].m_scale;
+      P.vs[q] = t[i].v_scale;
+      P.n[q] = t[i].n;
+      P.decay[q] = t[i].weight_decay;
+      P.p_fp32[q] = t[i].p_fp32 != 0;
+      P.g_fp32[q] = t[i].g_fp32 != 0;
+      P.first[q] = static_cast<uint32_t>(chunks);
+      chunks += c;
+    }
+    if (P.count == 0) break;
+    const dim3 grid(static_cast<uint32_t>(chunks));
+    if (bits8)
+      hipLaunchKernelGGL(adamw_kernel<true>, grid, dim3(kThreads), 0, s, P);
+    else
+      hipLaunchKernelGGL(adamw_kernel<false>, grid, dim3(kThreads), 0, s, P);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

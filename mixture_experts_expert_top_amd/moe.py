@@ -25,6 +25,10 @@ MOE_ENTRY_ROUTER_BWD = 3
 MOE_ENTRY_NORM_BWD = 4
 MOE_ENTRY_FFN_FWD = 5
 MOE_ENTRY_FFN_BWD = 6
+MOE_ENTRY_GRAD_NORM = 7
+MOE_MOMENTS_FP32 = 0
+MOE_MOMENTS_FP8 = 1
+MOE_ADAMW_BLOCK = 256
 MOE_NORM_LAYER = 0
 MOE_NORM_RMS = 1
 MOE_ACT_SILU = 0
@@ -42,7 +46,7 @@ EXPORTED = [
     "moe_mx_down_swiglu_bwd", "moe_mx_gate_up_dgrad", "moe_mx_grouped_wgrad",
     "moe_router_backward", "moe_mxfp4_quantize", "moe_permute_noalloc",
     "moe_norm_fwd", "moe_norm_bwd", "moe_dropout", "moe_ffn_fwd",
-    "moe_ffn_bwd",
+    "moe_ffn_bwd", "moe_grad_norm", "moe_adamw",
 ]
 # fixed per-GPU scratch of moe_permute_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 2 << 20
@@ -121,6 +125,10 @@ def _load():
                               P]),
         "moe_ffn_bwd": (I32, [I32, P, P, P, P, P, P, P, I64, I64, I64, P, P,
                               P, P, SZ, P]),
+        "moe_grad_norm": (I32, [P, I32, P, P, SZ, P]),
+        "moe_adamw": (I32, [I32, P, I32, P, P, ctypes.c_double,
+                            ctypes.c_double, ctypes.c_double, P,
+                            ctypes.c_double, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -670,6 +678,7 @@ def moe_mx_grouped_wgrad(aq, as_, bq, bs, offsets, Tk, c, stream=None,
 # which must be one of that GPU's) whichever device is current.
 
 _BF16, _F32 = torch.bfloat16, torch.float32
+_F8 = torch.float8_e4m3fn
 
 
 def _checked(name, specs):
@@ -823,3 +832,142 @@ def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
     _enqueue("moe_ffn_bwd", stream, dev, lib.moe_ffn_bwd, act, p[0], p[1],
              p[2], p[3], p[4], p[5], p[6], T, d, f, p[7], p[8],
              p[9], p[10], _nbytes(workspace))
+
+
+# --------------------------------------------------------- optimizer step
+
+class Grad(ctypes.Structure):
+    """moe_grad of include/moe.h."""
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("g_fp32", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """moe_adamw_tensor of include/moe.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("p", "master", "g", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+        ("p_fp32", ctypes.c_int32), ("g_fp32", ctypes.c_int32),
+        ("reserved", ctypes.c_int32)]
+
+
+class _Table:
+    """Descriptors of tensors that live as long as the table does, all on
+    the GPU `dev`; built once and passed to every step."""
+
+    def __init__(self, name, rows, struct, specs_of, fill):
+        if not rows:
+            raise ValueError(f"{name}: no tensors")
+        self.entries = (struct * len(rows))()
+        self.count = len(rows)
+        self.tensors = []
+        self.dev = None
+        for i, row in enumerate(rows):
+            specs = specs_of(row)
+            dev, p = _checked(f"{name}: tensor {i}", specs)
+            if self.dev is None:
+                self.dev = dev
+            elif dev != self.dev:
+                raise ValueError(f"{name}: tensor {i} on cuda:{dev}, others "
+                                 f"on cuda:{self.dev}")
+            fill(self.entries[i], row, p)
+            self.tensors.append([t for _, t, _, _ in specs if t is not None])
+        self.ptr = ctypes.addressof(self.entries)
+
+
+def grad_table(grads):
+    """The table of moe_grad_norm: bf16 or fp32 tensors of any shape on one
+    GPU, which have to stay where they are while the table is used (it holds
+    a reference to each)."""
+    def fill(e, g, p):
+        e.g, e.n, e.g_fp32 = p[0], g.numel(), g.dtype is _F32
+    return _Table("grad_table", grads, Grad,
+                  lambda g: (("g", g, _stream_dtype(g, "g"), None),), fill)
+
+
+class AdamwTable(_Table):
+    moments = MOE_MOMENTS_FP32
+
+
+def adamw_table(tensors):
+    """The table of moe_adamw.  tensors: dicts of p (bf16 or fp32), g (bf16
+    or fp32), m and v of one shape, master (fp32, for a bf16 p; optional) and
+    weight_decay (0 if it is left out).  m and v are fp32, or all of them
+    torch.float8_e4m3fn with m_scale and v_scale (fp32, one for each
+    MOE_ADAMW_BLOCK values); a tensor that was never stepped has zeros in
+    all of them.  The tensors have to stay where they are while the table is
+    used (it holds a reference to each)."""
+    known = {"p", "master", "g", "m", "v", "m_scale", "v_scale",
+             "weight_decay"}
+    fp8 = bool(tensors) and tensors[0]["m"].dtype is _F8
+
+    def specs_of(t):
+        if not known.issuperset(t):
+            raise TypeError("adamw_table: unknown " +
+                            ", ".join(sorted(set(t) - known)))
+        p = t["p"]
+        if p is None:
+            raise ValueError("adamw_table: p is required")
+        shape = p.shape
+        for n in ("g", "m", "v"):
+            _want(t[n], n, t[n].dtype if t[n] is not None else None)
+        st = _F8 if fp8 else _F32
+        blocks = (-(-p.numel() // MOE_ADAMW_BLOCK),)
+        for n in ("m_scale", "v_scale"):
+            if (t.get(n) is not None) != fp8:
+                raise ValueError(f"adamw_table: {n} goes with moments in "
+                                 "float8_e4m3fn")
+        return (("p", p, _stream_dtype(p, "p"), None),
+                ("master", t.get("master"), _F32, shape),
+                ("g", t["g"], _stream_dtype(t["g"], "g"), shape),
+                ("m", t["m"], st, shape), ("v", t["v"], st, shape),
+                ("m_scale", t.get("m_scale"), _F32, blocks),
+                ("v_scale", t.get("v_scale"), _F32, blocks))
+
+    def fill(e, t, p):
+        (e.p, e.master, e.g, e.m, e.v, e.m_scale, e.v_scale) = p
+        e.n = t["p"].numel()
+        e.weight_decay = float(t.get("weight_decay", 0.0))
+        e.p_fp32 = t["p"].dtype is _F32
+        e.g_fp32 = t["g"].dtype is _F32
+
+    table = AdamwTable("adamw_table", tensors, AdamwTensor, specs_of, fill)
+    table.moments = MOE_MOMENTS_FP8 if fp8 else MOE_MOMENTS_FP32
+    return table
+
+
+def _on_table(name, table, kind, specs):
+    """Pointers of the tensors beside a table, which lie on its GPU."""
+    if not isinstance(table, kind):
+        raise TypeError(f"{name}: expected a table, got "
+                        f"{type(table).__name__}")
+    dev, p = _checked(name, specs)
+    if dev != table.dev:
+        raise ValueError(f"{name}: the table is on cuda:{table.dev}, other "
+                         f"tensors on cuda:{dev}")
+    return dev, p
+
+
+def moe_grad_norm(table, norm, workspace, stream=None):
+    """norm[0] = the 2-norm of all gradients of grad_table(...) together."""
+    dev, p = _on_table("moe_grad_norm", table, _Table, (
+        ("norm", norm, _F32, (1,)),
+        ("workspace", workspace, _dtype(workspace), None)))
+    if isinstance(table, AdamwTable):
+        raise TypeError("moe_grad_norm: expected a grad_table")
+    _enqueue("moe_grad_norm", stream, dev, lib.moe_grad_norm, table.ptr,
+             table.count, p[0], p[1], _nbytes(workspace))
+
+
+def moe_adamw(table, step, lr, beta1, beta2, eps, grad_norm=None,
+              max_norm=1.0, stream=None):
+    """One AdamW step over adamw_table(...), in place (see include/moe.h).
+    step (int64 [1], the first step is 1), lr (fp32 [1]) and grad_norm (fp32
+    [1] or None: no clipping) lie on the device and are read when the kernel
+    runs."""
+    dev, p = _on_table("moe_adamw", table, AdamwTable, (
+        ("step", step, torch.int64, (1,)), ("lr", lr, _F32, (1,)),
+        ("grad_norm", grad_norm, _F32, (1,))))
+    _enqueue("moe_adamw", stream, dev, lib.moe_adamw, table.moments,
+             table.ptr, table.count, p[0], p[1], beta1, beta2, eps, p[2],
+             max_norm)

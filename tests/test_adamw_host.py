@@ -1,0 +1,184 @@
+"""Host-side checks of moe_grad_norm and moe_adamw (fake device addresses:
+validation fails before anything is launched), and of the oracle's 8-bit
+moments."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from mixture_experts_expert_top_amd import moe
+from oracle import mx_ref
+from oracle import optim_ref as R
+
+L = moe.lib
+INVALID, UNSUP, WS = 1, 2, 3
+A = 1 << 20       # fake, aligned device addresses
+STEP, LR, NORM, WSP = 4096, 4104, 4112, 8192
+
+
+def adamw_tensor(i=0, n=1000, **kw):
+    base = A + i * (1 << 24)
+    t = moe.AdamwTensor(p=base, g=base + (1 << 18), m=base + (2 << 18),
+                        v=base + (3 << 18), n=n)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return t
+
+
+def call(tensors, moments=0, count=None, step=STEP, lr=LR, b1=0.9, b2=0.95,
+         eps=1e-8, norm=None, max_norm=1.0):
+    arr = (moe.AdamwTensor * max(1, len(tensors)))(*tensors)
+    return L.moe_adamw(moments, ctypes.addressof(arr),
+                       len(tensors) if count is None else count, step, lr,
+                       b1, b2, eps, norm, max_norm, None)
+
+
+def refused(status, *words):
+    msg = L.moe_last_error()
+    assert status in (INVALID, UNSUP, WS)
+    for w in words:
+        assert w in msg, msg
+    return status
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(moments=2), b"moments"), (dict(count=0), b"count"),
+    (dict(count=-3), b"count"), (dict(step=None), b"step"),
+    (dict(step=4100), b"step"), (dict(lr=None), b"lr"), (dict(lr=4106), b"lr"),
+    (dict(b1=1.0), b"beta"), (dict(b1=-0.1), b"beta"),
+    (dict(b2=1.0), b"beta"), (dict(b2=float("nan")), b"beta"),
+    (dict(eps=0.0), b"eps"), (dict(eps=1e-30), b"eps"),
+    (dict(eps=2.0), b"eps"), (dict(eps=float("nan")), b"eps"),
+    (dict(norm=4114), b"grad_norm"), (dict(norm=NORM, max_norm=0.0), b"max"),
+    (dict(norm=NORM, max_norm=float("inf")), b"max"),
+    (dict(norm=NORM, max_norm=float("nan")), b"max")])
+def test_adamw_refuses_arguments(kw, word):
+    assert refused(call([adamw_tensor()], **kw), word) == INVALID
+
+
+@pytest.mark.parametrize("kw,moments,want", [
+    (dict(p=None), 0, INVALID), (dict(g=None), 0, INVALID),
+    (dict(m=None), 0, INVALID), (dict(v=None), 0, INVALID),
+    (dict(p=A + 8), 0, INVALID), (dict(g=A + 4), 0, INVALID),
+    (dict(m=A + 2), 0, INVALID), (dict(v=A + 1), 0, INVALID),
+    (dict(master=A + 4), 0, INVALID), (dict(n=-1), 0, INVALID),
+    (dict(n=(1 << 34) + 1), 0, UNSUP),
+    (dict(p_fp32=1, master=A + (5 << 18)), 0, INVALID),
+    (dict(m_scale=A + (6 << 18)), 0, INVALID),
+    (dict(), 1, INVALID),                       # no scales
+    (dict(m_scale=A + (6 << 18)), 1, INVALID),
+    (dict(weight_decay=-0.1), 0, INVALID),
+    (dict(weight_decay=float("nan")), 0, INVALID),
+    (dict(weight_decay=float("inf")), 0, INVALID)])
+def test_adamw_refuses_tensors(kw, moments, want):
+    """The faulty tensor is named, wherever it stands."""
+    good = adamw_tensor(1)
+    if moments:
+        good.m_scale, good.v_scale = good.p + (6 << 18), good.p + (7 << 18)
+    bad = adamw_tensor(0, **kw)
+    assert refused(call([good, bad], moments), b"tensor 1") == want
+
+
+def test_adamw_refuses_overlaps():
+    a, b = adamw_tensor(0), adamw_tensor(1)
+    same = lambda **kw: call([a, adamw_tensor(1, **kw)])  # noqa: E731
+    for kw in (dict(p=a.p), dict(m=a.m), dict(v=a.p + 16), dict(p=a.g),
+               dict(g=a.p), dict(g=a.v + 3984), dict(m=b.p),
+               dict(master=b.p), dict(p=a.p + 1984)):
+        assert refused(same(**kw), b"overlaps") == INVALID, kw
+    assert refused(call([a, a]), b"overlaps") == INVALID
+    # step, lr and the norm are read while the tensors are written
+    for k, at in (("step", a.p), ("lr", a.p + 1996), ("norm", a.v + 8)):
+        assert refused(call([a], **{k: at}), b"overlaps") == INVALID
+    # many tensors: the table's checks use the heap
+    many = [adamw_tensor(i) for i in range(200)]
+    many[150].m = many[20].v
+    assert refused(call(many), b"20", b"150", b"overlaps") == INVALID
+    # in 8 bits the scales are written, one for 256 values
+    c = adamw_tensor(2, n=1000, m_scale=a.p, v_scale=a.p + 16)
+    assert refused(call([adamw_tensor(0, m_scale=A + (6 << 18),
+                                      v_scale=A + (7 << 18)), c], 1),
+                   b"overlaps") == INVALID
+
+
+def norm_call(grads, count=None, norm=NORM, ws=WSP, nbytes=8192):
+    arr = (moe.Grad * max(1, len(grads)))(*grads)
+    return L.moe_grad_norm(ctypes.addressof(arr),
+                           len(grads) if count is None else count, norm, ws,
+                           nbytes, None)
+
+
+def test_grad_norm_refuses():
+    G = moe.Grad
+    ok = G(g=A, n=100)
+    assert refused(norm_call([ok], count=0), b"count") == INVALID
+    assert refused(norm_call([ok], norm=None), b"norm") == INVALID
+    assert refused(norm_call([ok], norm=4114), b"norm") == INVALID
+    assert refused(norm_call([ok], ws=None), b"workspace") == INVALID
+    assert refused(norm_call([ok], ws=8200), b"workspace") == INVALID
+    assert refused(norm_call([ok], nbytes=8191), b"workspace") == WS
+    assert refused(norm_call([ok, G(g=None, n=1)]), b"tensor 1") == INVALID
+    assert refused(norm_call([ok, G(g=A + 8, n=1)]), b"tensor 1") == INVALID
+    assert refused(norm_call([ok, G(g=A, n=-1)]), b"tensor 1") == INVALID
+    assert refused(norm_call([G(g=A, n=(1 << 34) + 1)]), b"2^34") == UNSUP
+    assert refused(norm_call([ok], norm=A + 40), b"overlaps") == INVALID
+    assert refused(norm_call([ok], norm=WSP), b"overlaps") == INVALID
+    assert refused(norm_call([G(g=WSP + 16, n=1)]), b"overlaps") == INVALID
+    assert L.moe_grad_norm(None, 1, NORM, WSP, 8192, None) == INVALID
+    assert L.moe_adamw(0, None, 1, STEP, LR, 0.9, 0.95, 1e-8, None, 1.0,
+                       None) == INVALID
+
+
+def test_grad_norm_workspace_depends_on_nothing():
+    n = moe.moe_workspace_bytes(moe.MOE_ENTRY_GRAD_NORM, 0, 0, 0, 0, 0, 0)
+    assert n == 8192 == moe.moe_workspace_bytes(
+        moe.MOE_ENTRY_GRAD_NORM, 0, 1 << 30, 64, 8, 2048, 1408)
+
+
+# ----------------------------------------------------------- the oracle
+def test_dither_averages_out():
+    """Over the steps the cut value's mean is the value: a moment that moves
+    by a hundredth of a code a step follows, where nearest rounding would
+    hold it."""
+    x = np.full(256, 1.0, np.float32)
+    x[1:] = np.linspace(0.01, 0.99, 255, dtype=np.float32)
+    got = np.zeros(256)
+    steps = 4000
+    for t in range(1, steps + 1):
+        c, s = R.quantize8(x, t, True)
+        got += mx_ref.e4m3_decode(c) * s[0]
+    got /= steps
+    # above the subnormal codes (2^-6 of 256) the mean is within the
+    # discrepancy of 4000 multiples of the golden ratio (below 10 / 4000) of a
+    # code, at most an eighth of the value
+    big = x * 256 > 2.0 ** -6
+    assert np.all(np.abs(got - x)[big] <= x[big] / 8 * 10 / steps + 1e-6)
+
+
+def test_quantize8_by_hand():
+    x = np.zeros(300, np.float32)
+    x[0], x[1], x[2], x[299] = 2.0, -1.0625, 2e-9, 1e-31
+    # t = 0 adds nothing: values are cut towards zero
+    c, s = R.quantize8(x, 0, False)
+    v = mx_ref.e4m3_decode(c)
+    assert s.tolist() == [2.0 / 256, 0.0]
+    assert (v[0], v[1], v[2], v[299]) == (256.0, -128.0, 0.0, 0.0)
+    r, s = R.quantize8(np.abs(x), 0, True)
+    assert mx_ref.e4m3_decode(r)[2] == 2.0 ** -9 and s[1] == 0.0
+    # half of the last bit or more is carried: 0x9E3779B1 >> 12 is 0.618 of it
+    assert R.dither(1) == 0x9E377
+    c, _ = R.quantize8(x, 1, False)
+    assert mx_ref.e4m3_decode(c)[1] == -144.0
+
+
+def test_adamw_oracle_by_hand():
+    """First step: both corrections cancel the moments' factors, so p moves
+    by lr g / (|g| + eps) and by lr wd p."""
+    g, p = np.array([0.5, -2.0, 0.0]), np.array([1.0, 1.0, 1.0])
+    m, v = R.moments(np.zeros(3), np.zeros(3), g, 0.9, 0.95)
+    q = R.parameter(p, m, np.sqrt(v), 1, 0.1, 0.9, 0.95, 1e-8, 0.01)
+    assert np.allclose(q, p - 0.1 * 0.01 * p - 0.1 * np.sign(g), atol=1e-7)
+    assert R.grad_norm([np.array([3.0]), np.array([0.0, 4.0])]) == 5.0
+    assert R.clip_factor(5.0, 1.0) == 1.0 / (5.0 + 1e-6)
+    assert R.clip_factor(0.5, 1.0) == 1.0
