@@ -762,9 +762,11 @@ typedef struct moe_adamw_tensor {
  * included.  Gradients are finite, g'^2 too, unless grad_norm leaves the step
  * out; the fp32 arithmetic of p uses the hardware reciprocal.
  * count >= 1, 0 <= n <= 2^34 each (MOE_ERR_UNSUPPORTED above), 0 <= beta < 1,
- * 1e-20 <= eps <= 1, max_norm > 0 with grad_norm.  Tensors 16-byte aligned,
- * step, lr and grad_norm aligned to their own size; what is written overlaps nothing else of the call
- * (MOE_ERR_INVALID_ARG), gradients may overlap each other.  No workspace.
+ * 1e-20 <= eps <= 1, max_norm > 0 with grad_norm.  Tensors are 16-byte
+ * aligned, scales, step, lr and grad_norm to their own size (the scales of
+ * tensors held in one buffer may follow each other).  What is written
+ * overlaps nothing else of the call (MOE_ERR_INVALID_ARG); gradients may
+ * overlap each other.  No workspace.
  */
 moe_status moe_adamw(moe_moments moments, const moe_adamw_tensor* tensors,
                      int32_t count, const int64_t* step, const float* lr,

@@ -427,8 +427,12 @@ moe_status check_adamw_tensor(int i, const moe_adamw_tensor& t, bool fp8) {
     if (moe_status st = check_member(i, "master", t.master)) return st;
   }
   if (fp8) {
-    if (moe_status st = check_member(i, "m_scale", t.m_scale)) return st;
-    if (moe_status st = check_member(i, "v_scale", t.v_scale)) return st;
+    REQUIRE(t.m_scale && t.v_scale, MOE_ERR_INVALID_ARG,
+            "tensor %d: m_scale and v_scale are required", i);
+    REQUIRE((reinterpret_cast<uintptr_t>(t.m_scale) |
+             reinterpret_cast<uintptr_t>(t.v_scale)) % 4 == 0,
+            MOE_ERR_INVALID_ARG,
+            "tensor %d: m_scale or v_scale is not 4-byte aligned", i);
   } else {
     REQUIRE(!t.m_scale && !t.v_scale, MOE_ERR_INVALID_ARG,
             "tensor %d: fp32 moments take no scales", i);

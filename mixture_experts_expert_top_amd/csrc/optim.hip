@@ -142,10 +142,12 @@ __device__ __forceinline__ int find_tensor(const uint32_t* first, int count,
 // and the clip factor then depends on no order of summation.
 constexpr int kNormTensors = 160;
 constexpr int kNormGroups = 1024;
+constexpr int kNormBytes = kThreads * 32;       // a chunk: 32 bytes a thread
+constexpr int kNormAhead = 2;                   // chunks in flight
 
 struct NormTable {
   const void* g[kNormTensors];
-  int64_t n[kNormTensors];
+  int64_t bytes[kNormTensors];
   uint32_t first[kNormTensors];       // first chunk
   uint8_t fp32[kNormTensors];
   int count;
@@ -160,31 +162,60 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ double sum8(const T* g, int64_t left) {
-  float v[kVec];
-  load_some(g, left, v);
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const double x = v[i];
-    s = fma(x, x, s);
-  }
-  return s;
+__device__ __forceinline__ double square_add(float v, double s) {
+  const double x = v;
+  return fma(x, x, s);
 }
 
+// Chunks are counted in bytes, so that what is in flight does not depend on a
+// tensor's type; a resource that ends with the tensor zeroes what lies past
+// it.
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(
     NormTable P, double* __restrict__ part) {
   __shared__ double red[kThreads / kWave];
   double s = 0.0;
-  for (uint32_t c = blockIdx.x; c < P.chunks; c += gridDim.x) {
-    const int i = find_tensor(P.first, P.count, c);
-    const int64_t at = static_cast<int64_t>(c - P.first[i]) * kChunk +
-                       threadIdx.x * kVec;
-    const int64_t left = P.n[i] - at;
-    if (left <= 0) continue;
-    s += P.fp32[i] ? sum8(static_cast<const float*>(P.g[i]) + at, left)
-                   : sum8(static_cast<const bf16_t*>(P.g[i]) + at, left);
+  for (uint32_t c = blockIdx.x; c < P.chunks; c += kNormAhead * gridDim.x) {
+    i32x4 raw[kNormAhead][2];
+    bool fp32[kNormAhead];
+#pragma unroll
+    for (int u = 0; u < kNormAhead; ++u) {
+      const uint32_t cu = c + u * gridDim.x;
+      const bool in = cu < P.chunks;
+      const int i = in ? find_tensor(P.first, P.count, cu) : 0;
+      const int64_t at =
+          in ? static_cast<int64_t>(cu - P.first[i]) * kNormBytes : 0;
+      const int64_t left = in ? P.bytes[i] - at : 0;
+      const uint32_t bytes =
+          left < kNormBytes ? static_cast<uint32_t>(left) : kNormBytes;
+      // an odd number of bf16 values: the last one's word is read whole and
+      // its upper half cleared
+      const auto rs = make_rsrc(static_cast<const char*>(P.g[i]) + at,
+                                (bytes + 3) & ~3u);
+      fp32[u] = P.fp32[i] != 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t off = (h * kThreads + threadIdx.x) * 16;
+        raw[u][h] = buf_load16(rs, off);
+        if (bytes & 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (off + q * 4 + 2 == bytes) raw[u][h][q] &= 0xffff;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kNormAhead; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t w = static_cast<uint32_t>(raw[u][h][q]);
+          if (fp32[u]) {
+            s = square_add(__uint_as_float(w), s);
+          } else {
+            s = square_add(bf_lo(w), s);
+            s = square_add(bf_hi(w), s);
+          }
+        }
   }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -382,10 +413,17 @@ size_t grad_norm_workspace() { return kNormGroups * sizeof(double); }
 hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
                             void* ws, hipStream_t s) {
   double* part = static_cast<double*>(ws);
+  const auto bytes = [&](int i) {
+    return grads[i].n * (grads[i].g_fp32 ? 4 : 2);
+  };
+  const auto chunks_of = [&](int i) {
+    return (bytes(i) + kNormBytes - 1) / kNormBytes;
+  };
   int64_t all = 0;
-  for (int i = 0; i < count; ++i) all += (grads[i].n + kChunk - 1) / kChunk;
+  for (int i = 0; i < count; ++i) all += chunks_of(i);
   const int groups = static_cast<int>(
       all < 1 ? 1 : all < kNormGroups ? all : kNormGroups);
+  // each launch adds to what the ones before it left
   int i = 0;
   bool first = true;
   do {
@@ -393,11 +431,12 @@ hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
     int64_t chunks = 0;
     for (; i < count && P.count < kNormTensors; ++i) {
       if (grads[i].n == 0) continue;
-      const int64_t c = (grads[i].n + kChunk - 1) / kChunk;
-      if (chunks + c > 0xffffffff) break;
+      const int64_t c = chunks_of(i);
+      // chunk numbers, also those past the end that a group asks for
+      if (chunks + c > 0xffffffff - kNormAhead * kNormGroups) break;
       const int q = P.count++;
       P.g[q] = grads[i].g;
-      P.n[q] = grads[i].n;
+      P.bytes[q] = bytes(i);
       P.fp32[q] = grads[i].g_fp32 != 0;
       P.first[q] = static_cast<uint32_t>(chunks);
       chunks += c;

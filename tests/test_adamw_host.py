@@ -68,6 +68,8 @@ def test_adamw_refuses_arguments(kw, word):
     (dict(m_scale=A + (6 << 18)), 0, INVALID),
     (dict(), 1, INVALID),                       # no scales
     (dict(m_scale=A + (6 << 18)), 1, INVALID),
+    (dict(m_scale=A + (6 << 18), v_scale=A + (7 << 18) + 2), 1, INVALID),
+    (dict(m_scale=A + (6 << 18) + 1, v_scale=A + (7 << 18)), 1, INVALID),
     (dict(weight_decay=-0.1), 0, INVALID),
     (dict(weight_decay=float("nan")), 0, INVALID),
     (dict(weight_decay=float("inf")), 0, INVALID)])
