@@ -751,8 +751,8 @@ typedef struct moe_adamw_tensor {
  * MOE_MOMENTS_FP8: code q of value i stands for q * scale[i / 256].  The
  *   moments are updated in fp32, every operation rounded by itself, from
  *   m = q_m s_m and r = q_v s_v, v = r^2; r' = sqrt(beta2 r^2 +
- *   (1 - beta2) g'^2) is held in place of v and also used as it is for p.  A
- *   block's scale is its largest |m| or r over 256 (0, with codes 0, where
+ *   (1 - beta2) g'^2) (0 where the sum is below 2^-96) is held in place of v
+ *   and also used as it is for p.  A block's scale is its largest |m| or r over 256 (0, with codes 0, where
  *   that is below 1e-30); a value over its scale, y, is given u 2^-20ths of
  *   its fourth significant bit (u = (t * 0x9E3779B1 mod 2^32) >> 12, in the
  *   bits of the fp32 value), cut to four significant bits, and rounded to
@@ -762,7 +762,7 @@ typedef struct moe_adamw_tensor {
  * included.  Gradients are finite, g'^2 too, unless grad_norm leaves the step
  * out; the fp32 arithmetic of p uses the hardware reciprocal.
  * count >= 1, 0 <= n <= 2^34 each (MOE_ERR_UNSUPPORTED above), 0 <= beta < 1,
- * 1e-20 <= eps <= 1, max_norm > 0 with grad_norm.  Tensors are 16-byte
+ * 1e-20 <= eps <= 1 (FP8: 1e-12 <= eps), max_norm > 0 with grad_norm.  Tensors are 16-byte
  * aligned, scales, step, lr and grad_norm to their own size (the scales of
  * tensors held in one buffer may follow each other).  What is written
  * overlaps nothing else of the call (MOE_ERR_INVALID_ARG); gradients may

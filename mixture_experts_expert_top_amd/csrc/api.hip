@@ -1555,8 +1555,10 @@ moe_status moe_adamw(moe_moments moments, const moe_adamw_tensor* tensors,
   if (moe_status st = check_scalar("lr", lr, 4)) return st;
   REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0,
           MOE_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  REQUIRE(eps >= 1e-20 && eps <= 1.0, MOE_ERR_INVALID_ARG,
-          "eps must be in [1e-20, 1]");
+  // roots of 8-bit second moments below 2^-48 read as 0: eps stands above
+  const double least = moments == MOE_MOMENTS_FP8 ? 1e-12 : 1e-20;
+  REQUIRE(eps >= least && eps <= 1.0, MOE_ERR_INVALID_ARG,
+          "eps must be in [%g, 1]", least);
   if (grad_norm) {
     if (moe_status st = check_scalar("grad_norm", grad_norm, 4)) return st;
     REQUIRE(max_norm > 0.0 && max_norm <= 3.4e38, MOE_ERR_INVALID_ARG,

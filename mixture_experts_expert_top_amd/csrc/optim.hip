@@ -25,6 +25,8 @@
 
 #include "optim.h"
 
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace moe {
@@ -43,8 +45,17 @@ constexpr int kThreads = 256;
 // gradients): fp32 moments and copies 2814 us with R = 4, 3094 with R = 8, and
 // 2915 with R = 8 and ordinary accesses; 8-bit moments 1605, 1329 and 1398.
 constexpr int kVec = 8;
-constexpr int kChunk = kThreads * kVec;         // values a workgroup
+constexpr int kChunk = kThreads * kVec;         // values a workgroup and pass
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+// Passes a workgroup of the 8-bit form, which the vector units bound (75
+// instructions a value with one pass, 53 with eight: what all values share,
+// the corrections' exponentials among it, is computed once a workgroup): as
+// many as leave the CUs 16 rounds of workgroups, up to eight.  554 M values
+// 1332 -> 1210 us with the norm; 45 M, where eight passes would leave 11
+// workgroups a CU, 143 us with one and 163 with eight.  The fp32 form is bound
+// by memory and stays at one (2820 us for 2986).
+constexpr int kMostPasses = 8;
+constexpr int64_t kRoundsChunks = int64_t{16} * 256 * 8;
 
 // first value of the thread in its chunk
 template <int R>
@@ -305,6 +316,7 @@ struct AdamwTable {
   float decay[kTensors];
   uint8_t p_fp32[kTensors], g_fp32[kTensors];
   int count;
+  int passes;
   AdamwHyper h;
 };
 static_assert(sizeof(AdamwTable) <= 4096, "kernel arguments");
@@ -326,6 +338,16 @@ __device__ __forceinline__ float one_minus_power(double log_b, int64_t t) {
 // a moment, cut to what E4M3 holds: `y` in units of the block's scale
 __device__ __forceinline__ float cut(float y, uint32_t dither) {
   return __uint_as_float((__float_as_uint(y) + dither) & ~0xfffffu);
+}
+
+// The correctly rounded root of x >= 2^-96, by the last step of Newton's
+// method on a root and half its reciprocal (each good to about an ulp) with
+// the residual x - s^2 exact: five instructions where the library's root for
+// every float takes 14.  Equal to it on every float of [2^-96, 2^100).
+__device__ __forceinline__ float root(float x) {
+  const float y = __builtin_amdgcn_rsqf(x);
+  const float s = x * y;
+  return fmaf(fmaf(-s, s, x), 0.5f * y, s);
 }
 
 // The largest of 32 lanes' values, in each of them.
@@ -368,7 +390,8 @@ __device__ __forceinline__ void update(const AdamwTable& P, int i, int64_t at,
     for (int q = 0; q < kVec; ++q) {
       m[q] = m[q] * sm * S.b1 + g[q] * S.c1;
       const float ro = r[q] * sv;
-      r[q] = sqrtf(ro * ro * S.b2 + g[q] * g[q] * S.c2);
+      const float v = ro * ro * S.b2 + g[q] * g[q] * S.c2;
+      r[q] = v >= 0x1p-96f ? root(v) : 0.0f;
       tm = fmaxf(tm, fabsf(m[q]));
       tr = fmaxf(tr, r[q]);
     }
@@ -435,22 +458,26 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamwTable P) {
   S.root = 1.0f / sqrtf(one_minus_power(P.h.log_b2, t));
   S.dither = (static_cast<uint32_t>(t) * 0x9e3779b1u) >> 12;
   const int i = find_tensor(P.first, P.count, blockIdx.x);
-  const int64_t at = static_cast<int64_t>(blockIdx.x - P.first[i]) * kChunk;
-  if (P.p_fp32[i]) {
-    if (P.g_fp32[i])
-      update<kBits8, float, false, float>(P, i, at, S);
-    else
-      update<kBits8, float, false, bf16_t>(P, i, at, S);
-  } else if (P.master[i]) {
-    if (P.g_fp32[i])
-      update<kBits8, bf16_t, true, float>(P, i, at, S);
-    else
-      update<kBits8, bf16_t, true, bf16_t>(P, i, at, S);
-  } else {
-    if (P.g_fp32[i])
-      update<kBits8, bf16_t, false, float>(P, i, at, S);
-    else
-      update<kBits8, bf16_t, false, bf16_t>(P, i, at, S);
+  const int64_t chunk = static_cast<int64_t>(P.passes) * kChunk;
+  int64_t at = (blockIdx.x - P.first[i]) * chunk;
+  const int64_t end = min(at + chunk, P.n[i]);
+  for (; at < end; at += kChunk) {
+    if (P.p_fp32[i]) {
+      if (P.g_fp32[i])
+        update<kBits8, float, false, float>(P, i, at, S);
+      else
+        update<kBits8, float, false, bf16_t>(P, i, at, S);
+    } else if (P.master[i]) {
+      if (P.g_fp32[i])
+        update<kBits8, bf16_t, true, float>(P, i, at, S);
+      else
+        update<kBits8, bf16_t, true, bf16_t>(P, i, at, S);
+    } else {
+      if (P.g_fp32[i])
+        update<kBits8, bf16_t, false, float>(P, i, at, S);
+      else
+        update<kBits8, bf16_t, false, bf16_t>(P, i, at, S);
+    }
   }
 }
 
@@ -504,14 +531,23 @@ hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
 
 hipError_t launch_adamw(bool bits8, const moe_adamw_tensor* t, int count,
                         const AdamwHyper& h, hipStream_t s) {
+  int64_t all = 0;
+  for (int i = 0; i < count; ++i) all += t[i].n;
+  const int passes = static_cast<int>(
+      bits8 ? std::max<int64_t>(1, std::min<int64_t>(
+                                       kMostPasses,
+                                       all / kChunk / kRoundsChunks))
+            : 1);
+  const int64_t chunk = static_cast<int64_t>(passes) * kChunk;
   int i = 0;
   while (i < count) {
     AdamwTable P{};
     P.h = h;
+    P.passes = passes;
     int64_t chunks = 0;
     for (; i < count && P.count < kTensors; ++i) {
       if (t[i].n == 0) continue;
-      const int64_t c = (t[i].n + kChunk - 1) / kChunk;
+      const int64_t c = (t[i].n + chunk - 1) / chunk;
       if (chunks + c > kMaxGroups) break;
       const int q = P.count++;
       P.p[q] = t[i].p;

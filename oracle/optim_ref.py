@@ -46,7 +46,8 @@ def moments8(qm, sm, qr, sr, g, b1, b2):
     m = mx_ref.e4m3_decode(qm).astype(F) * np.repeat(sm, BLOCK)[:n]
     r = mx_ref.e4m3_decode(qr).astype(F) * np.repeat(sr, BLOCK)[:n]
     m = m * b1f + g * c1f
-    r = np.sqrt(r * r * b2f + g * g * c2f)
+    v = r * r * b2f + g * g * c2f
+    r = np.where(v >= F(2.0 ** -96), np.sqrt(v), F(0.0))
     return m, r
 
 

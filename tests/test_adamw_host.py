@@ -49,7 +49,7 @@ def refused(status, *words):
     (dict(b1=1.0), b"beta"), (dict(b1=-0.1), b"beta"),
     (dict(b2=1.0), b"beta"), (dict(b2=float("nan")), b"beta"),
     (dict(eps=0.0), b"eps"), (dict(eps=1e-30), b"eps"),
-    (dict(eps=2.0), b"eps"), (dict(eps=float("nan")), b"eps"),
+    (dict(eps=1e-13, moments=1), b"eps"), (dict(eps=2.0), b"eps"), (dict(eps=float("nan")), b"eps"),
     (dict(norm=4114), b"grad_norm"), (dict(norm=NORM, max_norm=0.0), b"max"),
     (dict(norm=NORM, max_norm=float("inf")), b"max"),
     (dict(norm=NORM, max_norm=float("nan")), b"max")])

@@ -291,6 +291,7 @@ def test_blocks_of_zeros_and_of_tiny_values():
     g[256:512] = 1e-32            # m = 1e-33, and its square vanishes
     g[512:768] = 1e-9
     g[600] = 1.0
+    g[768:1024] = 1e-15           # (1 - beta2) g^2 is below 2^-96
     t["g"] = g
     old = _before([t])[0]
     step, lr = _scalars(1)
@@ -298,6 +299,7 @@ def test_blocks_of_zeros_and_of_tiny_values():
     _check(t, old, 1, 1.0, float(lr.double()))
     assert float(t["m_scale"][1]) == 0.0 and not _bits(t["m"])[:512].any()
     assert (_bits(t["v"])[512:768] >= 1).all()
+    assert not _bits(t["v"])[768:].any() and _bits(t["m"])[768:].all()
     assert torch.isfinite(t["p"]).all()
 
 
