@@ -2,7 +2,8 @@
  * moe.h -- C-ABI of libmoe.so: the mixture-of-experts expert-MLP hot path
  * (top-k routing, permutation by expert, grouped GEMM with fused SwiGLU and
  * routing-weight scaling, optional MXFP8 block quantization, un-permute
- * combine; forward and backward), the residual block around it (norm,
+ * combine; forward and backward), the same layer for few tokens in one call
+ * (serving), the residual block around it (norm,
  * dense gated feed-forward block, dropout) and the optimizer step that uses
  * its gradients (gradient norm, AdamW) as hand-written HIP kernels for
  * gfx950.
@@ -87,7 +88,8 @@ typedef enum moe_entry {
   MOE_ENTRY_NORM_BWD = 4,
   MOE_ENTRY_FFN_FWD = 5,
   MOE_ENTRY_FFN_BWD = 6,
-  MOE_ENTRY_GRAD_NORM = 7
+  MOE_ENTRY_GRAD_NORM = 7,
+  MOE_ENTRY_LAYER_FWD = 8
 } moe_entry;
 
 /* Gate activation of moe_ffn_fwd and moe_ffn_bwd. */
@@ -683,6 +685,48 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
                        const void* dx_add, int64_t T, int64_t d, int64_t f,
                        void* dx, void* dw_gu, void* dw2, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
+
+/* Most tokens of a moe_layer_fwd call. */
+#define MOE_LAYER_MAX_TOKENS 64
+
+/*
+ * moe_layer_fwd -- the whole expert layer for few tokens (generation, the
+ * end of a prompt) without a dispatch plan: the router of moe_router_logits
+ * and moe_route, the experts of moe_grouped_mlp_fwd and the combine of
+ * moe_unpermute in one call that reads the weights of the experts it
+ * reaches once.
+ *   z[t] = x[t] . w_g^T (+ bias)            (or logits[t])
+ *   topk_idx[t], topk_w[t]: as moe_route chooses from z[t]
+ *   S[t][j] = topk_w[t][j] * silu(x[t] . G^T) * (x[t] . U^T), e =
+ *     topk_idx[t][j], G = w_gu[e][:f], U = w_gu[e][f:]
+ *   y[t]  = y_add[t] + sum_j S[t][j] . w2[e]^T     (y_add NULL: zero)
+ *   x [T][d] bf16; w_g [E][d] bf16 with bias [E] fp32 (or NULL), or both NULL
+ *   and logits [T][E] fp32; y_add (or NULL) and y [T][d] bf16; topk_idx
+ *   int32, topk_w fp32 [T][k] out.
+ * prec == MOE_BF16: w_gu [E][2f][d], w2 [E][d][f] bf16, scales NULL; d and f
+ *   multiples of 8.
+ * prec == MOE_MXFP8: w_gu and w2 are E4M3 codes with E8M0 scales along
+ *   their last axis (moe_mxfp8_quantize axis 0, as moe_grouped_mlp_fwd takes
+ *   them); x and S stay bf16 here, so y differs from that entry's by its
+ *   quantization of both.  d and f multiples of 128.  A scale byte of 0
+ *   stands for 0 or 2^-127.
+ * prec == MOE_MXFP4: MOE_ERR_UNSUPPORTED.
+ * Sums are fp32 in a fixed order, S is rounded to bf16 for the second
+ * product, y is rounded once.  A token's bits may differ between calls of
+ * different tokens around it.  y may be y_add itself; otherwise outputs and
+ * the workspace overlap neither inputs nor each other.  1 <= T <=
+ * MOE_LAYER_MAX_TOKENS, E, k and the size of an expert's weight as
+ * moe_grouped_mlp_fwd.  Workspace: MOE_ENTRY_LAYER_FWD.
+ */
+moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
+                         const float* bias, const float* logits, int64_t T,
+                         int64_t d, int64_t f, int32_t E, int32_t k,
+                         int32_t renorm, const void* w_gu,
+                         const uint8_t* w_gu_scales, const void* w2,
+                         const uint8_t* w2_scales, const void* y_add,
+                         int32_t* topk_idx, float* topk_w, void* y,
+                         void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
 
 /* One gradient of moe_grad_norm: n values at g (device memory), bf16 or
  * (g_fp32 != 0) fp32.  With n == 0 the pointer is not looked at. */

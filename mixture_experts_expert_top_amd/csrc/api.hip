@@ -12,6 +12,7 @@
 #include <new>
 
 #include "../../include/moe.h"
+#include "decode.h"
 #include "internal.h"
 #include "optim.h"
 
@@ -550,6 +551,9 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       if (f < 1 || d < 1) return 0;
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
       return mx_bwd_layout(Tk, E, d, f, mx_bwd_base(Tk, f)).total;
+    case MOE_ENTRY_LAYER_FWD:
+      if (T > moe::kFewTokens || k > moe::kMaxTopK || d < 1 || f < 1) return 0;
+      return moe::layer_fwd_workspace(T, E, k, f);
     default:
       break;
   }
@@ -1513,6 +1517,93 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
           static_cast<bf16_t*>(dx), static_cast<bf16_t*>(dw_gu),
           static_cast<bf16_t*>(dw2), workspace, stream),
       "moe_ffn_bwd");
+}
+
+moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
+                         const float* bias, const float* logits, int64_t T,
+                         int64_t d, int64_t f, int32_t E, int32_t k,
+                         int32_t renorm, const void* w_gu,
+                         const uint8_t* w_gu_scales, const void* w2,
+                         const uint8_t* w2_scales, const void* y_add,
+                         int32_t* topk_idx, float* topk_w, void* y,
+                         void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+  if (moe_status st = check_prec(prec)) return st;
+  REQUIRE(prec != MOE_MXFP4, MOE_ERR_UNSUPPORTED,
+          "moe_layer_fwd takes bf16 or MXFP8 weights");
+  const bool mx = prec == MOE_MXFP8;
+  REQUIRE_PTR(x);
+  REQUIRE_OPT_PTR(w_g);
+  REQUIRE_OPT_PTR(bias);
+  REQUIRE_OPT_PTR(logits);
+  REQUIRE((w_g != nullptr) != (logits != nullptr), MOE_ERR_INVALID_ARG,
+          "give either w_g or logits");
+  REQUIRE(w_g || !bias, MOE_ERR_INVALID_ARG, "bias given without w_g");
+  REQUIRE_PTR(w_gu);
+  REQUIRE_PTR(w2);
+  if (mx) {
+    REQUIRE_PTR(w_gu_scales);
+    REQUIRE_PTR(w2_scales);
+  } else {
+    REQUIRE(!w_gu_scales && !w2_scales, MOE_ERR_INVALID_ARG,
+            "bf16 weights take no scales");
+  }
+  REQUIRE_OPT_PTR(y_add);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(y);
+  if (moe_status st = check_route_dims(T, E, k)) return st;
+  REQUIRE(T <= moe::kFewTokens, MOE_ERR_UNSUPPORTED,
+          "T must be at most %d (got %lld)", moe::kFewTokens,
+          static_cast<long long>(T));
+  if (moe_status st = check_mlp_dims(E, T * k, d, f, prec)) return st;
+  if (mx)
+    if (moe_status st = check_mx_dims(d, f)) return st;
+  REQUIRE(d <= (int64_t{1} << 20) && f <= (int64_t{1} << 20),
+          MOE_ERR_UNSUPPORTED, "d and f must be at most 2^20");
+  REQUIRE(T * k * f * 2 <= kMaxRange, MOE_ERR_UNSUPPORTED,
+          "T * k * f is too large");
+  const size_t need = moe::layer_fwd_workspace(T, E, k, f);
+  REQUIRE_PTR(workspace);
+  REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE,
+          "workspace too small: %zu < %zu", workspace_bytes, need);
+  const int64_t n = T * d * 2, w = static_cast<int64_t>(E) * d * f;
+  const Range outs[] = {
+      {"y", y, n},
+      {"topk_idx", topk_idx, T * k * 4},
+      {"topk_w", topk_w, T * k * 4},
+      {"workspace", workspace, static_cast<int64_t>(need)}};
+  const Range ins[] = {{"x", x, n},
+                       {"w_g", w_g, E * d * 2},
+                       {"bias", bias, E * int64_t{4}},
+                       {"logits", logits, T * E * 4},
+                       {"w_gu", w_gu, 2 * w * (mx ? 1 : 2)},
+                       {"w_gu_scales", w_gu_scales, 2 * w / 32},
+                       {"w2", w2, w * (mx ? 1 : 2)},
+                       {"w2_scales", w2_scales, w / 32},
+                       {"y_add", y_add == y ? nullptr : y_add, n}};
+  if (moe_status st = check_disjoint(outs, ins)) return st;
+  moe::LayerArgs a{};
+  a.x = static_cast<const bf16_t*>(x);
+  a.w_g = static_cast<const bf16_t*>(w_g);
+  a.bias = bias;
+  a.logits = logits;
+  a.T = static_cast<int>(T);
+  a.d = static_cast<int>(d);
+  a.f = static_cast<int>(f);
+  a.E = E;
+  a.k = k;
+  a.renorm = renorm;
+  a.w_gu = w_gu;
+  a.w_gu_scales = w_gu_scales;
+  a.w2 = w2;
+  a.w2_scales = w2_scales;
+  a.y_add = static_cast<const bf16_t*>(y_add);
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.y = static_cast<bf16_t*>(y);
+  return hip_status(moe::launch_layer_fwd(mx, a, workspace, stream),
+                    "moe_layer_fwd");
 }
 
 moe_status moe_grad_norm(const moe_grad* grads, int32_t count, float* norm,

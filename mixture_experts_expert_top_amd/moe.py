@@ -26,6 +26,8 @@ MOE_ENTRY_NORM_BWD = 4
 MOE_ENTRY_FFN_FWD = 5
 MOE_ENTRY_FFN_BWD = 6
 MOE_ENTRY_GRAD_NORM = 7
+MOE_ENTRY_LAYER_FWD = 8
+MOE_LAYER_MAX_TOKENS = 64
 MOE_MOMENTS_FP32 = 0
 MOE_MOMENTS_FP8 = 1
 MOE_ADAMW_BLOCK = 256
@@ -46,7 +48,7 @@ EXPORTED = [
     "moe_mx_down_swiglu_bwd", "moe_mx_gate_up_dgrad", "moe_mx_grouped_wgrad",
     "moe_router_backward", "moe_mxfp4_quantize", "moe_permute_noalloc",
     "moe_norm_fwd", "moe_norm_bwd", "moe_dropout", "moe_ffn_fwd",
-    "moe_ffn_bwd", "moe_grad_norm", "moe_adamw",
+    "moe_ffn_bwd", "moe_grad_norm", "moe_adamw", "moe_layer_fwd",
 ]
 # fixed per-GPU scratch of moe_permute_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 2 << 20
@@ -125,6 +127,8 @@ def _load():
                               P]),
         "moe_ffn_bwd": (I32, [I32, P, P, P, P, P, P, P, I64, I64, I64, P, P,
                               P, P, SZ, P]),
+        "moe_layer_fwd": (I32, [I32, P, P, P, P, I64, I64, I64, I32, I32, I32,
+                                P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_grad_norm": (I32, [P, I32, P, P, SZ, P]),
         "moe_adamw": (I32, [I32, P, I32, P, P, ctypes.c_double,
                             ctypes.c_double, ctypes.c_double, P,
@@ -678,7 +682,7 @@ def moe_mx_grouped_wgrad(aq, as_, bq, bs, offsets, Tk, c, stream=None,
 # which must be one of that GPU's) whichever device is current.
 
 _BF16, _F32 = torch.bfloat16, torch.float32
-_F8 = torch.float8_e4m3fn
+_F8, _U8, _I32 = torch.float8_e4m3fn, torch.uint8, torch.int32
 
 
 def _checked(name, specs):
@@ -832,6 +836,37 @@ def moe_ffn_bwd(act, dy, x, w_gu, w2, ab_saved, s_saved, dx_add, dx, dw_gu,
     _enqueue("moe_ffn_bwd", stream, dev, lib.moe_ffn_bwd, act, p[0], p[1],
              p[2], p[3], p[4], p[5], p[6], T, d, f, p[7], p[8],
              p[9], p[10], _nbytes(workspace))
+
+
+# --------------------------------------------------- few tokens (serving)
+
+def moe_layer_fwd(prec, x, w_g, bias, logits, k, renorm, w_gu, w_gu_scales,
+                  w2, w2_scales, y_add, topk_idx, topk_w, y, workspace,
+                  stream=None):
+    """The whole expert layer for up to MOE_LAYER_MAX_TOKENS tokens (see
+    include/moe.h): the router's w_g (and bias) or its logits; weights bf16,
+    or E4M3 codes with E8M0 scales (MOE_MXFP8); y = y_add + the layer's (y_add
+    may be None, and y may be y_add)."""
+    T, d = x.shape
+    E, two_f, _ = w_gu.shape
+    f = two_f // 2
+    if prec == MOE_BF16:
+        wt, sd, sf = _BF16, 0, 0
+    else:
+        wt, sd, sf = _U8, d // 32, f // 32
+    dev, p = _checked("moe_layer_fwd", (
+        ("x", x, _BF16, None), ("w_g", w_g, _BF16, (E, d)),
+        ("bias", bias, _F32, (E,)), ("logits", logits, _F32, (T, E)),
+        ("w_gu", w_gu, wt, (E, 2 * f, d)),
+        ("w_gu_scales", w_gu_scales, _U8, (E, 2 * f, sd)),
+        ("w2", w2, wt, (E, d, f)), ("w2_scales", w2_scales, _U8, (E, d, sf)),
+        ("y_add", y_add, _BF16, (T, d)),
+        ("topk_idx", topk_idx, _I32, (T, k)), ("topk_w", topk_w, _F32, (T, k)),
+        ("y", y, _BF16, (T, d)),
+        ("workspace", workspace, _dtype(workspace), None)))
+    _enqueue("moe_layer_fwd", stream, dev, lib.moe_layer_fwd, prec, p[0], p[1],
+             p[2], p[3], T, d, f, E, k, renorm, p[4], p[5], p[6], p[7], p[8],
+             p[9], p[10], p[11], p[12], _nbytes(workspace))
 
 
 # --------------------------------------------------------- optimizer step

@@ -1,0 +1,76 @@
+"""Host-side checks of moe_layer_fwd: what it refuses before anything is
+launched (fake device addresses), and its workspace."""
+
+import pytest
+
+from mixture_experts_expert_top_amd import moe
+
+L = moe.lib
+INVALID, UNSUP, WS = 1, 2, 3
+BASE = 1 << 32
+GOOD = dict(prec=0, x=BASE, w_g=BASE + (1 << 20), bias=None, logits=None, T=4,
+            d=256, f=128, E=8, k=2, renorm=1, w_gu=BASE + (2 << 20),
+            w_gu_s=None, w2=BASE + (6 << 20), w2_s=None, y_add=None,
+            idx=BASE + (9 << 20), w=BASE + (10 << 20), y=BASE + (11 << 20),
+            ws=BASE + (12 << 20), nbytes=1 << 20)
+
+
+def call(**kw):
+    a = {**GOOD, **kw}
+    st = L.moe_layer_fwd(*[a[n] for n in GOOD], None)
+    return st, L.moe_last_error()
+
+
+@pytest.mark.parametrize("kw,want,word", [
+    (dict(prec=2), UNSUP, b"MXFP8"), (dict(prec=7), INVALID, b"precision"),
+    (dict(x=None), INVALID, b"x"), (dict(x=BASE + 8), INVALID, b"x"),
+    (dict(w_g=None), INVALID, b"either"),
+    (dict(logits=BASE + (13 << 20)), INVALID, b"either"),
+    (dict(w_g=None, logits=BASE + (13 << 20), bias=BASE + (14 << 20)),
+     INVALID, b"bias"),
+    (dict(w_g=BASE + 4), INVALID, b"w_g"),
+    (dict(bias=BASE + 4), INVALID, b"bias"),
+    (dict(w_gu=None), INVALID, b"w_gu"), (dict(w2=None), INVALID, b"w2"),
+    (dict(w2=BASE + 2), INVALID, b"w2"),
+    (dict(w_gu_s=BASE + (13 << 20)), INVALID, b"scales"),
+    (dict(prec=1), INVALID, b"scales"),
+    (dict(prec=1, w_gu_s=BASE + (13 << 20)), INVALID, b"w2_scales"),
+    (dict(idx=None), INVALID, b"topk_idx"), (dict(w=None), INVALID, b"topk_w"),
+    (dict(y=None), INVALID, b"y"), (dict(y=BASE + 12), INVALID, b"y"),
+    (dict(y_add=BASE + 12), INVALID, b"y_add"),
+    (dict(T=0), INVALID, b"T"), (dict(T=65), UNSUP, b"64"),
+    (dict(E=0), INVALID, b"E"), (dict(E=1025), INVALID, b"E"),
+    (dict(k=0), INVALID, b"k"), (dict(k=9), INVALID, b"k"),
+    (dict(E=64, k=33), UNSUP, b"k"),
+    (dict(d=0), INVALID, b"d"), (dict(d=12), INVALID, b"d"),
+    (dict(f=4), INVALID, b"f"), (dict(f=129), INVALID, b"f"),
+    (dict(d=1 << 16, f=1 << 15), UNSUP, b"4 GiB"),
+    (dict(d=1 << 21, f=8), UNSUP, b"2^20"),
+    (dict(prec=1, w_gu_s=BASE + (13 << 20), w2_s=BASE + (14 << 20), d=160),
+     INVALID, b"128"),
+    (dict(ws=None), INVALID, b"workspace"),
+    (dict(ws=BASE + (12 << 20) + 8), INVALID, b"workspace"),
+    (dict(nbytes=100), WS, b"workspace"),
+    (dict(y=BASE), INVALID, b"overlaps"),
+    (dict(y=BASE + (9 << 20)), INVALID, b"overlaps"),
+    (dict(y_add=BASE + (11 << 20) + 16), INVALID, b"overlaps"),
+    (dict(ws=BASE + (2 << 20) + 1024), INVALID, b"overlaps"),
+    (dict(idx=BASE + (6 << 20)), INVALID, b"overlaps"),
+    (dict(w=BASE + (9 << 20) + 16), INVALID, b"overlaps"),
+    (dict(ws=BASE + (11 << 20) + 1024), INVALID, b"overlaps")])
+def test_refuses(kw, want, word):
+    st, msg = call(**kw)
+    assert st == want, msg
+    assert word in msg, msg
+
+
+def test_workspace():
+    """S, in bf16 for every slot; 0 for what no call takes."""
+    W = lambda **kw: moe.moe_workspace_bytes(*{**dict(  # noqa: E731
+        entry=moe.MOE_ENTRY_LAYER_FWD, prec=0, T=4, E=8, k=2, d=256, f=128),
+        **kw}.values())
+    assert W() >= 4 * 2 * 128 * 2
+    assert W(T=64) >= 64 * 2 * 128 * 2
+    for kw in (dict(T=65), dict(T=0), dict(k=9), dict(E=0), dict(E=2000),
+               dict(E=64, k=33), dict(d=0), dict(f=0), dict(prec=9)):
+        assert W(**kw) == 0, kw
