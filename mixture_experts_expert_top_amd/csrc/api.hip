@@ -553,7 +553,7 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       return mx_bwd_layout(Tk, E, d, f, mx_bwd_base(Tk, f)).total;
     case MOE_ENTRY_LAYER_FWD:
       if (T > moe::kFewTokens || k > moe::kMaxTopK || d < 1 || f < 1) return 0;
-      return moe::layer_fwd_workspace(T, E, k, f);
+      return moe::layer_fwd_workspace(T, k, E, d, f);
     default:
       break;
   }
@@ -1561,9 +1561,9 @@ moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
     if (moe_status st = check_mx_dims(d, f)) return st;
   REQUIRE(d <= (int64_t{1} << 20) && f <= (int64_t{1} << 20),
           MOE_ERR_UNSUPPORTED, "d and f must be at most 2^20");
-  REQUIRE(T * k * f * 2 <= kMaxRange, MOE_ERR_UNSUPPORTED,
+  REQUIRE(T * k * f * 4 <= kMaxRange, MOE_ERR_UNSUPPORTED,
           "T * k * f is too large");
-  const size_t need = moe::layer_fwd_workspace(T, E, k, f);
+  const size_t need = moe::layer_fwd_workspace(T, k, E, d, f);
   REQUIRE_PTR(workspace);
   REQUIRE(workspace_bytes >= need, MOE_ERR_WORKSPACE,
           "workspace too small: %zu < %zu", workspace_bytes, need);

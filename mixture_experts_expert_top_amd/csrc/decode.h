@@ -27,7 +27,7 @@ struct LayerArgs {
   uint16_t* y;
 };
 
-size_t layer_fwd_workspace(int64_t T, int E, int k, int64_t f);
+size_t layer_fwd_workspace(int64_t T, int k, int E, int64_t d, int64_t f);
 hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
                             hipStream_t s);
 

@@ -58,58 +58,98 @@ __global__ __launch_bounds__(kRouteThreads) void few_route_kernel(
     int E, int k, int renorm, int32_t* __restrict__ idx,
     float* __restrict__ wt) {
   __shared__ float s_z[kMaxExperts];
-  __shared__ uint32_t s_key[kMaxExperts];
+  __shared__ float s_part[kMaxExperts];      // [cut][E]: cuts * E <= 64, or E
+  __shared__ __attribute__((aligned(16))) uint32_t s_key[kMaxExperts];
+  __shared__ int s_place[kMaxExperts];
   __shared__ int s_idx[kMaxTopK];
   __shared__ float s_p[kMaxTopK];
   __shared__ float s_sum[kRouteWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t = blockIdx.x;
   if (w_g) {
+    // Groups of four experts go to the waves; where there are fewer groups
+    // than waves the reduction is cut into `cuts` too.  A wave has 4 x 512 k
+    // of its experts in flight.
+    const int groups = (E + 3) / 4;
+    int cuts = 1;
+    while (2 * cuts * groups <= kRouteWaves) cuts *= 2;
+    const int steps = (d + 511) / 512;
+    const int per = (steps + cuts - 1) / cuts;        // steps of a cut
     const auto rx = make_rsrc(x + static_cast<int64_t>(t) * d, d * 2);
-    // four experts a wave at a time
-    for (int e0 = wave * 4; e0 < E; e0 += kRouteWaves * 4) {
+    for (int item = wave; item < groups * cuts; item += kRouteWaves) {
+      const int cut = item / groups, e0 = (item - cut * groups) * 4;
       const int ne = min(4, E - e0);
       const auto rw = make_rsrc(w_g + static_cast<int64_t>(e0) * d,
                                 static_cast<uint32_t>(ne) * d * 2);
+      const int end = min(steps, (cut + 1) * per);
       float acc[4] = {};
-      for (int k0 = lane * 8; k0 < d; k0 += 512) {
-        const i32x4 xv = buf_load16(rx, k0 * 2);
-        i32x4 wv[4];
+      for (int s0 = cut * per; s0 < end; s0 += 4) {
+        i32x4 xv[4], wv[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          wv[i] = buf_load16(rw, i < ne ? (i * d + k0) * 2 : kOob);
+        for (int u = 0; u < 4; ++u) {
+          const int k0 = (s0 + u) * 512 + lane * 8;
+          const bool ok = s0 + u < end && k0 < d;
+          xv[u] = buf_load16(rx, ok ? k0 * 2 : kOob);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
+            wv[u][i] = buf_load16(rw, ok && i < ne ? (i * d + k0) * 2 : kOob);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t a = xv[q], b = wv[i][q];
-            acc[i] = fmaf(bf_lo(a), bf_lo(b), acc[i]);
-            acc[i] = fmaf(bf_hi(a), bf_hi(b), acc[i]);
-          }
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t a = xv[u][q], b = wv[u][i][q];
+              acc[i] = fmaf(bf_lo(a), bf_lo(b), acc[i]);
+              acc[i] = fmaf(bf_hi(a), bf_hi(b), acc[i]);
+            }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float z = wave_sum(acc[i]);
-        if (lane == 0 && i < ne)
-          s_z[e0 + i] = bias ? z + bias[e0 + i] : z;
+        if (lane == 0 && i < ne) s_part[cut * E + e0 + i] = z;
       }
+    }
+    __syncthreads();
+    if (tid < E) {
+      float z = s_part[tid];
+      for (int c = 1; c < cuts; ++c) z += s_part[c * E + tid];
+      s_z[tid] = bias ? z + bias[tid] : z;
     }
   } else if (tid < E) {
     s_z[tid] = logits[static_cast<int64_t>(t) * E + tid];
   }
   __syncthreads();
-  if (tid < E) s_key[tid] = score_key(s_z[tid]);
-  __syncthreads();
-  // an expert's place is the number of better ones
-  if (tid < E) {
-    const uint32_t key = s_key[tid];
-    int place = 0;
-    for (int e = 0; e < E; ++e) {
-      const uint32_t o = s_key[e];
-      place += o > key || (o == key && e < tid);
-    }
-    if (place < k) s_idx[place] = tid;
+  // An expert's place is the number of better ones.  The keys (padded to a
+  // multiple of four that nothing is worse than) are compared by `segs`
+  // threads an expert, each with its share of them.
+  const int E4 = (E + 3) & ~3;
+  if (tid < E4) {
+    s_key[tid] = tid < E ? score_key(s_z[tid]) : 0;
+    s_place[tid] = 0;
   }
+  __syncthreads();
+  int width = 64;
+  while (width < E) width *= 2;
+  const int me = tid & (width - 1), seg = tid / width;
+  if (me < E) {
+    const int fours = E4 / 4, segs = kRouteThreads / width;
+    const int per = (fours + segs - 1) / segs;
+    const uint32_t key = s_key[me];
+    int place = 0;
+    for (int q = seg * per; q < min(fours, (seg + 1) * per); ++q) {
+      const uint4 o = reinterpret_cast<const uint4*>(s_key)[q];
+      const uint32_t ok[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        place += ok[i] > key || (ok[i] == key && q * 4 + i < me);
+    }
+    if (place) atomicAdd(&s_place[me], place);
+  }
+  __syncthreads();
+  if (tid < E && s_place[tid] < k) s_idx[s_place[tid]] = tid;
   __syncthreads();
   const float top = s_z[s_idx[0]];
   if (tid < k) s_p[tid] = expf(s_z[s_idx[tid]] - top);
@@ -130,13 +170,39 @@ __global__ __launch_bounds__(kRouteThreads) void few_route_kernel(
 }
 
 // ---------------------------------------------------------------- weights
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kRows = 8;              // weight rows of a tile
-constexpr int kTok = 8;               // tokens of a block
 constexpr int kChunkK = 256;          // k a wave takes at a time
 
-// A wave's place in a tile: row or token lane & 7 of each, and first k.
+// Workgroups of the two products: four waves for a tile of gate and up (the
+// tiles are many, and small workgroups start and end independently); for a
+// tile of y, whose reduction is long, kDownThreads.
+constexpr int kUpThreads = 256;
+constexpr int kUpWaves = kUpThreads / kWave;
+
+struct FewParams {
+  const bf16_t* x;
+  const uint8_t* w_gu;
+  const uint8_t* w_gu_scales;
+  const uint8_t* w2;
+  const uint8_t* w2_scales;
+  const int32_t* idx;                 // [T][k]
+  const float* wt;
+  bf16_t* s;                          // [T k][2][f]: S in two parts
+  const bf16_t* y_add;
+  bf16_t* y;
+  float* part;                        // [part][T][d]
+  int T, d, f, E, k;
+  int parts;                          // of the reduction of a tile of y
+  uint32_t inv_k;                     // ceil(2^16 / k)
+
+  // i / k for slots below 2048 and k up to 32: i (k - 1) stays below 2^16
+  __device__ __forceinline__ int token(int i) const {
+    return static_cast<int>((static_cast<uint32_t>(i) * inv_k) >> 16);
+  }
+};
+
+// A wave's place in a tile of 8 rows: the lane's row (and token), and its
+// first k in a load.
 template <bool MX>
 struct Lane {
   int r, k;
@@ -147,58 +213,72 @@ struct Lane {
   }
 };
 
-// The k of a chunk of kChunkK for 8 weight rows, as loaded.
-template <bool MX>
-struct Weights {
-  static constexpr int kSteps = MX ? 2 : 4;      // loads
-  static constexpr int kStepK = kChunkK / kSteps;
-  static constexpr int kFrags = MX ? 4 : 4;      // MFMA operands
-  i32x4 w[kSteps];
-  i32x2 s;                                       // MX: the 8 scale bytes
+// bf16 values of eight E4M3 codes; `scale`: 4 scale bytes of 32 codes each,
+// `block`: which of them, as the exponent of a float.
+__device__ __forceinline__ bf16x8_v widen(int c0, int c1, uint32_t scale,
+                                          int block) {
+  const float sc = __uint_as_float(((scale >> (block * 8)) & 0xff) << 23);
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  i32x4 o;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t c = static_cast<uint32_t>(q ? c1 : c0);
+    const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc,
+                                                                  false);
+    const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc,
+                                                                  true);
+    o[2 * q] = __builtin_bit_cast(int, lo);
+    o[2 * q + 1] = __builtin_bit_cast(int, hi);
+  }
+  return __builtin_bit_cast(bf16x8_v, o);
+}
 
-  // row0: byte offset of the lane's row; k0: first k of the chunk
+// KC k of 8 weight rows, as loaded; KC / 64 MFMA operands.
+template <bool MX, int KC = kChunkK>
+struct Weights {
+  static constexpr int kLoadK = MX ? 128 : 64;
+  static constexpr int kLoads = KC / kLoadK;
+  static constexpr int kFrags = KC / 64;
+  i32x4 w[kLoads];
+  uint32_t s[MX ? kLoads : 1];         // MX: 4 scale bytes a load
+
+  // row: byte offset of the lane's row (MX: of a byte a value)
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r,
                                        __amdgpu_buffer_rsrc_t rs,
                                        uint32_t row, int k0, int K,
                                        const Lane<MX>& L) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int k = k0 + i * kStepK + L.k;
-      w[i] = buf_load16(r, k < K ? row + static_cast<uint32_t>(k) *
-                                             (MX ? 1 : 2)
-                                 : kOob);
+    for (int i = 0; i < kLoads; ++i) {
+      const int k = k0 + i * kLoadK + L.k;
+      w[i] = buf_load16(
+          r, k < K ? row + static_cast<uint32_t>(k) * (MX ? 1 : 2) : kOob);
     }
-    if constexpr (MX)
-      s = __builtin_amdgcn_raw_buffer_load_b64(
-          rs, row / 32 + static_cast<uint32_t>(k0) / 32, 0, 0);
+    if constexpr (MX) {
+      const uint32_t at =
+          k0 < K ? row / 32 + static_cast<uint32_t>(k0) / 32 : kOob;
+      if constexpr (kLoads == 4) {
+        const i32x4 v = buf_load16(rs, at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = static_cast<uint32_t>(v[i]);
+      } else {
+        static_assert(kLoads == 2, "256 or 512 codes");
+        const i32x2 v = __builtin_bit_cast(
+            i32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0));
+        s[0] = static_cast<uint32_t>(v[0]);
+        s[1] = static_cast<uint32_t>(v[1]);
+      }
+    }
   }
   __device__ __forceinline__ bf16x8_v frag(int i, const Lane<MX>& L) const {
-    if constexpr (!MX) {
+    if constexpr (!MX)
       return __builtin_bit_cast(bf16x8_v, w[i]);
-    } else {
-      // codes 8 (i % 2) .. + 7 of load i / 2; its scale byte, of 4 a load,
-      // as the exponent of a float
-      const uint32_t sb = static_cast<uint32_t>(s[i >> 1]);
-      const float sc =
-          __uint_as_float(((sb >> ((L.k >> 5) * 8)) & 0xff) << 23);
-      typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-      i32x4 o;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint32_t c = static_cast<uint32_t>(w[i >> 1][2 * (i & 1) + q]);
-        const bf16x2_t lo =
-            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, false);
-        const bf16x2_t hi =
-            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, true);
-        o[2 * q] = __builtin_bit_cast(int, lo);
-        o[2 * q + 1] = __builtin_bit_cast(int, hi);
-      }
-      return __builtin_bit_cast(bf16x8_v, o);
-    }
+    else
+      return widen(w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1],
+                   s[i >> 1], L.k >> 5);
   }
 };
 
-// The same k of one block of tokens: fragment i matches Weights' i.
+// The same k of a block of 8 tokens: fragment i matches Weights' i.
 template <bool MX>
 struct Tokens {
   i32x4 v[4];
@@ -223,183 +303,74 @@ __device__ __forceinline__ f32x4 mma(bf16x8_v a, bf16x8_v b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// bytes of n x K weights, and of their scales
-template <bool MX>
-__device__ __forceinline__ uint32_t weight_bytes(int64_t n, int K) {
-  return static_cast<uint32_t>(n * K * (MX ? 1 : 2));
-}
-
-// ---------------------------------------------------------------- gate, up
-struct FewParams {
-  const bf16_t* x;
-  const uint8_t* w_gu;
-  const uint8_t* w_gu_scales;
-  const uint8_t* w2;
-  const uint8_t* w2_scales;
-  const int32_t* idx;                 // [T][k]
-  const float* wt;
-  bf16_t* s;                          // [T k][f]
-  const bf16_t* y_add;
-  bf16_t* y;
-  int T, d, f, E, k;
-  int slots;                          // units are slots (T k < E), or experts
-};
-
-// S of one expert for the NB blocks of its tokens.  slot: of member `lane`.
-template <bool MX, int NB>
-__device__ __forceinline__ void up_tile(const FewParams& P, int e, int n0,
-                                        int members, int slot,
-                                        float* __restrict__ red) {
-  const Lane<MX> L;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int K = P.d;
-  const int64_t per = static_cast<int64_t>(2) * P.f * K;   // values an expert
-  const auto rw = make_rsrc(P.w_gu + e * per * (MX ? 1 : 2),
-                            weight_bytes<MX>(2 * P.f, K));
-  const auto rs = MX ? make_rsrc(P.w_gu_scales + e * (per / 32),
-                                 static_cast<uint32_t>(per / 32))
-                     : rw;
-  const auto rx = make_rsrc(P.x, static_cast<uint32_t>(P.T) * K * 2);
-  const uint32_t gate = static_cast<uint32_t>(n0 + L.r) * K * (MX ? 1 : 2);
-  const uint32_t up = gate + static_cast<uint32_t>(P.f) * K * (MX ? 1 : 2);
-  uint32_t tok[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int m = b * kTok + L.r;
-    const int sl = __shfl(slot, m, kWave);
-    tok[b] = m < members ? static_cast<uint32_t>(sl / P.k) * K * 2 : kOob;
-  }
-  f32x4 ag[NB], au[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) ag[b] = au[b] = f32x4{};
-  Weights<MX> g, u;
-  Tokens<MX> x[NB];
-  int k0 = wave * kChunkK;
-  if (k0 < K) {
-    g.load(rw, rs, gate, k0, K, L);
-    u.load(rw, rs, up, k0, K, L);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) x[b].load(rx, tok[b], k0, K, L);
-  }
-  while (k0 < K) {
-    const int k1 = k0 + kWaves * kChunkK;
-    const Weights<MX> cg = g, cu = u;
-    Tokens<MX> cx[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) cx[b] = x[b];
-    if (k1 < K) {
-      g.load(rw, rs, gate, k1, K, L);
-      u.load(rw, rs, up, k1, K, L);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[b].load(rx, tok[b], k1, K, L);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bf16x8_v fg = cg.frag(i, L), fu = cu.frag(i, L);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        ag[b] = mma(fg, cx[b].frag(i), ag[b]);
-        au[b] = mma(fu, cx[b].frag(i), au[b]);
-      }
-    }
-    k0 = k1;
-  }
-  // red[wave][gate, up][lane][4]: row 4 (lane / 16) + v, token lane % 16
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    if (b) __syncthreads();
-    *reinterpret_cast<f32x4*>(red + (wave * 2 * 64 + lane) * 4) = ag[b];
-    *reinterpret_cast<f32x4*>(red + ((wave * 2 + 1) * 64 + lane) * 4) = au[b];
-    __syncthreads();
-    if (tid < kRows * kTok) {
-      const int row = tid & 7, c = tid >> 3;
-      // the two halves of k: rows and tokens 0-7, and 8-15
-      const int o1 = ((row >> 2) * 16 + c) * 4 + (row & 3);
-      const int o2 = (((row >> 2) + 2) * 16 + c + 8) * 4 + (row & 3);
-      float a = 0.0f, v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float* q = red + w * 2 * 256;
-        a += q[o1] + q[o2];
-        v += q[256 + o1] + q[256 + o2];
-      }
-      const int m = b * kTok + c;
-      const int sl = __shfl(slot, m, kWave);
-      if (m < members) {
-        const float h = a * sigmoidf_(a) * v * P.wt[sl];
-        P.s[static_cast<int64_t>(sl) * P.f + n0 + row] = f2bf(h);
-      }
-    }
-  }
-}
-
-// MAXB: blocks that T tokens can fill.
-template <bool MX, int MAXB>
-__global__ __launch_bounds__(kThreads) void few_up_kernel(FewParams P) {
-  __shared__ __attribute__((aligned(16))) float red[kWaves * 2 * 256];
-  const int lane = threadIdx.x & 63;
-  const int tiles = P.f / kRows;
-  const int unit = blockIdx.x / tiles;
-  const int n0 = (blockIdx.x - unit * tiles) * kRows;
-  // lane t looks for the unit's expert among token t's choices
-  const int e = __builtin_amdgcn_readfirstlane(P.slots ? P.idx[unit] : unit);
-  int slot = -1;
-  if (lane < P.T)
-    for (int j = 0; j < P.k; ++j)
-      if (P.idx[lane * P.k + j] == e) slot = lane * P.k + j;
-  const uint64_t mask = __ballot(slot >= 0);
-  if (mask == 0) return;
-  // a slot whose expert an earlier token has too is left to that token's
-  if (P.slots && __ffsll(static_cast<unsigned long long>(mask)) - 1 !=
-                     unit / P.k)
-    return;
-  const int members = __popcll(mask);
-  // member m's slot to lane m
-  const int rank = __popcll(mask & ((uint64_t{1} << lane) - 1));
-  slot = __builtin_amdgcn_ds_permute((slot >= 0 ? rank : 63) * 4, slot);
-  if (members <= 8) {
-    up_tile<MX, 1>(P, e, n0, members, slot, red);
-  } else if (MAXB >= 2 && members <= 16) {
-    up_tile<MX, MAXB >= 2 ? 2 : 1>(P, e, n0, members, slot, red);
-  } else if (MAXB >= 4 && members <= 32) {
-    up_tile<MX, MAXB >= 4 ? 4 : 1>(P, e, n0, members, slot, red);
-  } else if (MAXB >= 8) {
-    up_tile<MX, MAXB >= 8 ? 8 : 1>(P, e, n0, members, slot, red);
-  }
-}
-
-// -------------------------------------------------------------------- down
-// What every wave of few_down_kernel knows of the experts that are reached.
+// --------------------------------------------------------- reached experts
+// The experts that are reached, in order, with the slots of their tokens, in
+// the front of a kernel's dynamic LDS.
 struct Units {
-  uint64_t mask[kMaxExperts];         // tokens of an expert
-  uint16_t first[kMaxExperts];        // its first place in `slot`
-  uint16_t expert[kMaxExperts];       // reached experts in order
-  uint16_t slot[kFewTokens * kMaxTopK];
+  uint64_t* mask;       // [E] tokens of an expert
+  float* wt;            // [T k] weight of a slot
+  uint16_t* slot;       // [T k] slots, those of an expert in a row
+  uint16_t* first;      // [E] where an expert's are
+  uint16_t* expert;     // [E] reached experts, in order
   int count;
+
+  // bytes for E experts and n slots, a multiple of 16
+  __host__ __device__ static int bytes(int E, int n) {
+    return (E * 12 + n * 6 + 4 + 15) & ~15;
+  }
 };
 
-__device__ __forceinline__ void find_units(const FewParams& P, Units& U) {
+template <int kThreads>
+__device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
+                                           Units* out) {
+  constexpr int kPer = kFewTokens * kMaxTopK / kThreads;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int n = P.T * P.k;
-  for (int e = tid; e < P.E; e += kThreads) U.mask[e] = 0;
-  int mine[kFewTokens * kMaxTopK / kThreads];
+  const int n = P.T * P.k, E = P.E;
+  Units U;
+  U.mask = reinterpret_cast<uint64_t*>(lds);
+  U.wt = reinterpret_cast<float*>(U.mask + E);
+  int* const count_at = reinterpret_cast<int*>(U.wt + n);
+  U.slot = reinterpret_cast<uint16_t*>(count_at + 1);
+  U.first = U.slot + n;
+  U.expert = U.first + E;
+  if (P.T == 1) {                     // every slot, in its own order
+    if (tid < n) {
+      const int e = P.idx[tid];
+      U.wt[tid] = P.wt[tid];
+      U.expert[tid] = static_cast<uint16_t>(e);
+      U.mask[e] = 1;
+      U.first[e] = static_cast<uint16_t>(tid);
+      U.slot[tid] = static_cast<uint16_t>(tid);
+    }
+    __syncthreads();
+    U.count = n;
+    *out = U;
+    return;
+  }
+  int mine[kPer];
+  float wt[kPer];
 #pragma unroll
-  for (int q = 0; q < kFewTokens * kMaxTopK / kThreads; ++q) {
+  for (int q = 0; q < kPer; ++q) {
     const int i = tid + q * kThreads;
     mine[q] = i < n ? P.idx[i] : -1;
+    wt[q] = i < n ? P.wt[i] : 0.0f;
   }
+  for (int e = tid; e < E; e += kThreads) U.mask[e] = 0;
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < kFewTokens * kMaxTopK / kThreads; ++q)
-    if (mine[q] >= 0)
+  for (int q = 0; q < kPer; ++q)
+    if (mine[q] >= 0) {
+      const int i = tid + q * kThreads;
+      U.wt[i] = wt[q];
       atomicOr(reinterpret_cast<unsigned long long*>(&U.mask[mine[q]]),
-               1ull << ((tid + q * kThreads) / P.k));
+               1ull << P.token(i));
+    }
   __syncthreads();
   if (tid < 64) {
     int count = 0, first = 0;
-    for (int e0 = 0; e0 < P.E; e0 += 64) {
+    for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
-      const int c = e < P.E ? __popcll(U.mask[e]) : 0;
+      const int c = e < E ? __popcll(U.mask[e]) : 0;
       const uint64_t act = __ballot(c > 0);
       int incl = c;
 #pragma unroll
@@ -407,133 +378,829 @@ __device__ __forceinline__ void find_units(const FewParams& P, Units& U) {
         const int o = __shfl_up(incl, m, kWave);
         if (lane >= m) incl += o;
       }
-      if (e < P.E) U.first[e] = static_cast<uint16_t>(first + incl - c);
+      if (e < E) U.first[e] = static_cast<uint16_t>(first + incl - c);
       if (c)
         U.expert[count + __popcll(act & ((uint64_t{1} << lane) - 1))] =
             static_cast<uint16_t>(e);
       count += __popcll(act);
       first += __shfl(incl, 63, kWave);
     }
-    if (lane == 0) U.count = count;
+    if (lane == 0) *count_at = count;
   }
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < kFewTokens * kMaxTopK / kThreads; ++q)
+  for (int q = 0; q < kPer; ++q)
     if (mine[q] >= 0) {
-      const int i = tid + q * kThreads, t = i / P.k;
-      const uint64_t below = (uint64_t{1} << t) - 1;
+      const int i = tid + q * kThreads;
+      const uint64_t below = (uint64_t{1} << P.token(i)) - 1;
       U.slot[U.first[mine[q]] + __popcll(U.mask[mine[q]] & below)] =
           static_cast<uint16_t>(i);
     }
   __syncthreads();
+  U.count = __builtin_amdgcn_readfirstlane(*count_at);
+  *out = U;
 }
 
-// Adds a wave's sums of the expert's members b * 8 .. + 7 to its own plane
-// [half of k][token][8 rows].
-__device__ __forceinline__ void add_members(float* plane, int T, f32x4 acc,
-                                            int token) {
-  const int lane = lane_id(), c = lane & 15, q = lane >> 4;
-  // the diagonal blocks: rows 0-7 with tokens 0-7, rows 8-15 with 8-15
-  if ((q >> 1) != (c >> 3) || token < 0) return;
-  f32x4* p = reinterpret_cast<f32x4*>(
-      plane + (((q >> 1) * T + token) * kRows + (q & 1) * 4));
-  *p += acc;
-}
-
-template <bool MX, int MAXB>
-__global__ __launch_bounds__(kThreads) void few_down_kernel(FewParams P) {
-  __shared__ Units U;
-  // [wave][half][T][8]
-  extern __shared__ __attribute__((aligned(16))) float planes[];
-  const Lane<MX> L;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n0 = blockIdx.x * kRows;
-  const int K = P.f, T = P.T;
-  for (int i = tid; i < kWaves * 2 * T * kRows; i += kThreads) planes[i] = 0;
-  find_units(P, U);
-  float* const plane = planes + wave * 2 * T * kRows;
-  const int chunks = (K + kChunkK - 1) / kChunkK;      // of an expert
-  const int total = U.count * chunks;
-  const auto rx =
-      make_rsrc(P.s, static_cast<uint32_t>(T) * P.k * K * 2);
-  const int64_t per = static_cast<int64_t>(P.d) * K;
-  const uint32_t row = static_cast<uint32_t>(L.r) * K * (MX ? 1 : 2);
-
-  // (unit, chunk) pairs in order, dealt to the waves in turn
-  for (int q = wave; q < total; q += kWaves) {
-    const int un = q / chunks, k0 = (q - un * chunks) * kChunkK;
+// ---------------------------------------------------------------- gate, up
+// One reached expert, as its gate and up projection sees it.
+template <bool MX>
+struct UpExpert {
+  __amdgpu_buffer_rsrc_t rw, rs;
+  int first, members;
+  __device__ __forceinline__ UpExpert(const FewParams& P, const Units& U,
+                                      int un) {
     const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
-    const int members = __builtin_amdgcn_readfirstlane(
-        __popcll(U.mask[e]));
-    const int first = U.first[e];
-    const auto rw = make_rsrc(
-        P.w2 + (e * per + static_cast<int64_t>(n0) * K) * (MX ? 1 : 2),
-        weight_bytes<MX>(kRows, K));
-    const auto rs =
-        MX ? make_rsrc(P.w2_scales +
-                           (e * per + static_cast<int64_t>(n0) * K) / 32,
-                       static_cast<uint32_t>(kRows) * K / 32)
-           : rw;
-    Weights<MX> w;
-    w.load(rw, rs, row, k0, K, L);
-    for (int b = 0; b * kTok < members; ++b) {
-      const int m = b * kTok + L.r;
-      const int sl = m < members ? U.slot[first + m] : -1;
-      Tokens<MX> x;
-      x.load(rx, sl >= 0 ? static_cast<uint32_t>(sl) * K * 2 : kOob, k0, K,
-             L);
-      f32x4 acc = {};
+    first = __builtin_amdgcn_readfirstlane(U.first[e]);
+    members = __builtin_amdgcn_readfirstlane(__popcll(U.mask[e]));
+    const int64_t per = static_cast<int64_t>(2) * P.f * P.d;
+    rw = make_rsrc(P.w_gu + e * per * (MX ? 1 : 2),
+                   static_cast<uint32_t>(per * (MX ? 1 : 2)));
+    rs = MX ? make_rsrc(P.w_gu_scales + e * (per / 32),
+                        static_cast<uint32_t>(per / 32))
+            : rw;
+  }
+  // byte offset of row n of gate, or of up
+  __device__ __forceinline__ static uint32_t row(const FewParams& P, int n,
+                                                 bool up) {
+    return (static_cast<uint32_t>(n) + (up ? P.f : 0)) * P.d * (MX ? 1 : 2);
+  }
+};
+
+// S = wt silu(a) u in two bf16 parts, the second what the first leaves.
+__device__ __forceinline__ float swiglu(float a, float u, float wt) {
+  return a * sigmoidf_(a) * u * wt;
+}
+
+// Tiles [t0, t1) of an expert, 8 gate and 8 up rows each, for up to 8 members;
+// the waves divide the reduction.  red: two buffers, `flip` tells which is
+// next.
+template <bool MX>
+__device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
+                                         int un, int t0, int t1,
+                                         float* __restrict__ red, int* flip) {
+  const Lane<MX> L;
+  const UpExpert<MX> X(P, U, un);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int K = P.d;
+  const auto rx = make_rsrc(P.x, static_cast<uint32_t>(P.T) * K * 2);
+  const uint32_t tok =
+      L.r < X.members
+          ? static_cast<uint32_t>(P.token(U.slot[X.first + L.r])) * K * 2
+          : kOob;
+  // the member that the lane stores for, and its weight
+  const int mine = lane >> 3;
+  const int slot = mine < X.members ? U.slot[X.first + mine] : -1;
+  const float wt = slot >= 0 ? U.wt[slot] : 0.0f;
+  // A wave's chunks of a tile, then the next tile's: one is in flight while
+  // the one before it is multiplied.  Loads past the last are masked and
+  // issued all the same: with a branch around them the compiler would wait
+  // for all that is in flight.
+  struct Item {
+    Weights<MX> g, u;
+    Tokens<MX> x;
+  };
+  auto load = [&](Item& it, int tile, int k0) {
+    const int n = tile * kRows + L.r;
+    const int k = tile < t1 ? k0 : K;
+    it.g.load(X.rw, X.rs, X.row(P, n, false), k, K, L);
+    it.u.load(X.rw, X.rs, X.row(P, n, true), k, K, L);
+    it.x.load(rx, tok, k, K, L);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int rounds = (K + kUpWaves * kChunkK - 1) / (kUpWaves * kChunkK);
+  Item nxt;
+  load(nxt, t0, wave * kChunkK);
+  for (int tile = t0; tile < t1; ++tile) {
+    f32x4 ag = {}, au = {};
+    for (int c = 0; c < rounds; ++c) {
+      const Item cur = nxt;
+      const bool last = c + 1 == rounds;
+      load(nxt, last ? tile + 1 : tile,
+           ((last ? 0 : c + 1) * kUpWaves + wave) * kChunkK);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc = mma(w.frag(i, L), x.frag(i), acc);
-      add_members(plane, T, acc, sl >= 0 ? sl / P.k : -1);
+      for (int i = 0; i < 4; ++i) {
+        ag = mma(cur.g.frag(i, L), cur.x.frag(i), ag);
+        au = mma(cur.u.frag(i, L), cur.x.frag(i), au);
+      }
+    }
+    // red[wave][gate, up][lane][4]: row 4 (lane / 16) + v, token lane % 16.
+    // A wave that still adds up one buffer passes the next barrier before
+    // anyone writes to that buffer again.
+    float* const r = red + *flip * (kUpWaves * 512);
+    *flip ^= 1;
+    *reinterpret_cast<f32x4*>(r + (wave * 128 + lane) * 4) = ag;
+    *reinterpret_cast<f32x4*>(r + (wave * 128 + 64 + lane) * 4) = au;
+    __syncthreads();
+    if (wave == (tile & (kUpWaves - 1))) {
+      const int row = lane & 7;
+      // the two halves of k: rows and tokens 0-7, and 8-15
+      const int o1 = ((row >> 2) * 16 + mine) * 4 + (row & 3);
+      const int o2 = (((row >> 2) + 2) * 16 + mine + 8) * 4 + (row & 3);
+      float a = 0.0f, v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kUpWaves; ++w) {
+        const float* q = r + w * 512;
+        a += q[o1] + q[o2];
+        v += q[256 + o1] + q[256 + o2];
+      }
+      if (slot >= 0) {
+        const float h = swiglu(a, v, wt);
+        const bf16_t hi = f2bf(h);
+        bf16_t* const o =
+            P.s + static_cast<int64_t>(slot) * 2 * P.f + tile * kRows + row;
+        o[0] = hi;
+        o[P.f] = f2bf(h - bf2f(hi));
+      }
     }
   }
-  __syncthreads();
-  for (int i = tid; i < T * kRows; i += kThreads) {
-    const int t = i >> 3, r = i & 7;
-    float v = 0.0f;
-    for (int p = 0; p < kWaves * 2; ++p) v += planes[(p * T + t) * kRows + r];
-    const int64_t o = static_cast<int64_t>(t) * P.d + n0 + r;
-    if (P.y_add) v += bf2f(P.y_add[o]);
-    P.y[o] = f2bf(v);
+}
+
+// All tiles of all reached experts in order, divided evenly over the
+// workgroups (what the CUs hold at once, so that starting and finding the
+// experts is paid once).
+template <bool MX>
+__global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ __attribute__((aligned(16))) float red[2 * kUpWaves * 512];
+  Units U;
+  find_units<kUpThreads>(P, lds, &U);
+  const int tiles = P.f / kRows;
+  const int total = U.count * tiles;
+  const int groups = gridDim.x, me = blockIdx.x;
+  const int per = total / groups, more = total - per * groups;
+  int at = me * per + min(me, more);
+  const int end = at + per + (me < more);
+  int flip = 0;
+  while (at < end) {
+    const int un = at / tiles;
+    const int t0 = at - un * tiles, t1 = min(tiles, t0 + end - at);
+    up_tiles<MX>(P, U, un, t0, t1, red, &flip);
+    at += t1 - t0;
   }
 }
 
+// ------------------------------------------------------------------- batch
+// More tokens.  The waves of a workgroup own rows and go through the same k
+// in step: the tokens' k (x, or S) are staged in LDS once for all of them,
+// and a wave holds the sums of its two 8-row tiles whole, so nothing is added
+// across waves.  Tokens stand in blocks of eight columns.
+//
+// A step is kStepK k (512 bytes of a weight row): D of a wave's steps are in
+// flight, 16 KB or more, and 8 waves a CU then cover the memory's latency
+// (128 KB; a kernel that only reads needs as much for 6 TB/s).  The columns
+// of step s + 2 are requested before the weights of step s + D, since loads
+// return in order and waiting for the columns must not wait for those.
+constexpr int kBatchThreads = 256;
+constexpr int kBatchWaves = kBatchThreads / kWave;
+constexpr int kBatchRows = kBatchWaves * 2 * kRows;
+
+// bytes of a step's columns, of the largest of the shapes up to `blocks`
+template <bool MX>
+constexpr int batch_bytes(int blocks) {
+  return MX && blocks <= 2 ? blocks * 8192
+         : MX              ? (blocks * 4096 > 16384 ? blocks * 4096 : 16384)
+                           : blocks * 4096;
+}
+
+template <bool MX, int NB>
+struct BatchShape {
+  static constexpr int kStepK = MX && NB <= 2 ? 512 : 256;
+  static constexpr int kAhead = MX && NB > 2 ? 4 : 2;
+  static constexpr int kPieces = kStepK / 8;            // of 16 bytes a column
+  static constexpr int kLoads = kPieces * 8 / kBatchThreads;  // a block
+  static constexpr int kBytes = NB * 8 * kPieces * 16;  // of a buffer
+};
+
+// The columns' k in LDS: 16-byte piece p of column c lies at p ^ swizzle(c),
+// so that the sixteen lanes of a fragment read that share a cycle (8 columns
+// x 2 pieces, 4 (bf16) or 8 apart) meet every bank once.
+template <bool MX>
+__device__ __forceinline__ int swizzle(int c) {
+  return MX ? c : (c & 3) | ((c & 4) << 1);
+}
+
+// Source: what step q of [begin, end) reads and what becomes of its sums
+//   weights(q, a, b): loads of the wave's two tiles
+//   column(q, c, b): byte offset of column c of block b in its resource, kOob
+//     for none; k(q): the step's first k (K for none); rx, K
+//   done(q, a, b): called with the sums at every step; true clears them
+template <bool MX, int NB, class Source>
+__device__ __forceinline__ void batch(Source& src, int begin, int end,
+                                      uint8_t* xs) {
+  using H = BatchShape<MX, NB>;
+  constexpr int D = H::kAhead;
+  static_assert(D % 2 == 0, "the LDS buffer is a compile-time constant");
+  const Lane<MX> L;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int fr = lane & 15, g = lane >> 4, col = fr & 7;
+  struct Columns {
+    i32x4 v[NB * H::kLoads];
+  };
+  Columns cx[2];
+  Weights<MX, H::kStepK> wa[D], wb[D];
+  auto load_columns = [&](Columns& x, int q) {
+    const int k0 = src.k(q);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < H::kLoads; ++j) {
+        const int id = tid + j * kBatchThreads;
+        const int c = id / H::kPieces, k = k0 + (id % H::kPieces) * 8;
+        const uint32_t at = src.column(q, c, b);
+        x.v[b * H::kLoads + j] = buf_load16(
+            src.rx, k < src.K && at != kOob
+                        ? at + static_cast<uint32_t>(k) * 2
+                        : kOob);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto store_columns = [&](const Columns& x, uint8_t* to) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < H::kLoads; ++j) {
+        const int id = tid + j * kBatchThreads;
+        const int c = id / H::kPieces, p = id % H::kPieces;
+        *reinterpret_cast<i32x4*>(
+            to + ((b * 8 + c) * H::kPieces + (p ^ swizzle<MX>(c))) * 16) =
+            x.v[b * H::kLoads + j];
+      }
+  };
+  // byte offset of fragment i of the lane's column of a block
+  auto piece = [&](int i) {
+    const int p = MX ? (i >> 1) * 16 + (fr >> 3) * 8 + g * 2 + (i & 1)
+                     : i * 8 + (fr >> 3) * 4 + g;
+    return (col * H::kPieces + (p ^ swizzle<MX>(col))) * 16;
+  };
+  load_columns(cx[0], begin);
+  load_columns(cx[1], begin + 1);
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    src.weights(begin + i, wa[i], wb[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  store_columns(cx[0], xs);
+  __syncthreads();
+  f32x4 a[NB], b[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) a[i] = b[i] = f32x4{};
+  for (int q0 = begin; q0 < end; q0 += D)
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      const int q = q0 + u;
+      uint8_t* const now = xs + (u & 1) * H::kBytes;
+      uint8_t* const then = xs + ((u & 1) ^ 1) * H::kBytes;
+      load_columns(cx[u & 1], q + 2);
+#pragma unroll
+      for (int i = 0; i < H::kStepK / 64; ++i) {
+        const bf16x8_v fa = wa[u].frag(i, L), fb = wb[u].frag(i, L);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const bf16x8_v x = __builtin_bit_cast(
+              bf16x8_v, *reinterpret_cast<const i32x4*>(
+                            now + n * 8 * H::kPieces * 16 + piece(i)));
+          a[n] = mma(fa, x, a[n]);
+          b[n] = mma(fb, x, b[n]);
+        }
+      }
+      src.weights(q + D, wa[u], wb[u]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (src.done(q, a, b))
+#pragma unroll
+        for (int i = 0; i < NB; ++i) a[i] = b[i] = f32x4{};
+      // the other buffer: its last reads were before the last barrier
+      store_columns(cx[(u & 1) ^ 1], then);
+      __syncthreads();
+    }
+}
+
+// Adds the two halves of k: rows 0-7 with columns 0-7 (lanes below 32 of
+// columns 0-7) and rows 8-15 with columns 8-15.
+__device__ __forceinline__ f32x4 join_halves(f32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += shfl_xor(v[i], 40);
+  return v;
+}
+
+// Gate and up: steps are (expert, group of 32 rows each, k), a wave's tiles
+// its gate and its up rows.
+template <bool MX, int NB>
+struct UpSource {
+  using H = BatchShape<MX, NB>;
+  const FewParams& P;
+  const Units& U;
+  __amdgpu_buffer_rsrc_t rx;
+  int K, rounds, groups, end, wave;
+  Lane<MX> L;
+
+  __device__ __forceinline__ UpSource(const FewParams& p, const Units& u,
+                                      int last)
+      : P(p), U(u),
+        rx(make_rsrc(p.x, static_cast<uint32_t>(p.T) * p.d * 2)), K(p.d),
+        rounds((p.d + H::kStepK - 1) / H::kStepK),
+        groups((p.f + 4 * kRows - 1) / (4 * kRows)), end(last),
+        wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {}
+  // (expert, group, round) of a step
+  __device__ __forceinline__ void split(int q, int* un, int* gr,
+                                        int* r) const {
+    const int t = q / rounds;
+    *r = q - t * rounds;
+    *un = t / groups;
+    *gr = t - *un * groups;
+  }
+  __device__ __forceinline__ int k(int q) const {
+    return q < end ? (q % rounds) * H::kStepK : K;
+  }
+  __device__ __forceinline__ uint32_t column(int q, int c, int b) const {
+    if (q >= end) return kOob;
+    const int e = U.expert[q / rounds / groups];
+    const int m = b * 8 + c;
+    return m < __popcll(U.mask[e])
+               ? static_cast<uint32_t>(P.token(U.slot[U.first[e] + m])) * K * 2
+               : kOob;
+  }
+  __device__ __forceinline__ void weights(int q, Weights<MX, H::kStepK>& a,
+                                          Weights<MX, H::kStepK>& b) const {
+    int un = 0, gr = 0, r = 0;
+    if (q < end) split(q, &un, &gr, &r);
+    const UpExpert<MX> X(P, U, un);
+    const int n = (gr * kBatchWaves + wave) * kRows;
+    const int k0 = q < end && n < P.f ? r * H::kStepK : K;
+    a.load(X.rw, X.rs, X.row(P, n + L.r, false), k0, K, L);
+    b.load(X.rw, X.rs, X.row(P, n + L.r, true), k0, K, L);
+  }
+  __device__ __forceinline__ bool done(int q, const f32x4* a,
+                                       const f32x4* b) const {
+    if (q >= end) return false;
+    int un, gr, r;
+    split(q, &un, &gr, &r);
+    if (r + 1 < rounds) return false;
+    const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
+    const int e = U.expert[un], members = __popcll(U.mask[e]);
+    const int n = (gr * kBatchWaves + wave) * kRows;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const f32x4 ga = join_halves(a[i]), up = join_halves(b[i]);
+      const int m = i * 8 + c;
+      if (c >= 8 || qr >= 2 || m >= members || n >= P.f) continue;
+      const int slot = U.slot[U.first[e] + m];
+      const float wt = U.wt[slot];
+      float h[4], l[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        h[v] = swiglu(ga[v], up[v], wt);
+        l[v] = h[v] - bf2f(f2bf(h[v]));
+      }
+      bf16_t* const o =
+          P.s + static_cast<int64_t>(slot) * 2 * P.f + n + qr * 4;
+      *reinterpret_cast<i32x2*>(o) =
+          i32x2{static_cast<int>(pack_bf16x2(h[0], h[1])),
+                static_cast<int>(pack_bf16x2(h[2], h[3]))};
+      *reinterpret_cast<i32x2*>(o + P.f) =
+          i32x2{static_cast<int>(pack_bf16x2(l[0], l[1])),
+                static_cast<int>(pack_bf16x2(l[2], l[3]))};
+    }
+    return true;
+  }
+};
+
+// The largest number of members of the experts [u0, u1).
+__device__ __forceinline__ int most_members(const Units& U, int u0, int u1) {
+  int most = 0;
+  for (int u = u0 + lane_id(); u < u1; u += kWave)
+    most = max(most, __popcll(U.mask[U.expert[u]]));
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) most = max(most, shfl_xor(most, m));
+  return __builtin_amdgcn_readfirstlane(most);
+}
+
+template <bool MX, int NB>
+__device__ __forceinline__ void up_batch(const FewParams& P, const Units& U,
+                                         int first, int last, uint8_t* xs) {
+  constexpr int kStepK = BatchShape<MX, NB>::kStepK;
+  const int rounds = (P.d + kStepK - 1) / kStepK;
+  UpSource<MX, NB> src(P, U, last * rounds);
+  batch<MX, NB>(src, first * rounds, last * rounds, xs);
+}
+
+// MAXB: blocks of 8 that T tokens can fill.
 template <bool MX, int MAXB>
-hipError_t launch_few(const FewParams& P, hipStream_t s) {
-  const int units = P.slots ? P.T * P.k : P.E;
-  hipLaunchKernelGGL((few_up_kernel<MX, MAXB>),
-                     dim3(static_cast<uint32_t>(units) * (P.f / kRows)),
-                     dim3(kThreads), 0, s, P);
-  hipError_t e = hipGetLastError();
+__global__ __launch_bounds__(kBatchThreads, 2) void few_up_batch_kernel(
+    FewParams P) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  Units U;
+  find_units<kBatchThreads>(P, lds, &U);
+  uint8_t* const xs = lds + Units::bytes(P.E, P.T * P.k);
+  const int groups = (P.f + 4 * kRows - 1) / (4 * kRows);
+  const int total = U.count * groups;
+  const int n = gridDim.x, me = blockIdx.x;
+  const int per = total / n, more = total - per * n;
+  const int first = me * per + min(me, more);
+  const int last = first + per + (me < more);
+  if (first >= last) return;
+  const int most = most_members(U, first / groups, (last - 1) / groups + 1);
+  if (MAXB == 1 || most <= 8)
+    up_batch<MX, 1>(P, U, first, last, xs);
+  else if (MAXB == 2 || most <= 16)
+    up_batch<MX, MAXB >= 2 ? 2 : 1>(P, U, first, last, xs);
+  else if (MAXB == 4 || most <= 32)
+    up_batch<MX, MAXB >= 4 ? 4 : 1>(P, U, first, last, xs);
+  else
+    up_batch<MX, MAXB >= 8 ? 8 : 1>(P, U, first, last, xs);
+}
+
+// Down: steps are (expert, pass, k), a wave's tiles 16 rows of y.  A block
+// holds four members, each as two columns, S's larger and smaller part; an
+// expert with more members than NB blocks hold takes several passes.
+template <bool MX, int NB>
+struct DownSource {
+  using H = BatchShape<MX, NB>;
+  static constexpr int kMembers = 4 * NB;
+  const FewParams& P;
+  const Units& U;
+  __amdgpu_buffer_rsrc_t rx;
+  int K, rounds, passes, end, n0;
+  float* plane;                       // [T][16], the wave's
+  Lane<MX> L;
+
+  __device__ __forceinline__ DownSource(const FewParams& p, const Units& u,
+                                        int last, int most, int row0,
+                                        float* sums)
+      : P(p), U(u),
+        rx(make_rsrc(p.s, static_cast<uint32_t>(p.T) * p.k * 4 * p.f)),
+        K(p.f), rounds((p.f + H::kStepK - 1) / H::kStepK),
+        passes((most + kMembers - 1) / kMembers), end(last), n0(row0),
+        plane(sums) {}
+  // (expert, pass, round) of a step
+  __device__ __forceinline__ void split(int q, int* un, int* ps,
+                                        int* r) const {
+    const int t = q / rounds;
+    *r = q - t * rounds;
+    *un = t / passes;
+    *ps = t - *un * passes;
+  }
+  __device__ __forceinline__ int k(int q) const {
+    return q < end ? (q % rounds) * H::kStepK : K;
+  }
+  __device__ __forceinline__ uint32_t column(int q, int c, int b) const {
+    if (q >= end) return kOob;
+    int un, ps, r;
+    split(q, &un, &ps, &r);
+    const int e = U.expert[un];
+    const int m = ps * kMembers + b * 4 + (c >> 1);
+    return m < __popcll(U.mask[e])
+               ? (static_cast<uint32_t>(U.slot[U.first[e] + m]) * 2 +
+                  (c & 1)) * K * 2
+               : kOob;
+  }
+  __device__ __forceinline__ void weights(int q, Weights<MX, H::kStepK>& a,
+                                          Weights<MX, H::kStepK>& b) const {
+    int un = 0, ps = 0, r = 0;
+    if (q < end) split(q, &un, &ps, &r);
+    const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
+    const bool in = q < end && n0 < P.d;
+    const int64_t at = (e * static_cast<int64_t>(P.d) + (in ? n0 : 0)) * K;
+    const uint32_t rows = static_cast<uint32_t>(in ? min(16, P.d - n0) : 0);
+    const auto rw = make_rsrc(P.w2 + at * (MX ? 1 : 2),
+                              rows * K * (MX ? 1 : 2));
+    const auto rs =
+        MX ? make_rsrc(P.w2_scales + at / 32, rows * K / 32) : rw;
+    const uint32_t row = static_cast<uint32_t>(L.r) * K * (MX ? 1 : 2);
+    // an expert without members in this pass is not read
+    const bool some = ps == 0 || ps * kMembers < __popcll(U.mask[e]);
+    const int k0 = in && some ? r * H::kStepK : K;
+    a.load(rw, rs, row, k0, K, L);
+    b.load(rw, rs, row + static_cast<uint32_t>(kRows) * K * (MX ? 1 : 2),
+           n0 + kRows < P.d ? k0 : K, K, L);
+  }
+  __device__ __forceinline__ bool done(int q, const f32x4* a,
+                                       const f32x4* b) const {
+    if (q >= end) return false;
+    int un, ps, r;
+    split(q, &un, &ps, &r);
+    if (r + 1 < rounds && q + 1 < end) return false;
+    const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
+    const int e = U.expert[un], members = __popcll(U.mask[e]);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      f32x4 s0 = join_halves(a[i]), s1 = join_halves(b[i]);
+      // S's two parts stand in neighbouring columns
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        s0[v] += dpp_move<kDppXor1>(s0[v]);
+        s1[v] += dpp_move<kDppXor1>(s1[v]);
+      }
+      const int m = ps * kMembers + i * 4 + (c >> 1);
+      if (c >= 8 || (c & 1) || qr >= 2 || m >= members) continue;
+      f32x4* const o = reinterpret_cast<f32x4*>(
+          plane + P.token(U.slot[U.first[e] + m]) * 16 + qr * 4);
+      o[0] += s0;
+      o[2] += s1;
+    }
+    return true;
+  }
+};
+
+template <bool MX, int NB>
+__device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
+                                           int part, int most, int n0,
+                                           float* plane, uint8_t* xs) {
+  constexpr int kStepK = BatchShape<MX, NB>::kStepK;
+  const int rounds = (P.f + kStepK - 1) / kStepK;
+  const int passes = (most + 4 * NB - 1) / (4 * NB);
+  const int64_t total = static_cast<int64_t>(U.count) * passes * rounds;
+  const int begin = static_cast<int>(total * part / P.parts);
+  const int end = static_cast<int>(total * (part + 1) / P.parts);
+  if (begin >= end) return;
+  DownSource<MX, NB> src(P, U, end, most, n0, plane);
+  batch<MX, NB>(src, begin, end, xs);
+}
+
+// MAXB: blocks of 4 members that T tokens can fill, up to 8.
+template <bool MX, int MAXB>
+__global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
+    FewParams P) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, T = P.T;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = blockIdx.x / P.parts, part = blockIdx.x - group * P.parts;
+  float* const planes =
+      reinterpret_cast<float*>(lds + Units::bytes(P.E, T * P.k));
+  for (int i = tid; i < kBatchWaves * T * 16; i += kBatchThreads)
+    planes[i] = 0;
+  Units U;
+  find_units<kBatchThreads>(P, lds, &U);
+  float* const plane = planes + wave * T * 16;
+  uint8_t* const xs =
+      reinterpret_cast<uint8_t*>(planes + kBatchWaves * T * 16);
+  const int n0 = group * kBatchRows + wave * 16;
+  const int most = most_members(U, 0, U.count);
+  if (MAXB == 2 || most <= 8)
+    down_batch<MX, 2>(P, U, part, most, n0, plane, xs);
+  else if (MAXB == 4 || most <= 16)
+    down_batch<MX, MAXB >= 4 ? 4 : 2>(P, U, part, most, n0, plane, xs);
+  else
+    down_batch<MX, MAXB >= 8 ? 8 : 2>(P, U, part, most, n0, plane, xs);
+  // the wave's own rows of the part's sums
+  for (int i = lane; i < T * 4; i += kWave) {
+    const int t = i >> 2, r = (i & 3) * 4;
+    if (n0 + r < P.d)
+      *reinterpret_cast<f32x4*>(
+          P.part + (static_cast<int64_t>(part) * T + t) * P.d + n0 + r) =
+          *reinterpret_cast<const f32x4*>(plane + t * 16 + r);
+  }
+}
+
+// -------------------------------------------------------------------- down
+// Up to kDirect tokens: the columns of a tile are the tokens, each as two,
+// S's larger and smaller part, and a wave's sums run over all experts.
+constexpr int kDirect = 4;
+constexpr int kDownThreads = 1024;
+constexpr int kDownWaves = kDownThreads / kWave;
+constexpr int kAhead = 3;             // chunks of a wave in flight
+
+// A workgroup of sixteen waves a CU goes through its tiles of y: (tile,
+// expert, chunk) in order, dealt in turn to the waves, the next tile's loads
+// in flight while one is added up.
+template <bool MX>
+__global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
+    FewParams P) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ __attribute__((aligned(16))) float red[2 * kDownWaves * 256];
+  const Lane<MX> L;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = blockIdx.x / P.parts, part = blockIdx.x - group * P.parts;
+  const int groups = gridDim.x / P.parts, tiles = P.d / kRows;
+  const int K = P.f, T = P.T;
+  Units U;
+  find_units<kDownThreads>(P, lds, &U);
+  const int chunks = (K + kChunkK - 1) / kChunkK;      // of an expert
+  const int total = U.count * chunks;
+  const auto rx = make_rsrc(P.s, static_cast<uint32_t>(T) * P.k * 2 * K * 2);
+  const int64_t per = static_cast<int64_t>(P.d) * K;
+  const uint32_t row = static_cast<uint32_t>(L.r) * K * (MX ? 1 : 2);
+  const int t = L.r >> 1;              // the token of the lane's column
+
+  struct Item {
+    Weights<MX> w;
+    Tokens<MX> x;
+  };
+  // item q of a tile; past the last item or tile: masked
+  auto load = [&](Item& it, int tile, int q) {
+    const bool in = q < total && tile < tiles;
+    const int un = in ? q / chunks : 0;
+    const int k0 = in ? (q - un * chunks) * kChunkK : K;
+    const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
+    const int64_t at =
+        e * per + static_cast<int64_t>(in ? tile * kRows : 0) * K;
+    const auto rw = make_rsrc(
+        P.w2 + at * (MX ? 1 : 2),
+        static_cast<uint32_t>(kRows) * K * (MX ? 1 : 2));
+    const auto rs = MX ? make_rsrc(P.w2_scales + at / 32,
+                                   static_cast<uint32_t>(kRows) * K / 32)
+                       : rw;
+    it.w.load(rw, rs, row, k0, K, L);
+    const uint32_t mask = static_cast<uint32_t>(U.mask[e]);
+    const bool has = (mask >> t) & 1;
+    const int sl = U.slot[U.first[e] + (has ? __popc(mask & ((1u << t) - 1))
+                                            : 0)];
+    it.x.load(rx,
+              has ? static_cast<uint32_t>(sl * 2 + (L.r & 1)) * K * 2 : kOob,
+              k0, K, L);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int step = kDownWaves * P.parts;
+  const int q0 = part * kDownWaves + wave;
+  // rounds of a tile that all waves make, a multiple of kAhead
+  const int rounds = ((total + step - 1) / step + kAhead - 1) / kAhead *
+                     kAhead;
+  Item it[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(it[i], group, q0 + i * step);
+  int flip = 0;
+  for (int tile = group; tile < tiles; tile += groups) {
+    f32x4 acc = {};
+    for (int c = 0; c < rounds; c += kAhead) {
+      const bool last = c + kAhead == rounds;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          acc = mma(it[i].w.frag(s, L), it[i].x.frag(s), acc);
+        load(it[i], last ? tile + groups : tile,
+             q0 + (last ? i : c + kAhead + i) * step);
+      }
+    }
+    float* const r = red + flip * (kDownWaves * 256);
+    *reinterpret_cast<f32x4*>(r + (wave * 64 + lane) * 4) = acc;
+    __syncthreads();
+    // as in up_few a buffer is free again after the next barrier
+    if (wave == flip) {
+      const int n = lane & 7, c = lane >> 3;
+      // the two halves of k: rows and columns 0-7, and 8-15
+      const int o1 = ((n >> 2) * 16 + c) * 4 + (n & 3);
+      const int o2 = (((n >> 2) + 2) * 16 + c + 8) * 4 + (n & 3);
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kDownWaves; ++w)
+        v += r[w * 256 + o1] + r[w * 256 + o2];
+      v += shfl_xor(v, 8);              // S's two parts
+      if (!(c & 1) && (c >> 1) < T) {
+        const int64_t o = static_cast<int64_t>(c >> 1) * P.d + tile * kRows +
+                          n;
+        if (P.parts > 1) {
+          P.part[static_cast<int64_t>(part) * T * P.d + o] = v;
+        } else {
+          if (P.y_add) v += bf2f(P.y_add[o]);
+          P.y[o] = f2bf(v);
+        }
+      }
+    }
+    flip ^= 1;
+  }
+}
+
+// y = y_add + the parts in order; n values, a multiple of 8.
+__global__ __launch_bounds__(256) void few_sum_kernel(
+    const float* __restrict__ part, int parts, int64_t n, const bf16_t* y_add,
+    bf16_t* y) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 v = {};
+#pragma unroll 8
+  for (int p = 0; p < parts; ++p)
+    v += *reinterpret_cast<const f32x4*>(part + p * n + i);
+  if (y_add) {
+    const i32x2 a = *reinterpret_cast<const i32x2*>(y_add + i);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      v[2 * q] += bf_lo(static_cast<uint32_t>(a[q]));
+      v[2 * q + 1] += bf_hi(static_cast<uint32_t>(a[q]));
+    }
+  }
+  *reinterpret_cast<i32x2*>(y + i) =
+      i32x2{static_cast<int>(pack_bf16x2(v[0], v[1])),
+            static_cast<int>(pack_bf16x2(v[2], v[3]))};
+}
+
+// ---------------------------------------------------------------- launches
+// Experts that T tokens can reach.
+int most_units(int T, int k, int E) { return T * k < E ? T * k : E; }
+
+template <bool MX>
+hipError_t launch_direct(const FewParams& P, hipStream_t s) {
+  const int units = Units::bytes(P.E, P.T * P.k);
+  // four workgroups a CU, or fewer where the tiles cannot be more
+  const int64_t most =
+      static_cast<int64_t>(most_units(P.T, P.k, P.E)) * (P.f / kRows);
+  hipLaunchKernelGGL(few_up_kernel<MX>,
+                     dim3(static_cast<uint32_t>(most < 1024 ? most : 1024)),
+                     dim3(kUpThreads), units, s, P);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((few_down_kernel<MX, MAXB>), dim3(P.d / kRows),
-                     dim3(kThreads),
-                     kWaves * 2 * P.T * kRows * sizeof(float), s, P);
+  const uint32_t tiles = P.d / kRows;
+  hipLaunchKernelGGL(few_down_kernel<MX>,
+                     dim3((tiles < 256 ? tiles : 256) * P.parts),
+                     dim3(kDownThreads), units, s, P);
+  return hipGetLastError();
+}
+
+template <bool MX, int MAXB>
+hipError_t launch_up_batch(const FewParams& P, hipStream_t s) {
+  // two workgroups a CU, or fewer where the groups cannot be more
+  const int64_t most = static_cast<int64_t>(most_units(P.T, P.k, P.E)) *
+                       ((P.f + 4 * kRows - 1) / (4 * kRows));
+  hipLaunchKernelGGL(
+      (few_up_batch_kernel<MX, MAXB>),
+      dim3(static_cast<uint32_t>(most < 512 ? most : 512)),
+      dim3(kBatchThreads),
+      Units::bytes(P.E, P.T * P.k) + 2 * batch_bytes<MX>(MAXB), s, P);
+  return hipGetLastError();
+}
+
+template <bool MX, int MAXB>
+hipError_t launch_down_batch(const FewParams& P, hipStream_t s) {
+  const uint32_t groups = (P.d + kBatchRows - 1) / kBatchRows;
+  hipLaunchKernelGGL(
+      (few_down_batch_kernel<MX, MAXB>), dim3(groups * P.parts),
+      dim3(kBatchThreads),
+      Units::bytes(P.E, P.T * P.k) + kBatchWaves * P.T * 64 +
+          2 * batch_bytes<MX>(MAXB),
+      s, P);
   return hipGetLastError();
 }
 
 template <bool MX>
-hipError_t launch_blocks(const FewParams& P, hipStream_t s) {
-  if (P.T <= 8) return launch_few<MX, 1>(P, s);
-  if (P.T <= 16) return launch_few<MX, 2>(P, s);
-  if (P.T <= 32) return launch_few<MX, 4>(P, s);
-  return launch_few<MX, 8>(P, s);
+hipError_t launch_batch(const FewParams& P, hipStream_t s) {
+  hipError_t e = P.T <= 8    ? launch_up_batch<MX, 1>(P, s)
+                 : P.T <= 16 ? launch_up_batch<MX, 2>(P, s)
+                 : P.T <= 32 ? launch_up_batch<MX, 4>(P, s)
+                             : launch_up_batch<MX, 8>(P, s);
+  if (e != hipSuccess) return e;
+  return P.T <= 8    ? launch_down_batch<MX, 2>(P, s)
+         : P.T <= 16 ? launch_down_batch<MX, 4>(P, s)
+                     : launch_down_batch<MX, 8>(P, s);
+}
+
+template <bool MX>
+hipError_t launch_few(const FewParams& P, hipStream_t s) {
+  const hipError_t e = P.T <= kDirect ? launch_direct<MX>(P, s)
+                                      : launch_batch<MX>(P, s);
+  if (e != hipSuccess || P.parts == 1) return e;
+  const int64_t n = static_cast<int64_t>(P.T) * P.d;
+  hipLaunchKernelGGL(few_sum_kernel,
+                     dim3(static_cast<uint32_t>((n + 1023) / 1024)), dim3(256),
+                     0, s, P.part, P.parts, n, P.y_add, P.y);
+  return hipGetLastError();
+}
+
+// Parts that the reduction of y is cut into, so that all CUs have work, but
+// not more than its steps allow.
+int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
+  const int64_t most = most_units(static_cast<int>(T), k, E);
+  if (T <= kDirect) {
+    const int64_t items = most * ((f + kChunkK - 1) / kChunkK);
+    int parts = 1;
+    while (parts < 8 && d / kRows * parts * 2 <= 256 &&
+           items >= parts * 2 * kDownWaves)
+      parts *= 2;
+    return parts;
+  }
+  // a multiple of 8: workgroups of the same part then lie on the same XCD,
+  // whose L2 holds the part's rows of S
+  const int64_t steps = most * ((f + 255) / 256);
+  const int64_t groups = (d + kBatchRows - 1) / kBatchRows;
+  int parts = 8;
+  while (parts < 32 && groups * parts < 512 && steps >= parts * 8) parts *= 2;
+  return parts;
+}
+
+// Workspace: S, the parts' sums.
+struct FewLayout {
+  int parts;
+  size_t part, total;
+};
+size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
+FewLayout few_layout(int64_t T, int k, int E, int64_t d, int64_t f) {
+  FewLayout w;
+  w.parts = down_parts(T, k, E, d, f);
+  w.part = up256(static_cast<size_t>(T * k * f * 4));
+  w.total = w.part + up256(static_cast<size_t>(
+                         w.parts > 1 ? w.parts * T * d * 4 : 0));
+  return w;
 }
 
 }  // namespace
 
-size_t layer_fwd_workspace(int64_t T, int E, int k, int64_t f) {
-  return (static_cast<size_t>(T * k * f * 2) + 255) & ~size_t{255};
+size_t layer_fwd_workspace(int64_t T, int k, int E, int64_t d, int64_t f) {
+  return few_layout(T, k, E, d, f).total;
 }
 
 hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
                             hipStream_t s) {
-  hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
-                     a.x, a.w_g, a.bias, a.logits, a.d, a.E, a.k, a.renorm,
-                     a.topk_idx, a.topk_w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  const FewLayout w = few_layout(a.T, a.k, a.E, a.d, a.f);
   FewParams P{};
   P.x = a.x;
   P.w_gu = static_cast<const uint8_t*>(a.w_gu);
@@ -545,13 +1212,20 @@ hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
   P.s = static_cast<bf16_t*>(ws);
   P.y_add = a.y_add;
   P.y = a.y;
+  P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.part);
   P.T = a.T;
   P.d = a.d;
   P.f = a.f;
   P.E = a.E;
   P.k = a.k;
-  P.slots = a.T * a.k < a.E;
-  return mx ? launch_blocks<true>(P, s) : launch_blocks<false>(P, s);
+  P.parts = w.parts;
+  P.inv_k = (65536 + a.k - 1) / a.k;
+  hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
+                     a.x, a.w_g, a.bias, a.logits, a.d, a.E, a.k, a.renorm,
+                     a.topk_idx, a.topk_w);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return mx ? launch_few<true>(P, s) : launch_few<false>(P, s);
 }
 
 }  // namespace moe
