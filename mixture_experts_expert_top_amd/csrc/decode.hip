@@ -29,6 +29,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -306,17 +308,20 @@ __device__ __forceinline__ f32x4 mma(bf16x8_v a, bf16x8_v b, f32x4 c) {
 // --------------------------------------------------------- reached experts
 // The experts that are reached, in order, with the slots of their tokens, in
 // the front of a kernel's dynamic LDS.
+struct Expert {
+  uint16_t id, first, members, tokens;  // tokens: the mask of tokens 0 to 15
+};
 struct Units {
   uint64_t* mask;       // [E] tokens of an expert
+  Expert* expert;       // [E] reached experts, in order
   float* wt;            // [T k] weight of a slot
   uint16_t* slot;       // [T k] slots, those of an expert in a row
   uint16_t* first;      // [E] where an expert's are
-  uint16_t* expert;     // [E] reached experts, in order
   int count;
 
   // bytes for E experts and n slots, a multiple of 16
   __host__ __device__ static int bytes(int E, int n) {
-    return (E * 12 + n * 6 + 4 + 15) & ~15;
+    return (E * 18 + n * 6 + 4 + 15) & ~15;
   }
 };
 
@@ -328,19 +333,17 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
   const int n = P.T * P.k, E = P.E;
   Units U;
   U.mask = reinterpret_cast<uint64_t*>(lds);
-  U.wt = reinterpret_cast<float*>(U.mask + E);
+  U.expert = reinterpret_cast<Expert*>(U.mask + E);
+  U.wt = reinterpret_cast<float*>(U.expert + E);
   int* const count_at = reinterpret_cast<int*>(U.wt + n);
   U.slot = reinterpret_cast<uint16_t*>(count_at + 1);
   U.first = U.slot + n;
-  U.expert = U.first + E;
   if (P.T == 1) {                     // every slot, in its own order
     if (tid < n) {
-      const int e = P.idx[tid];
+      const uint16_t i = static_cast<uint16_t>(tid);
       U.wt[tid] = P.wt[tid];
-      U.expert[tid] = static_cast<uint16_t>(e);
-      U.mask[e] = 1;
-      U.first[e] = static_cast<uint16_t>(tid);
-      U.slot[tid] = static_cast<uint16_t>(tid);
+      U.expert[tid] = Expert{static_cast<uint16_t>(P.idx[tid]), i, 1, 1};
+      U.slot[tid] = i;
     }
     __syncthreads();
     U.count = n;
@@ -370,7 +373,8 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
     int count = 0, first = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
-      const int c = e < E ? __popcll(U.mask[e]) : 0;
+      const uint64_t mask = e < E ? U.mask[e] : 0;
+      const int c = __popcll(mask);
       const uint64_t act = __ballot(c > 0);
       int incl = c;
 #pragma unroll
@@ -378,10 +382,12 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
         const int o = __shfl_up(incl, m, kWave);
         if (lane >= m) incl += o;
       }
-      if (e < E) U.first[e] = static_cast<uint16_t>(first + incl - c);
+      const uint16_t at = static_cast<uint16_t>(first + incl - c);
+      if (e < E) U.first[e] = at;
       if (c)
         U.expert[count + __popcll(act & ((uint64_t{1} << lane) - 1))] =
-            static_cast<uint16_t>(e);
+            Expert{static_cast<uint16_t>(e), at, static_cast<uint16_t>(c),
+                   static_cast<uint16_t>(mask)};
       count += __popcll(act);
       first += __shfl(incl, 63, kWave);
     }
@@ -401,17 +407,26 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
   *out = U;
 }
 
+// A reached expert in scalar registers.
+struct Reached {
+  int id, first, members, tokens;
+  __device__ __forceinline__ void read(const Units& U, int un) {
+    const i32x2 v = *reinterpret_cast<const i32x2*>(&U.expert[un]);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(v[0]);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(v[1]);
+    id = static_cast<int>(lo & 0xffff);
+    first = static_cast<int>(lo >> 16);
+    members = static_cast<int>(hi & 0xffff);
+    tokens = static_cast<int>(hi >> 16);
+  }
+};
+
 // ---------------------------------------------------------------- gate, up
-// One reached expert, as its gate and up projection sees it.
+// The weights of an expert's gate and up projection.
 template <bool MX>
-struct UpExpert {
+struct UpWeights {
   __amdgpu_buffer_rsrc_t rw, rs;
-  int first, members;
-  __device__ __forceinline__ UpExpert(const FewParams& P, const Units& U,
-                                      int un) {
-    const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
-    first = __builtin_amdgcn_readfirstlane(U.first[e]);
-    members = __builtin_amdgcn_readfirstlane(__popcll(U.mask[e]));
+  __device__ __forceinline__ UpWeights(const FewParams& P, int e) {
     const int64_t per = static_cast<int64_t>(2) * P.f * P.d;
     rw = make_rsrc(P.w_gu + e * per * (MX ? 1 : 2),
                    static_cast<uint32_t>(per * (MX ? 1 : 2)));
@@ -439,7 +454,9 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
                                          int un, int t0, int t1,
                                          float* __restrict__ red, int* flip) {
   const Lane<MX> L;
-  const UpExpert<MX> X(P, U, un);
+  Reached X;
+  X.read(U, un);
+  const UpWeights<MX> W(P, X.id);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = P.d;
@@ -453,37 +470,32 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
   const int slot = mine < X.members ? U.slot[X.first + mine] : -1;
   const float wt = slot >= 0 ? U.wt[slot] : 0.0f;
   // A wave's chunks of a tile, then the next tile's: one is in flight while
-  // the one before it is multiplied.  Loads past the last are masked and
-  // issued all the same: with a branch around them the compiler would wait
-  // for all that is in flight.
+  // the one before it is multiplied.  The last is taken out of the loop: a
+  // branch around its loads would make the compiler wait for all that is in
+  // flight, every time.
   struct Item {
     Weights<MX> g, u;
     Tokens<MX> x;
   };
   auto load = [&](Item& it, int tile, int k0) {
     const int n = tile * kRows + L.r;
-    const int k = tile < t1 ? k0 : K;
-    it.g.load(X.rw, X.rs, X.row(P, n, false), k, K, L);
-    it.u.load(X.rw, X.rs, X.row(P, n, true), k, K, L);
-    it.x.load(rx, tok, k, K, L);
+    it.g.load(W.rw, W.rs, W.row(P, n, false), k0, K, L);
+    it.u.load(W.rw, W.rs, W.row(P, n, true), k0, K, L);
+    it.x.load(rx, tok, k0, K, L);
     __builtin_amdgcn_sched_barrier(0);
   };
   const int rounds = (K + kUpWaves * kChunkK - 1) / (kUpWaves * kChunkK);
   Item nxt;
   load(nxt, t0, wave * kChunkK);
-  for (int tile = t0; tile < t1; ++tile) {
-    f32x4 ag = {}, au = {};
-    for (int c = 0; c < rounds; ++c) {
-      const Item cur = nxt;
-      const bool last = c + 1 == rounds;
-      load(nxt, last ? tile + 1 : tile,
-           ((last ? 0 : c + 1) * kUpWaves + wave) * kChunkK);
+  f32x4 ag = {}, au = {};
+  auto multiply = [&](const Item& cur) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ag = mma(cur.g.frag(i, L), cur.x.frag(i), ag);
-        au = mma(cur.u.frag(i, L), cur.x.frag(i), au);
-      }
+    for (int i = 0; i < 4; ++i) {
+      ag = mma(cur.g.frag(i, L), cur.x.frag(i), ag);
+      au = mma(cur.u.frag(i, L), cur.x.frag(i), au);
     }
+  };
+  auto finish = [&](int tile) {
     // red[wave][gate, up][lane][4]: row 4 (lane / 16) + v, token lane % 16.
     // A wave that still adds up one buffer passes the next barrier before
     // anyone writes to that buffer again.
@@ -513,7 +525,21 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
         o[P.f] = f2bf(h - bf2f(hi));
       }
     }
+    ag = au = f32x4{};
+  };
+  int tile = t0, c = 0;
+  for (int left = (t1 - t0) * rounds; left > 1; --left) {
+    const Item cur = nxt;
+    const bool last = c + 1 == rounds;
+    const int now = tile;
+    c = last ? 0 : c + 1;
+    tile += last;
+    load(nxt, tile, (c * kUpWaves + wave) * kChunkK);
+    multiply(cur);
+    if (last) finish(now);
   }
+  multiply(nxt);
+  finish(tile);
 }
 
 // All tiles of all reached experts in order, divided evenly over the
@@ -580,14 +606,40 @@ __device__ __forceinline__ int swizzle(int c) {
   return MX ? c : (c & 3) | ((c & 4) << 1);
 }
 
-// Source: what step q of [begin, end) reads and what becomes of its sums
-//   weights(q, a, b): loads of the wave's two tiles
-//   column(q, c, b): byte offset of column c of block b in its resource, kOob
-//     for none; k(q): the step's first k (K for none); rx, K
-//   done(q, a, b): called with the sums at every step; true clears them
+// Where a batch stands: step (expert, part of it, round of k), one for the
+// columns, one for the weights and one for the sums.
+struct Cursor {
+  int left, un, mid, r;               // left: steps from here on
+  Reached X;
+  __device__ __forceinline__ Cursor(const Units& U, int begin, int end,
+                                    int mids, int rounds)
+      : left(end - begin) {
+    const int t = begin / rounds;
+    r = begin - t * rounds;
+    un = t / mids;
+    mid = t - un * mids;
+    X.read(U, un);
+  }
+  __device__ __forceinline__ void next(const Units& U, int mids, int rounds) {
+    --left;
+    if (++r < rounds) return;
+    r = 0;
+    if (++mid < mids) return;
+    mid = 0;
+    ++un;
+    if (left > 0) X.read(U, un);
+  }
+};
+
+// Steps [begin, end) of a Source, which says what a step reads and what
+// becomes of the sums:
+//   weights(cursor, a, b): loads the wave's two tiles
+//   column(cursor, c, b): byte offset of column c of block b in rx, kOob for
+//     none; K: the columns' length
+//   done(cursor, a, b): called at every step; true clears the sums
 template <bool MX, int NB, class Source>
-__device__ __forceinline__ void batch(Source& src, int begin, int end,
-                                      uint8_t* xs) {
+__device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
+                                      int end, uint8_t* xs) {
   using H = BatchShape<MX, NB>;
   constexpr int D = H::kAhead;
   static_assert(D % 2 == 0, "the LDS buffer is a compile-time constant");
@@ -599,20 +651,26 @@ __device__ __forceinline__ void batch(Source& src, int begin, int end,
   };
   Columns cx[2];
   Weights<MX, H::kStepK> wa[D], wb[D];
-  auto load_columns = [&](Columns& x, int q) {
-    const int k0 = src.k(q);
+  Cursor at_x(U, begin, end, src.mids, src.rounds), at_w = at_x, at = at_x;
+  auto load_columns = [&](Columns& x) {
+    const int k0 = at_x.left > 0 ? at_x.r * H::kStepK : src.K;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int j = 0; j < H::kLoads; ++j) {
         const int id = tid + j * kBatchThreads;
         const int c = id / H::kPieces, k = k0 + (id % H::kPieces) * 8;
-        const uint32_t at = src.column(q, c, b);
+        const uint32_t o = src.column(at_x, c, b);
         x.v[b * H::kLoads + j] = buf_load16(
-            src.rx, k < src.K && at != kOob
-                        ? at + static_cast<uint32_t>(k) * 2
-                        : kOob);
+            src.rx, k < src.K && o != kOob ? o + static_cast<uint32_t>(k) * 2
+                                           : kOob);
       }
+    at_x.next(U, src.mids, src.rounds);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto load_weights = [&](int u) {
+    src.weights(at_w, wa[u], wb[u]);
+    at_w.next(U, src.mids, src.rounds);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto store_columns = [&](const Columns& x, uint8_t* to) {
@@ -633,25 +691,23 @@ __device__ __forceinline__ void batch(Source& src, int begin, int end,
                      : i * 8 + (fr >> 3) * 4 + g;
     return (col * H::kPieces + (p ^ swizzle<MX>(col))) * 16;
   };
-  load_columns(cx[0], begin);
-  load_columns(cx[1], begin + 1);
+  load_columns(cx[0]);
+  load_columns(cx[1]);
 #pragma unroll
-  for (int i = 0; i < D; ++i) {
-    src.weights(begin + i, wa[i], wb[i]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
+  for (int i = 0; i < D; ++i) load_weights(i);
   store_columns(cx[0], xs);
   __syncthreads();
   f32x4 a[NB], b[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) a[i] = b[i] = f32x4{};
-  for (int q0 = begin; q0 < end; q0 += D)
+  // D steps; the last of a batch (kMore false) request nothing
+  auto steps = [&](auto more) {
+    constexpr bool kMore = decltype(more)::value;
 #pragma unroll
     for (int u = 0; u < D; ++u) {
-      const int q = q0 + u;
       uint8_t* const now = xs + (u & 1) * H::kBytes;
       uint8_t* const then = xs + ((u & 1) ^ 1) * H::kBytes;
-      load_columns(cx[u & 1], q + 2);
+      if (kMore || u + 2 < D) load_columns(cx[u & 1]);
 #pragma unroll
       for (int i = 0; i < H::kStepK / 64; ++i) {
         const bf16x8_v fa = wa[u].frag(i, L), fb = wb[u].frag(i, L);
@@ -664,15 +720,20 @@ __device__ __forceinline__ void batch(Source& src, int begin, int end,
           b[n] = mma(fb, x, b[n]);
         }
       }
-      src.weights(q + D, wa[u], wb[u]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (src.done(q, a, b))
+      if (kMore) load_weights(u);
+      if (at.left > 0 && src.done(at, a, b))
 #pragma unroll
         for (int i = 0; i < NB; ++i) a[i] = b[i] = f32x4{};
-      // the other buffer: its last reads were before the last barrier
-      store_columns(cx[(u & 1) ^ 1], then);
-      __syncthreads();
+      at.next(U, src.mids, src.rounds);
+      if (kMore || u + 1 < D) {
+        // the other buffer: its last reads were before the last barrier
+        store_columns(cx[(u & 1) ^ 1], then);
+        __syncthreads();
+      }
     }
+  };
+  for (int q = begin; q + D < end; q += D) steps(std::true_type{});
+  steps(std::false_type{});
 }
 
 // Adds the two halves of k: rows 0-7 with columns 0-7 (lanes below 32 of
@@ -691,60 +752,43 @@ struct UpSource {
   const FewParams& P;
   const Units& U;
   __amdgpu_buffer_rsrc_t rx;
-  int K, rounds, groups, end, wave;
+  int K, rounds, mids, wave;
   Lane<MX> L;
 
-  __device__ __forceinline__ UpSource(const FewParams& p, const Units& u,
-                                      int last)
+  __device__ __forceinline__ UpSource(const FewParams& p, const Units& u)
       : P(p), U(u),
         rx(make_rsrc(p.x, static_cast<uint32_t>(p.T) * p.d * 2)), K(p.d),
         rounds((p.d + H::kStepK - 1) / H::kStepK),
-        groups((p.f + 4 * kRows - 1) / (4 * kRows)), end(last),
+        mids((p.f + 4 * kRows - 1) / (4 * kRows)),
         wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {}
-  // (expert, group, round) of a step
-  __device__ __forceinline__ void split(int q, int* un, int* gr,
-                                        int* r) const {
-    const int t = q / rounds;
-    *r = q - t * rounds;
-    *un = t / groups;
-    *gr = t - *un * groups;
-  }
-  __device__ __forceinline__ int k(int q) const {
-    return q < end ? (q % rounds) * H::kStepK : K;
-  }
-  __device__ __forceinline__ uint32_t column(int q, int c, int b) const {
-    if (q >= end) return kOob;
-    const int e = U.expert[q / rounds / groups];
+  __device__ __forceinline__ uint32_t column(const Cursor& at, int c,
+                                             int b) const {
     const int m = b * 8 + c;
-    return m < __popcll(U.mask[e])
-               ? static_cast<uint32_t>(P.token(U.slot[U.first[e] + m])) * K * 2
+    return m < at.X.members
+               ? static_cast<uint32_t>(P.token(U.slot[at.X.first + m])) * K * 2
                : kOob;
   }
-  __device__ __forceinline__ void weights(int q, Weights<MX, H::kStepK>& a,
+  __device__ __forceinline__ void weights(const Cursor& at,
+                                          Weights<MX, H::kStepK>& a,
                                           Weights<MX, H::kStepK>& b) const {
-    int un = 0, gr = 0, r = 0;
-    if (q < end) split(q, &un, &gr, &r);
-    const UpExpert<MX> X(P, U, un);
-    const int n = (gr * kBatchWaves + wave) * kRows;
-    const int k0 = q < end && n < P.f ? r * H::kStepK : K;
-    a.load(X.rw, X.rs, X.row(P, n + L.r, false), k0, K, L);
-    b.load(X.rw, X.rs, X.row(P, n + L.r, true), k0, K, L);
+    const UpWeights<MX> W(P, at.X.id);
+    const int n = (at.mid * kBatchWaves + wave) * kRows;
+    const int k0 = at.left > 0 && n < P.f ? at.r * H::kStepK : K;
+    a.load(W.rw, W.rs, W.row(P, n + L.r, false), k0, K, L);
+    b.load(W.rw, W.rs, W.row(P, n + L.r, true), k0, K, L);
   }
-  __device__ __forceinline__ bool done(int q, const f32x4* a,
+  __device__ __forceinline__ bool done(const Cursor& at, const f32x4* a,
                                        const f32x4* b) const {
-    if (q >= end) return false;
-    int un, gr, r;
-    split(q, &un, &gr, &r);
-    if (r + 1 < rounds) return false;
+    if (at.r + 1 < rounds) return false;
     const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
-    const int e = U.expert[un], members = __popcll(U.mask[e]);
-    const int n = (gr * kBatchWaves + wave) * kRows;
+    const int n = (at.mid * kBatchWaves + wave) * kRows;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
+      if (i * 8 >= at.X.members) break;
       const f32x4 ga = join_halves(a[i]), up = join_halves(b[i]);
       const int m = i * 8 + c;
-      if (c >= 8 || qr >= 2 || m >= members || n >= P.f) continue;
-      const int slot = U.slot[U.first[e] + m];
+      if (c >= 8 || qr >= 2 || m >= at.X.members || n >= P.f) continue;
+      const int slot = U.slot[at.X.first + m];
       const float wt = U.wt[slot];
       float h[4], l[4];
 #pragma unroll
@@ -769,7 +813,7 @@ struct UpSource {
 __device__ __forceinline__ int most_members(const Units& U, int u0, int u1) {
   int most = 0;
   for (int u = u0 + lane_id(); u < u1; u += kWave)
-    most = max(most, __popcll(U.mask[U.expert[u]]));
+    most = max(most, static_cast<int>(U.expert[u].members));
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) most = max(most, shfl_xor(most, m));
   return __builtin_amdgcn_readfirstlane(most);
@@ -778,10 +822,8 @@ __device__ __forceinline__ int most_members(const Units& U, int u0, int u1) {
 template <bool MX, int NB>
 __device__ __forceinline__ void up_batch(const FewParams& P, const Units& U,
                                          int first, int last, uint8_t* xs) {
-  constexpr int kStepK = BatchShape<MX, NB>::kStepK;
-  const int rounds = (P.d + kStepK - 1) / kStepK;
-  UpSource<MX, NB> src(P, U, last * rounds);
-  batch<MX, NB>(src, first * rounds, last * rounds, xs);
+  UpSource<MX, NB> src(P, U);
+  batch<MX, NB>(src, U, first * src.rounds, last * src.rounds, xs);
 }
 
 // MAXB: blocks of 8 that T tokens can fill.
@@ -820,70 +862,50 @@ struct DownSource {
   const FewParams& P;
   const Units& U;
   __amdgpu_buffer_rsrc_t rx;
-  int K, rounds, passes, end, n0;
+  int K, rounds, mids, n0;
   float* plane;                       // [T][16], the wave's
   Lane<MX> L;
 
   __device__ __forceinline__ DownSource(const FewParams& p, const Units& u,
-                                        int last, int most, int row0,
-                                        float* sums)
+                                        int most, int row0, float* sums)
       : P(p), U(u),
         rx(make_rsrc(p.s, static_cast<uint32_t>(p.T) * p.k * 4 * p.f)),
         K(p.f), rounds((p.f + H::kStepK - 1) / H::kStepK),
-        passes((most + kMembers - 1) / kMembers), end(last), n0(row0),
-        plane(sums) {}
-  // (expert, pass, round) of a step
-  __device__ __forceinline__ void split(int q, int* un, int* ps,
-                                        int* r) const {
-    const int t = q / rounds;
-    *r = q - t * rounds;
-    *un = t / passes;
-    *ps = t - *un * passes;
-  }
-  __device__ __forceinline__ int k(int q) const {
-    return q < end ? (q % rounds) * H::kStepK : K;
-  }
-  __device__ __forceinline__ uint32_t column(int q, int c, int b) const {
-    if (q >= end) return kOob;
-    int un, ps, r;
-    split(q, &un, &ps, &r);
-    const int e = U.expert[un];
-    const int m = ps * kMembers + b * 4 + (c >> 1);
-    return m < __popcll(U.mask[e])
-               ? (static_cast<uint32_t>(U.slot[U.first[e] + m]) * 2 +
+        mids((most + kMembers - 1) / kMembers), n0(row0), plane(sums) {}
+  __device__ __forceinline__ uint32_t column(const Cursor& at, int c,
+                                             int b) const {
+    const int m = at.mid * kMembers + b * 4 + (c >> 1);
+    return m < at.X.members
+               ? (static_cast<uint32_t>(U.slot[at.X.first + m]) * 2 +
                   (c & 1)) * K * 2
                : kOob;
   }
-  __device__ __forceinline__ void weights(int q, Weights<MX, H::kStepK>& a,
+  __device__ __forceinline__ void weights(const Cursor& at,
+                                          Weights<MX, H::kStepK>& a,
                                           Weights<MX, H::kStepK>& b) const {
-    int un = 0, ps = 0, r = 0;
-    if (q < end) split(q, &un, &ps, &r);
-    const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
-    const bool in = q < end && n0 < P.d;
-    const int64_t at = (e * static_cast<int64_t>(P.d) + (in ? n0 : 0)) * K;
+    // an expert without members in this pass is not read
+    const bool in = at.left > 0 && n0 < P.d &&
+                    at.mid * kMembers < at.X.members;
+    const int64_t o = (at.X.id * static_cast<int64_t>(P.d) + (in ? n0 : 0)) *
+                      K;
     const uint32_t rows = static_cast<uint32_t>(in ? min(16, P.d - n0) : 0);
-    const auto rw = make_rsrc(P.w2 + at * (MX ? 1 : 2),
+    const auto rw = make_rsrc(P.w2 + o * (MX ? 1 : 2),
                               rows * K * (MX ? 1 : 2));
     const auto rs =
-        MX ? make_rsrc(P.w2_scales + at / 32, rows * K / 32) : rw;
+        MX ? make_rsrc(P.w2_scales + o / 32, rows * K / 32) : rw;
     const uint32_t row = static_cast<uint32_t>(L.r) * K * (MX ? 1 : 2);
-    // an expert without members in this pass is not read
-    const bool some = ps == 0 || ps * kMembers < __popcll(U.mask[e]);
-    const int k0 = in && some ? r * H::kStepK : K;
+    const int k0 = in ? at.r * H::kStepK : K;
     a.load(rw, rs, row, k0, K, L);
     b.load(rw, rs, row + static_cast<uint32_t>(kRows) * K * (MX ? 1 : 2),
-           n0 + kRows < P.d ? k0 : K, K, L);
+           rows > kRows ? k0 : K, K, L);
   }
-  __device__ __forceinline__ bool done(int q, const f32x4* a,
+  __device__ __forceinline__ bool done(const Cursor& at, const f32x4* a,
                                        const f32x4* b) const {
-    if (q >= end) return false;
-    int un, ps, r;
-    split(q, &un, &ps, &r);
-    if (r + 1 < rounds && q + 1 < end) return false;
+    if (at.r + 1 < rounds && at.left > 1) return false;
     const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
-    const int e = U.expert[un], members = __popcll(U.mask[e]);
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
+      if (at.mid * kMembers + i * 4 >= at.X.members) break;
       f32x4 s0 = join_halves(a[i]), s1 = join_halves(b[i]);
       // S's two parts stand in neighbouring columns
 #pragma unroll
@@ -891,10 +913,10 @@ struct DownSource {
         s0[v] += dpp_move<kDppXor1>(s0[v]);
         s1[v] += dpp_move<kDppXor1>(s1[v]);
       }
-      const int m = ps * kMembers + i * 4 + (c >> 1);
-      if (c >= 8 || (c & 1) || qr >= 2 || m >= members) continue;
+      const int m = at.mid * kMembers + i * 4 + (c >> 1);
+      if (c >= 8 || (c & 1) || qr >= 2 || m >= at.X.members) continue;
       f32x4* const o = reinterpret_cast<f32x4*>(
-          plane + P.token(U.slot[U.first[e] + m]) * 16 + qr * 4);
+          plane + P.token(U.slot[at.X.first + m]) * 16 + qr * 4);
       o[0] += s0;
       o[2] += s1;
     }
@@ -906,15 +928,11 @@ template <bool MX, int NB>
 __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
                                            int part, int most, int n0,
                                            float* plane, uint8_t* xs) {
-  constexpr int kStepK = BatchShape<MX, NB>::kStepK;
-  const int rounds = (P.f + kStepK - 1) / kStepK;
-  const int passes = (most + 4 * NB - 1) / (4 * NB);
-  const int64_t total = static_cast<int64_t>(U.count) * passes * rounds;
+  DownSource<MX, NB> src(P, U, most, n0, plane);
+  const int64_t total = static_cast<int64_t>(U.count) * src.mids * src.rounds;
   const int begin = static_cast<int>(total * part / P.parts);
   const int end = static_cast<int>(total * (part + 1) / P.parts);
-  if (begin >= end) return;
-  DownSource<MX, NB> src(P, U, end, most, n0, plane);
-  batch<MX, NB>(src, begin, end, xs);
+  if (begin < end) batch<MX, NB>(src, U, begin, end, xs);
 }
 
 // MAXB: blocks of 4 members that T tokens can fill, up to 8.
@@ -987,14 +1005,20 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     Weights<MX> w;
     Tokens<MX> x;
   };
-  // item q of a tile; past the last item or tile: masked
-  auto load = [&](Item& it, int tile, int q) {
-    const bool in = q < total && tile < tiles;
-    const int un = in ? q / chunks : 0;
-    const int k0 = in ? (q - un * chunks) * kChunkK : K;
-    const int e = __builtin_amdgcn_readfirstlane(U.expert[un]);
+  // items of a tile are dealt in turn to the waves of all parts; a wave makes
+  // `rounds` of them, a multiple of kAhead, the last ones masked
+  const int step = kDownWaves * P.parts;
+  const int rounds = ((total + step - 1) / step + kAhead - 1) / kAhead *
+                     kAhead;
+  int l_tile = group, l_left = rounds, l_q = part * kDownWaves + wave;
+  auto load = [&](Item& it) {
+    const bool in = l_q < total;
+    const int un = in ? l_q / chunks : 0;
+    const int k0 = in ? (l_q - un * chunks) * kChunkK : K;
+    Reached X;
+    X.read(U, un);
     const int64_t at =
-        e * per + static_cast<int64_t>(in ? tile * kRows : 0) * K;
+        X.id * per + static_cast<int64_t>(l_tile * kRows) * K;
     const auto rw = make_rsrc(
         P.w2 + at * (MX ? 1 : 2),
         static_cast<uint32_t>(kRows) * K * (MX ? 1 : 2));
@@ -1002,41 +1026,30 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
                                    static_cast<uint32_t>(kRows) * K / 32)
                        : rw;
     it.w.load(rw, rs, row, k0, K, L);
-    const uint32_t mask = static_cast<uint32_t>(U.mask[e]);
-    const bool has = (mask >> t) & 1;
-    const int sl = U.slot[U.first[e] + (has ? __popc(mask & ((1u << t) - 1))
-                                            : 0)];
+    const bool has = (X.tokens >> t) & 1;
+    const int sl = U.slot[X.first +
+                          (has ? __popc(X.tokens & ((1 << t) - 1)) : 0)];
     it.x.load(rx,
               has ? static_cast<uint32_t>(sl * 2 + (L.r & 1)) * K * 2 : kOob,
               k0, K, L);
+    l_q += step;
+    if (--l_left == 0) {
+      l_left = rounds;
+      l_q = part * kDownWaves + wave;
+      l_tile += groups;
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
-  const int step = kDownWaves * P.parts;
-  const int q0 = part * kDownWaves + wave;
-  // rounds of a tile that all waves make, a multiple of kAhead
-  const int rounds = ((total + step - 1) / step + kAhead - 1) / kAhead *
-                     kAhead;
   Item it[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(it[i], group, q0 + i * step);
+  for (int i = 0; i < kAhead; ++i) load(it[i]);
+  f32x4 acc = {};
   int flip = 0;
-  for (int tile = group; tile < tiles; tile += groups) {
-    f32x4 acc = {};
-    for (int c = 0; c < rounds; c += kAhead) {
-      const bool last = c + kAhead == rounds;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          acc = mma(it[i].w.frag(s, L), it[i].x.frag(s), acc);
-        load(it[i], last ? tile + groups : tile,
-             q0 + (last ? i : c + kAhead + i) * step);
-      }
-    }
+  auto finish = [&](int tile) {
     float* const r = red + flip * (kDownWaves * 256);
     *reinterpret_cast<f32x4*>(r + (wave * 64 + lane) * 4) = acc;
     __syncthreads();
-    // as in up_few a buffer is free again after the next barrier
+    // as in up_tiles a buffer is free again after the next barrier
     if (wave == flip) {
       const int n = lane & 7, c = lane >> 3;
       // the two halves of k: rows and columns 0-7, and 8-15
@@ -1059,7 +1072,31 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
       }
     }
     flip ^= 1;
+    acc = f32x4{};
+  };
+  auto multiply = [&](const Item& c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc = mma(c.w.frag(s, L), c.x.frag(s), acc);
+  };
+  int tile = group, c = 0;
+  // kAhead items a time; the last are taken out of the loop, as in up_tiles
+  for (int left = (tiles - group + groups - 1) / groups * rounds;
+       left > kAhead; left -= kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      multiply(it[i]);
+      load(it[i]);
+    }
+    c += kAhead;
+    if (c == rounds) {
+      finish(tile);
+      tile += groups;
+      c = 0;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) multiply(it[i]);
+  finish(tile);
 }
 
 // y = y_add + the parts in order; n values, a multiple of 8.
