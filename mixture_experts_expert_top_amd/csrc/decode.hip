@@ -54,13 +54,48 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + shfl_xor(v, 32);
 }
 
-__global__ __launch_bounds__(kRouteThreads) void few_route_kernel(
+// Scores: a wave an expert and token, 4 KB of both in flight.
+constexpr int kLogitThreads = 256;
+constexpr int kLogitWaves = kLogitThreads / kWave;
+
+__global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
     const bf16_t* __restrict__ x, const bf16_t* __restrict__ w_g,
-    const float* __restrict__ bias, const float* __restrict__ logits, int d,
-    int E, int k, int renorm, int32_t* __restrict__ idx,
-    float* __restrict__ wt) {
+    const float* __restrict__ bias, int d, int E, float* __restrict__ logits) {
+  const int lane = threadIdx.x & 63;
+  const int e = __builtin_amdgcn_readfirstlane(
+      blockIdx.x * kLogitWaves + (threadIdx.x >> 6));
+  const int t = blockIdx.y;
+  if (e >= E) return;
+  const auto rx = make_rsrc(x + static_cast<int64_t>(t) * d, d * 2);
+  const auto rw = make_rsrc(w_g + static_cast<int64_t>(e) * d, d * 2);
+  // loads past the row read zeros
+  float acc = 0.0f;
+  for (int k0 = lane * 16; k0 < d * 2; k0 += 4096) {
+    i32x4 xv[4], wv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      xv[u] = buf_load16(rx, k0 + u * 1024);
+      wv[u] = buf_load16(rw, k0 + u * 1024);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a = xv[u][q], b = wv[u][q];
+        acc = fmaf(bf_lo(a), bf_lo(b), acc);
+        acc = fmaf(bf_hi(a), bf_hi(b), acc);
+      }
+  }
+  const float z = wave_sum(acc);
+  if (lane == 0)
+    logits[static_cast<int64_t>(t) * E + e] = bias ? z + bias[e] : z;
+}
+
+// The choice of one token from its scores, any number of experts.
+__global__ __launch_bounds__(kRouteThreads) void few_topk_kernel(
+    const float* __restrict__ logits, int E, int k, int renorm,
+    int32_t* __restrict__ idx, float* __restrict__ wt) {
   __shared__ float s_z[kMaxExperts];
-  __shared__ float s_part[kMaxExperts];      // [cut][E]: cuts * E <= 64, or E
   __shared__ __attribute__((aligned(16))) uint32_t s_key[kMaxExperts];
   __shared__ int s_place[kMaxExperts];
   __shared__ int s_idx[kMaxTopK];
@@ -68,68 +103,14 @@ __global__ __launch_bounds__(kRouteThreads) void few_route_kernel(
   __shared__ float s_sum[kRouteWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t = blockIdx.x;
-  if (w_g) {
-    // Groups of four experts go to the waves; where there are fewer groups
-    // than waves the reduction is cut into `cuts` too.  A wave has 4 x 512 k
-    // of its experts in flight.
-    const int groups = (E + 3) / 4;
-    int cuts = 1;
-    while (2 * cuts * groups <= kRouteWaves) cuts *= 2;
-    const int steps = (d + 511) / 512;
-    const int per = (steps + cuts - 1) / cuts;        // steps of a cut
-    const auto rx = make_rsrc(x + static_cast<int64_t>(t) * d, d * 2);
-    for (int item = wave; item < groups * cuts; item += kRouteWaves) {
-      const int cut = item / groups, e0 = (item - cut * groups) * 4;
-      const int ne = min(4, E - e0);
-      const auto rw = make_rsrc(w_g + static_cast<int64_t>(e0) * d,
-                                static_cast<uint32_t>(ne) * d * 2);
-      const int end = min(steps, (cut + 1) * per);
-      float acc[4] = {};
-      for (int s0 = cut * per; s0 < end; s0 += 4) {
-        i32x4 xv[4], wv[4][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int k0 = (s0 + u) * 512 + lane * 8;
-          const bool ok = s0 + u < end && k0 < d;
-          xv[u] = buf_load16(rx, ok ? k0 * 2 : kOob);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            wv[u][i] = buf_load16(rw, ok && i < ne ? (i * d + k0) * 2 : kOob);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t a = xv[u][q], b = wv[u][i][q];
-              acc[i] = fmaf(bf_lo(a), bf_lo(b), acc[i]);
-              acc[i] = fmaf(bf_hi(a), bf_hi(b), acc[i]);
-            }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float z = wave_sum(acc[i]);
-        if (lane == 0 && i < ne) s_part[cut * E + e0 + i] = z;
-      }
-    }
-    __syncthreads();
-    if (tid < E) {
-      float z = s_part[tid];
-      for (int c = 1; c < cuts; ++c) z += s_part[c * E + tid];
-      s_z[tid] = bias ? z + bias[tid] : z;
-    }
-  } else if (tid < E) {
-    s_z[tid] = logits[static_cast<int64_t>(t) * E + tid];
-  }
-  __syncthreads();
   // An expert's place is the number of better ones.  The keys (padded to a
   // multiple of four that nothing is worse than) are compared by `segs`
   // threads an expert, each with its share of them.
   const int E4 = (E + 3) & ~3;
   if (tid < E4) {
-    s_key[tid] = tid < E ? score_key(s_z[tid]) : 0;
+    const float z = tid < E ? logits[static_cast<int64_t>(t) * E + tid] : 0.0f;
+    s_z[tid] = z;
+    s_key[tid] = tid < E ? score_key(z) : 0;
     s_place[tid] = 0;
   }
   __syncthreads();
@@ -171,6 +152,57 @@ __global__ __launch_bounds__(kRouteThreads) void few_route_kernel(
   }
 }
 
+// The same by one wave for up to 64 N experts, N a lane: its choices go to
+// idx[0 .. k) and wt.
+template <int N>
+__device__ __forceinline__ void choose(const float* __restrict__ z, int E,
+                                       int k, int renorm, int* idx,
+                                       float* wt) {
+  const int lane = lane_id();
+  float v[N];
+  uint32_t key[N];
+  int place[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = i * kWave + lane;
+    v[i] = e < E ? z[e] : 0.0f;
+    key[i] = e < E ? score_key(v[i]) : 0;
+    place[i] = e < E ? 0 : kMaxExperts;
+  }
+#pragma unroll
+  for (int h = 0; h < N; ++h) {
+    const int ne = min(kWave, E - h * kWave);
+    for (int j = 0; j < ne; ++j) {
+      const uint32_t o = static_cast<uint32_t>(
+          __builtin_amdgcn_readlane(static_cast<int>(key[h]), j));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        place[i] += o > key[i] ||
+                    (o == key[i] && h * kWave + j < i * kWave + lane);
+    }
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t b = __ballot(place[i] == 0);
+    if (b) top = __shfl(v[i], __ffsll(static_cast<unsigned long long>(b)) - 1,
+                        kWave);
+  }
+  float p[N], part = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = expf(v[i] - top);
+    if (i * kWave + lane < E && (!renorm || place[i] < k)) part += p[i];
+  }
+  const float sum = wave_sum(part);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (place[i] < k) {
+      idx[place[i]] = i * kWave + lane;
+      wt[place[i]] = p[i] / sum;
+    }
+}
+
 // ---------------------------------------------------------------- weights
 constexpr int kRows = 8;              // weight rows of a tile
 constexpr int kChunkK = 256;          // k a wave takes at a time
@@ -187,8 +219,10 @@ struct FewParams {
   const uint8_t* w_gu_scales;
   const uint8_t* w2;
   const uint8_t* w2_scales;
-  const int32_t* idx;                 // [T][k]
-  const float* wt;
+  int32_t* idx;                       // [T][k]
+  float* wt;
+  const float* logits;                // few_up_kernel: to choose from, or null
+  int renorm;
   bf16_t* s;                          // [T k][2][f]: S in two parts
   const bf16_t* y_add;
   bf16_t* y;
@@ -325,12 +359,27 @@ struct Units {
   }
 };
 
+// Up to kDirect tokens and 64 kChooseLanes experts: a wave of few_up_kernel
+// chooses for a token itself, in every workgroup, and the first one writes the
+// choices down.
+constexpr int kDirect = 4;
+constexpr int kChooseLanes = 2;
+
+struct Choices {
+  int idx[kDirect * kMaxTopK];
+  float wt[kDirect * kMaxTopK];
+};
+
+// own: the choices where the workgroup made them, else null.
 template <int kThreads>
 __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
-                                           Units* out) {
+                                           Units* out,
+                                           const Choices* own = nullptr) {
   constexpr int kPer = kFewTokens * kMaxTopK / kThreads;
   const int tid = threadIdx.x, lane = tid & 63;
   const int n = P.T * P.k, E = P.E;
+  const int* const idx = own ? own->idx : P.idx;
+  const float* const weights = own ? own->wt : P.wt;
   Units U;
   U.mask = reinterpret_cast<uint64_t*>(lds);
   U.expert = reinterpret_cast<Expert*>(U.mask + E);
@@ -341,8 +390,8 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
   if (P.T == 1) {                     // every slot, in its own order
     if (tid < n) {
       const uint16_t i = static_cast<uint16_t>(tid);
-      U.wt[tid] = P.wt[tid];
-      U.expert[tid] = Expert{static_cast<uint16_t>(P.idx[tid]), i, 1, 1};
+      U.wt[tid] = weights[tid];
+      U.expert[tid] = Expert{static_cast<uint16_t>(idx[tid]), i, 1, 1};
       U.slot[tid] = i;
     }
     __syncthreads();
@@ -355,8 +404,8 @@ __device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int i = tid + q * kThreads;
-    mine[q] = i < n ? P.idx[i] : -1;
-    wt[q] = i < n ? P.wt[i] : 0.0f;
+    mine[q] = i < n ? idx[i] : -1;
+    wt[q] = i < n ? weights[i] : 0.0f;
   }
   for (int e = tid; e < E; e += kThreads) U.mask[e] = 0;
   __syncthreads();
@@ -549,8 +598,28 @@ template <bool MX>
 __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ __attribute__((aligned(16))) float red[2 * kUpWaves * 512];
+  __shared__ Choices mine;
   Units U;
-  find_units<kUpThreads>(P, lds, &U);
+  if (P.logits) {
+    const int t = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    static_assert(kUpWaves >= kDirect, "a wave a token");
+    if (t < P.T) {
+      const float* const z = P.logits + t * P.E;
+      int* const to = mine.idx + t * P.k;
+      float* const wt = mine.wt + t * P.k;
+      if (P.E <= kWave)
+        choose<1>(z, P.E, P.k, P.renorm, to, wt);
+      else
+        choose<kChooseLanes>(z, P.E, P.k, P.renorm, to, wt);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < P.T * P.k; i += kUpThreads) {
+        P.idx[i] = mine.idx[i];
+        P.wt[i] = mine.wt[i];
+      }
+  }
+  find_units<kUpThreads>(P, lds, &U, P.logits ? &mine : nullptr);
   const int tiles = P.f / kRows;
   const int total = U.count * tiles;
   const int groups = gridDim.x, me = blockIdx.x;
@@ -584,15 +653,13 @@ constexpr int kBatchRows = kBatchWaves * 2 * kRows;
 // bytes of a step's columns, of the largest of the shapes up to `blocks`
 template <bool MX>
 constexpr int batch_bytes(int blocks) {
-  return MX && blocks <= 2 ? blocks * 8192
-         : MX              ? (blocks * 4096 > 16384 ? blocks * 4096 : 16384)
-                           : blocks * 4096;
+  return blocks * (MX && blocks <= 4 ? 8192 : 4096);
 }
 
 template <bool MX, int NB>
 struct BatchShape {
-  static constexpr int kStepK = MX && NB <= 2 ? 512 : 256;
-  static constexpr int kAhead = MX && NB > 2 ? 4 : 2;
+  static constexpr int kStepK = MX && NB <= 4 ? 512 : 256;
+  static constexpr int kAhead = 2;
   static constexpr int kPieces = kStepK / 8;            // of 16 bytes a column
   static constexpr int kLoads = kPieces * 8 / kBatchThreads;  // a block
   static constexpr int kBytes = NB * 8 * kPieces * 16;  // of a buffer
@@ -973,7 +1040,6 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
 // -------------------------------------------------------------------- down
 // Up to kDirect tokens: the columns of a tile are the tokens, each as two,
 // S's larger and smaller part, and a wave's sums run over all experts.
-constexpr int kDirect = 4;
 constexpr int kDownThreads = 1024;
 constexpr int kDownWaves = kDownThreads / kWave;
 constexpr int kAhead = 3;             // chunks of a wave in flight
@@ -1006,19 +1072,18 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     Tokens<MX> x;
   };
   // items of a tile are dealt in turn to the waves of all parts; a wave makes
-  // `rounds` of them, a multiple of kAhead, the last ones masked
+  // `rounds` of them, the last one masked where there are fewer
   const int step = kDownWaves * P.parts;
-  const int rounds = ((total + step - 1) / step + kAhead - 1) / kAhead *
-                     kAhead;
+  const int rounds = (total + step - 1) / step;
   int l_tile = group, l_left = rounds, l_q = part * kDownWaves + wave;
   auto load = [&](Item& it) {
-    const bool in = l_q < total;
+    const bool in = l_q < total && l_tile < tiles;
     const int un = in ? l_q / chunks : 0;
     const int k0 = in ? (l_q - un * chunks) * kChunkK : K;
     Reached X;
     X.read(U, un);
     const int64_t at =
-        X.id * per + static_cast<int64_t>(l_tile * kRows) * K;
+        X.id * per + static_cast<int64_t>(in ? l_tile * kRows : 0) * K;
     const auto rw = make_rsrc(
         P.w2 + at * (MX ? 1 : 2),
         static_cast<uint32_t>(kRows) * K * (MX ? 1 : 2));
@@ -1079,43 +1144,51 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     for (int s = 0; s < 4; ++s) acc = mma(c.w.frag(s, L), c.x.frag(s), acc);
   };
   int tile = group, c = 0;
+  auto one = [&](const Item& i) {
+    multiply(i);
+    if (++c < rounds) return;
+    finish(tile);
+    tile += groups;
+    c = 0;
+  };
   // kAhead items a time; the last are taken out of the loop, as in up_tiles
-  for (int left = (tiles - group + groups - 1) / groups * rounds;
-       left > kAhead; left -= kAhead) {
+  int left = (tiles - group + groups - 1) / groups * rounds;
+  for (; left > kAhead; left -= kAhead)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      multiply(it[i]);
+      one(it[i]);
       load(it[i]);
     }
-    c += kAhead;
-    if (c == rounds) {
-      finish(tile);
-      tile += groups;
-      c = 0;
-    }
-  }
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) multiply(it[i]);
-  finish(tile);
+  for (int i = 0; i < kAhead; ++i)
+    if (i < left) one(it[i]);
 }
 
-// y = y_add + the parts in order; n values, a multiple of 8.
+// y = y_add + the parts; n values, a multiple of 8.  Four lanes share four
+// values, each with every fourth part.
 __global__ __launch_bounds__(256) void few_sum_kernel(
     const float* __restrict__ part, int parts, int64_t n, const bf16_t* y_add,
     bf16_t* y) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
+  const int lane = threadIdx.x & 63, share = lane >> 4;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 4 +
+                     (threadIdx.x >> 6)) * 64 + (lane & 15) * 4;
+  if (i >= n) return;                 // all four lanes of a value
+  i32x2 a = {};
+  if (y_add) a = *reinterpret_cast<const i32x2*>(y_add + i);
   f32x4 v = {};
-#pragma unroll 8
-  for (int p = 0; p < parts; ++p)
+#pragma unroll 4
+  for (int p = share; p < parts; p += 4)
     v += *reinterpret_cast<const f32x4*>(part + p * n + i);
-  if (y_add) {
-    const i32x2 a = *reinterpret_cast<const i32x2*>(y_add + i);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      v[2 * q] += bf_lo(static_cast<uint32_t>(a[q]));
-      v[2 * q + 1] += bf_hi(static_cast<uint32_t>(a[q]));
-    }
+  for (int q = 0; q < 4; ++q) {
+    v[q] += shfl_xor(v[q], 16);
+    v[q] += shfl_xor(v[q], 32);
+  }
+  if (share) return;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    v[2 * q] += bf_lo(static_cast<uint32_t>(a[q]));
+    v[2 * q + 1] += bf_hi(static_cast<uint32_t>(a[q]));
   }
   *reinterpret_cast<i32x2*>(y + i) =
       i32x2{static_cast<int>(pack_bf16x2(v[0], v[1])),
@@ -1188,7 +1261,7 @@ hipError_t launch_few(const FewParams& P, hipStream_t s) {
   if (e != hipSuccess || P.parts == 1) return e;
   const int64_t n = static_cast<int64_t>(P.T) * P.d;
   hipLaunchKernelGGL(few_sum_kernel,
-                     dim3(static_cast<uint32_t>((n + 1023) / 1024)), dim3(256),
+                     dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256),
                      0, s, P.part, P.parts, n, P.y_add, P.y);
   return hipGetLastError();
 }
@@ -1214,18 +1287,19 @@ int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   return parts;
 }
 
-// Workspace: S, the parts' sums.
+// Workspace: S, the parts' sums, the scores.
 struct FewLayout {
   int parts;
-  size_t part, total;
+  size_t part, logits, total;
 };
 size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
 FewLayout few_layout(int64_t T, int k, int E, int64_t d, int64_t f) {
   FewLayout w;
   w.parts = down_parts(T, k, E, d, f);
   w.part = up256(static_cast<size_t>(T * k * f * 4));
-  w.total = w.part + up256(static_cast<size_t>(
-                         w.parts > 1 ? w.parts * T * d * 4 : 0));
+  w.logits = w.part + up256(static_cast<size_t>(
+                          w.parts > 1 ? w.parts * T * d * 4 : 0));
+  w.total = w.logits + up256(static_cast<size_t>(T * E * 4));
   return w;
 }
 
@@ -1256,12 +1330,28 @@ hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
   P.E = a.E;
   P.k = a.k;
   P.parts = w.parts;
+  P.renorm = a.renorm;
   P.inv_k = (65536 + a.k - 1) / a.k;
-  hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
-                     a.x, a.w_g, a.bias, a.logits, a.d, a.E, a.k, a.renorm,
-                     a.topk_idx, a.topk_w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  const float* logits = a.logits;
+  if (!logits) {
+    float* const z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                              w.logits);
+    hipLaunchKernelGGL(few_logits_kernel,
+                       dim3((a.E + kLogitWaves - 1) / kLogitWaves, a.T),
+                       dim3(kLogitThreads), 0, s, a.x, a.w_g, a.bias, a.d, a.E,
+                       z);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    logits = z;
+  }
+  if (a.T <= kDirect && a.E <= kWave * kChooseLanes) {
+    P.logits = logits;
+  } else {
+    hipLaunchKernelGGL(few_topk_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
+                       logits, a.E, a.k, a.renorm, a.topk_idx, a.topk_w);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return mx ? launch_few<true>(P, s) : launch_few<false>(P, s);
 }
 
