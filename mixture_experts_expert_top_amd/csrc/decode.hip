@@ -152,6 +152,25 @@ __global__ __launch_bounds__(kRouteThreads) void few_topk_kernel(
   }
 }
 
+// The largest of a wave's values.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  auto step = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+#define MOE_DPP_MAX(ctrl)                                                    \
+  v = step(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(             \
+                  0, static_cast<int>(v), ctrl, 0xf, 0xf, false)))
+  MOE_DPP_MAX(kDppXor1);
+  MOE_DPP_MAX(kDppXor2);
+  MOE_DPP_MAX(kDppHalfMirror);
+  MOE_DPP_MAX(kDppMirror);
+#undef MOE_DPP_MAX
+  uint32_t m = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    m = step(m, static_cast<uint32_t>(__builtin_amdgcn_readlane(
+                    static_cast<int>(v), r * 16)));
+  return m;
+}
+
 // The same by one wave for up to 64 N experts, N a lane: its choices go to
 // idx[0 .. k) and wt.
 template <int N>
@@ -160,47 +179,52 @@ __device__ __forceinline__ void choose(const float* __restrict__ z, int E,
                                        float* wt) {
   const int lane = lane_id();
   float v[N];
-  uint32_t key[N];
-  int place[N];
+  uint32_t key[N];                    // 0: none, or chosen already
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = i * kWave + lane;
     v[i] = e < E ? z[e] : 0.0f;
-    key[i] = e < E ? score_key(v[i]) : 0;
-    place[i] = e < E ? 0 : kMaxExperts;
+    key[i] = e < E ? max(score_key(v[i]), 1u) : 0;
   }
+  int mine = 0;                       // choice `lane`, and its score
+  float score = 0.0f, top = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    uint32_t m = key[0];
 #pragma unroll
-  for (int h = 0; h < N; ++h) {
-    const int ne = min(kWave, E - h * kWave);
-    for (int j = 0; j < ne; ++j) {
-      const uint32_t o = static_cast<uint32_t>(
-          __builtin_amdgcn_readlane(static_cast<int>(key[h]), j));
+    for (int i = 1; i < N; ++i) m = max(m, key[i]);
+    m = wave_max(m);
+    // the lowest expert with that key
+    bool found = false;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        place[i] += o > key[i] ||
-                    (o == key[i] && h * kWave + j < i * kWave + lane);
+    for (int i = 0; i < N; ++i) {
+      const uint64_t b = __ballot(key[i] == m);
+      if (found || b == 0) continue;
+      found = true;
+      const int l = __ffsll(static_cast<unsigned long long>(b)) - 1;
+      const float s = __int_as_float(
+          __builtin_amdgcn_readlane(__float_as_int(v[i]), l));
+      if (j == 0) top = s;
+      if (lane == j) {
+        mine = i * kWave + l;
+        score = s;
+      }
+      if (lane == l) key[i] = 0;
     }
   }
-  float top = 0.0f;
+  const float p = expf(score - top);
+  float part = 0.0f;
+  if (renorm) {
+    part = lane < k ? p : 0.0f;
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint64_t b = __ballot(place[i] == 0);
-    if (b) top = __shfl(v[i], __ffsll(static_cast<unsigned long long>(b)) - 1,
-                        kWave);
-  }
-  float p[N], part = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    p[i] = expf(v[i] - top);
-    if (i * kWave + lane < E && (!renorm || place[i] < k)) part += p[i];
+    for (int i = 0; i < N; ++i)
+      if (i * kWave + lane < E) part += expf(v[i] - top);
   }
   const float sum = wave_sum(part);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (place[i] < k) {
-      idx[place[i]] = i * kWave + lane;
-      wt[place[i]] = p[i] / sum;
-    }
+  if (lane < k) {
+    idx[lane] = mine;
+    wt[lane] = p / sum;
+  }
 }
 
 // ---------------------------------------------------------------- weights
@@ -221,7 +245,7 @@ struct FewParams {
   const uint8_t* w2_scales;
   int32_t* idx;                       // [T][k]
   float* wt;
-  const float* logits;                // few_up_kernel: to choose from, or null
+  const float* logits;                // to choose from, or null: idx, wt given
   int renorm;
   bf16_t* s;                          // [T k][2][f]: S in two parts
   const bf16_t* y_add;
@@ -359,27 +383,58 @@ struct Units {
   }
 };
 
-// Up to kDirect tokens and 64 kChooseLanes experts: a wave of few_up_kernel
-// chooses for a token itself, in every workgroup, and the first one writes the
-// choices down.
+// Up to kDirect tokens take the kernels whose waves divide the reduction.
 constexpr int kDirect = 4;
-constexpr int kChooseLanes = 2;
+// Up to kChooseTokens and 64 kChooseLanes experts: the waves of a workgroup
+// of the first product choose for the tokens themselves, and the first one
+// writes the choices down.  8 tokens of 8 experts cost 1 us there, 5 in a
+// kernel of its own; from 24 tokens of 64 experts on it is the reverse.
+constexpr int kChooseTokens = 8;
+constexpr int kChooseLanes = 4;
 
 struct Choices {
-  int idx[kDirect * kMaxTopK];
-  float wt[kDirect * kMaxTopK];
+  int* idx;
+  float* wt;
 };
 
-// own: the choices where the workgroup made them, else null.
+// Chooses into LDS at `to` (8 bytes a slot) where the call left that to the
+// kernel.
 template <int kThreads>
-__device__ __forceinline__ void find_units(const FewParams& P, uint8_t* lds,
-                                           Units* out,
-                                           const Choices* own = nullptr) {
+__device__ __forceinline__ Choices choose_here(const FewParams& P,
+                                               uint8_t* to) {
+  Choices c{P.idx, P.wt};
+  if (!P.logits) return c;
+  const int n = P.T * P.k;
+  c.idx = reinterpret_cast<int*>(to);
+  c.wt = reinterpret_cast<float*>(c.idx + n);
+  for (int t = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t < P.T;
+       t += kThreads / kWave) {
+    const float* const z = P.logits + t * P.E;
+    int* const i = c.idx + t * P.k;
+    float* const w = c.wt + t * P.k;
+    if (P.E <= kWave)
+      choose<1>(z, P.E, P.k, P.renorm, i, w);
+    else
+      choose<kChooseLanes>(z, P.E, P.k, P.renorm, i, w);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      P.idx[i] = c.idx[i];
+      P.wt[i] = c.wt[i];
+    }
+  return c;
+}
+
+template <int kThreads>
+__device__ __forceinline__ void find_units(const FewParams& P,
+                                           const Choices& chosen, uint8_t* lds,
+                                           Units* out) {
   constexpr int kPer = kFewTokens * kMaxTopK / kThreads;
   const int tid = threadIdx.x, lane = tid & 63;
   const int n = P.T * P.k, E = P.E;
-  const int* const idx = own ? own->idx : P.idx;
-  const float* const weights = own ? own->wt : P.wt;
+  const int* const idx = chosen.idx;
+  const float* const weights = chosen.wt;
   Units U;
   U.mask = reinterpret_cast<uint64_t*>(lds);
   U.expert = reinterpret_cast<Expert*>(U.mask + E);
@@ -598,28 +653,10 @@ template <bool MX>
 __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ __attribute__((aligned(16))) float red[2 * kUpWaves * 512];
-  __shared__ Choices mine;
+  static_assert(sizeof(red) >= kDirect * kMaxTopK * 8, "room for choices");
   Units U;
-  if (P.logits) {
-    const int t = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    static_assert(kUpWaves >= kDirect, "a wave a token");
-    if (t < P.T) {
-      const float* const z = P.logits + t * P.E;
-      int* const to = mine.idx + t * P.k;
-      float* const wt = mine.wt + t * P.k;
-      if (P.E <= kWave)
-        choose<1>(z, P.E, P.k, P.renorm, to, wt);
-      else
-        choose<kChooseLanes>(z, P.E, P.k, P.renorm, to, wt);
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int i = threadIdx.x; i < P.T * P.k; i += kUpThreads) {
-        P.idx[i] = mine.idx[i];
-        P.wt[i] = mine.wt[i];
-      }
-  }
-  find_units<kUpThreads>(P, lds, &U, P.logits ? &mine : nullptr);
+  find_units<kUpThreads>(
+      P, choose_here<kUpThreads>(P, reinterpret_cast<uint8_t*>(red)), lds, &U);
   const int tiles = P.f / kRows;
   const int total = U.count * tiles;
   const int groups = gridDim.x, me = blockIdx.x;
@@ -899,8 +936,9 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_up_batch_kernel(
     FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   Units U;
-  find_units<kBatchThreads>(P, lds, &U);
   uint8_t* const xs = lds + Units::bytes(P.E, P.T * P.k);
+  static_assert(2 * 4096 >= kChooseTokens * kMaxTopK * 8, "room for choices");
+  find_units<kBatchThreads>(P, choose_here<kBatchThreads>(P, xs), lds, &U);
   const int groups = (P.f + 4 * kRows - 1) / (4 * kRows);
   const int total = U.count * groups;
   const int n = gridDim.x, me = blockIdx.x;
@@ -1015,7 +1053,7 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
   for (int i = tid; i < kBatchWaves * T * 16; i += kBatchThreads)
     planes[i] = 0;
   Units U;
-  find_units<kBatchThreads>(P, lds, &U);
+  find_units<kBatchThreads>(P, Choices{P.idx, P.wt}, lds, &U);
   float* const plane = planes + wave * T * 16;
   uint8_t* const xs =
       reinterpret_cast<uint8_t*>(planes + kBatchWaves * T * 16);
@@ -1059,7 +1097,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
   const int groups = gridDim.x / P.parts, tiles = P.d / kRows;
   const int K = P.f, T = P.T;
   Units U;
-  find_units<kDownThreads>(P, lds, &U);
+  find_units<kDownThreads>(P, Choices{P.idx, P.wt}, lds, &U);
   const int chunks = (K + kChunkK - 1) / kChunkK;      // of an expert
   const int total = U.count * chunks;
   const auto rx = make_rsrc(P.s, static_cast<uint32_t>(T) * P.k * 2 * K * 2);
@@ -1344,7 +1382,7 @@ hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
     if (e != hipSuccess) return e;
     logits = z;
   }
-  if (a.T <= kDirect && a.E <= kWave * kChooseLanes) {
+  if (a.T <= kChooseTokens && a.E <= kWave * kChooseLanes) {
     P.logits = logits;
   } else {
     hipLaunchKernelGGL(few_topk_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
