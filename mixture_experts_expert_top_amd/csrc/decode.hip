@@ -710,7 +710,7 @@ __device__ __forceinline__ int swizzle(int c) {
   return MX ? c : (c & 3) | ((c & 4) << 1);
 }
 
-// Where a batch stands: step (expert, part of it, round of k), one for the
+// Where a batch stands: step (expert, group of rows, round of k), one for the
 // columns, one for the weights and one for the sums.
 struct Cursor {
   int left, un, mid, r;               // left: steps from here on
@@ -724,14 +724,17 @@ struct Cursor {
     mid = t - un * mids;
     X.read(U, un);
   }
-  __device__ __forceinline__ void next(const Units& U, int mids, int rounds) {
+  // true where another expert begins
+  __device__ __forceinline__ bool next(const Units& U, int mids, int rounds) {
     --left;
-    if (++r < rounds) return;
+    if (++r < rounds) return false;
     r = 0;
-    if (++mid < mids) return;
+    if (++mid < mids) return false;
     mid = 0;
     ++un;
-    if (left > 0) X.read(U, un);
+    if (left <= 0) return false;
+    X.read(U, un);
+    return true;
   }
 };
 
@@ -756,20 +759,30 @@ __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
   Columns cx[2];
   Weights<MX, H::kStepK> wa[D], wb[D];
   Cursor at_x(U, begin, end, src.mids, src.rounds), at_w = at_x, at = at_x;
-  auto load_columns = [&](Columns& x) {
-    const int k0 = at_x.left > 0 ? at_x.r * H::kStepK : src.K;
+  // byte offsets of the thread's pieces at k = 0, which change with the
+  // expert; kOob and on: none
+  uint32_t from[NB * H::kLoads];
+  auto find_columns = [&]() {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int j = 0; j < H::kLoads; ++j) {
         const int id = tid + j * kBatchThreads;
-        const int c = id / H::kPieces, k = k0 + (id % H::kPieces) * 8;
-        const uint32_t o = src.column(at_x, c, b);
-        x.v[b * H::kLoads + j] = buf_load16(
-            src.rx, k < src.K && o != kOob ? o + static_cast<uint32_t>(k) * 2
-                                           : kOob);
+        from[b * H::kLoads + j] = src.column(at_x, id / H::kPieces, b);
       }
-    at_x.next(U, src.mids, src.rounds);
+  };
+  find_columns();
+  auto load_columns = [&](Columns& x) {
+    const int k0 = at_x.left > 0 ? at_x.r * H::kStepK : src.K;
+#pragma unroll
+    for (int i = 0; i < NB * H::kLoads; ++i) {
+      const int id = tid + i % H::kLoads * kBatchThreads;
+      const int k = k0 + (id % H::kPieces) * 8;
+      x.v[i] = buf_load16(src.rx, k < src.K && from[i] != kOob
+                                      ? from[i] + static_cast<uint32_t>(k) * 2
+                                      : kOob);
+    }
+    if (at_x.next(U, src.mids, src.rounds)) find_columns();
     __builtin_amdgcn_sched_barrier(0);
   };
   auto load_weights = [&](int u) {
@@ -841,10 +854,16 @@ __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
 }
 
 // Adds the two halves of k: rows 0-7 with columns 0-7 (lanes below 32 of
-// columns 0-7) and rows 8-15 with columns 8-15.
+// columns 0-7, where the sum is left) and rows 8-15 with columns 8-15, by a
+// rotation of each 16 lanes by 8 and an exchange of the wave's halves.
 __device__ __forceinline__ f32x4 join_halves(f32x4 v) {
+  constexpr int kDppRor8 = 0x128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] += shfl_xor(v[i], 40);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = __float_as_uint(dpp_move<kDppRor8>(v[i]));
+    const auto s = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+    v[i] += __uint_as_float(s[1]);
+  }
   return v;
 }
 
@@ -957,9 +976,9 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_up_batch_kernel(
     up_batch<MX, MAXB >= 8 ? 8 : 1>(P, U, first, last, xs);
 }
 
-// Down: steps are (expert, pass, k), a wave's tiles 16 rows of y.  A block
-// holds four members, each as two columns, S's larger and smaller part; an
-// expert with more members than NB blocks hold takes several passes.
+// Down: steps are (expert, k), a wave's tiles 16 rows of y.  A block holds
+// four members, each as two columns, S's larger and smaller part; members
+// past what NB blocks hold are left to further passes.
 template <bool MX, int NB>
 struct DownSource {
   using H = BatchShape<MX, NB>;
@@ -967,19 +986,19 @@ struct DownSource {
   const FewParams& P;
   const Units& U;
   __amdgpu_buffer_rsrc_t rx;
-  int K, rounds, mids, n0;
+  int K, rounds, mids, n0, skip;      // skip: members of earlier passes
   float* plane;                       // [T][16], the wave's
   Lane<MX> L;
 
   __device__ __forceinline__ DownSource(const FewParams& p, const Units& u,
-                                        int most, int row0, float* sums)
+                                        int rows, int row0, int members,
+                                        float* sums)
       : P(p), U(u),
         rx(make_rsrc(p.s, static_cast<uint32_t>(p.T) * p.k * 4 * p.f)),
-        K(p.f), rounds((p.f + H::kStepK - 1) / H::kStepK),
-        mids((most + kMembers - 1) / kMembers), n0(row0), plane(sums) {}
+        K(p.f), rounds(rows), mids(1), n0(row0), skip(members), plane(sums) {}
   __device__ __forceinline__ uint32_t column(const Cursor& at, int c,
                                              int b) const {
-    const int m = at.mid * kMembers + b * 4 + (c >> 1);
+    const int m = skip + b * 4 + (c >> 1);
     return m < at.X.members
                ? (static_cast<uint32_t>(U.slot[at.X.first + m]) * 2 +
                   (c & 1)) * K * 2
@@ -989,8 +1008,7 @@ struct DownSource {
                                           Weights<MX, H::kStepK>& a,
                                           Weights<MX, H::kStepK>& b) const {
     // an expert without members in this pass is not read
-    const bool in = at.left > 0 && n0 < P.d &&
-                    at.mid * kMembers < at.X.members;
+    const bool in = at.left > 0 && n0 < P.d && skip < at.X.members;
     const int64_t o = (at.X.id * static_cast<int64_t>(P.d) + (in ? n0 : 0)) *
                       K;
     const uint32_t rows = static_cast<uint32_t>(in ? min(16, P.d - n0) : 0);
@@ -1010,7 +1028,7 @@ struct DownSource {
     const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      if (at.mid * kMembers + i * 4 >= at.X.members) break;
+      if (skip + i * 4 >= at.X.members) break;
       f32x4 s0 = join_halves(a[i]), s1 = join_halves(b[i]);
       // S's two parts stand in neighbouring columns
 #pragma unroll
@@ -1018,7 +1036,7 @@ struct DownSource {
         s0[v] += dpp_move<kDppXor1>(s0[v]);
         s1[v] += dpp_move<kDppXor1>(s1[v]);
       }
-      const int m = at.mid * kMembers + i * 4 + (c >> 1);
+      const int m = skip + i * 4 + (c >> 1);
       if (c >= 8 || (c & 1) || qr >= 2 || m >= at.X.members) continue;
       f32x4* const o = reinterpret_cast<f32x4*>(
           plane + P.token(U.slot[at.X.first + m]) * 16 + qr * 4);
@@ -1029,15 +1047,23 @@ struct DownSource {
   }
 };
 
+// Pieces of kPartK k of the experts' reductions, [begin, end) of them; a unit
+// that does not depend on NB, so that neighbouring parts meet.
+template <bool MX>
+constexpr int kPartK = MX ? 512 : 256;
+
 template <bool MX, int NB>
 __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
-                                           int part, int most, int n0,
-                                           float* plane, uint8_t* xs) {
-  DownSource<MX, NB> src(P, U, most, n0, plane);
-  const int64_t total = static_cast<int64_t>(U.count) * src.mids * src.rounds;
-  const int begin = static_cast<int>(total * part / P.parts);
-  const int end = static_cast<int>(total * (part + 1) / P.parts);
-  if (begin < end) batch<MX, NB>(src, U, begin, end, xs);
+                                           int begin, int end, int most,
+                                           int n0, float* plane,
+                                           uint8_t* xs) {
+  constexpr int kSteps = kPartK<MX> / BatchShape<MX, NB>::kStepK;
+  const int rounds = (P.f + kPartK<MX> - 1) / kPartK<MX> * kSteps;
+  for (int skip = 0; skip < most; skip += 4 * NB) {
+    if (skip) __syncthreads();        // xs is free again
+    DownSource<MX, NB> src(P, U, rounds, n0, skip, plane);
+    batch<MX, NB>(src, U, begin * kSteps, end * kSteps, xs);
+  }
 }
 
 // MAXB: blocks of 4 members that T tokens can fill, up to 8.
@@ -1058,13 +1084,22 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
   uint8_t* const xs =
       reinterpret_cast<uint8_t*>(planes + kBatchWaves * T * 16);
   const int n0 = group * kBatchRows + wave * 16;
-  const int most = most_members(U, 0, U.count);
-  if (MAXB == 2 || most <= 8)
-    down_batch<MX, 2>(P, U, part, most, n0, plane, xs);
-  else if (MAXB == 4 || most <= 16)
-    down_batch<MX, MAXB >= 4 ? 4 : 2>(P, U, part, most, n0, plane, xs);
-  else
-    down_batch<MX, MAXB >= 8 ? 8 : 2>(P, U, part, most, n0, plane, xs);
+  const int pieces = (P.f + kPartK<MX> - 1) / kPartK<MX>;
+  const int64_t total = static_cast<int64_t>(U.count) * pieces;
+  const int begin = static_cast<int>(total * part / P.parts);
+  const int end = static_cast<int>(total * (part + 1) / P.parts);
+  if (begin < end) {
+    const int most =
+        most_members(U, begin / pieces, (end - 1) / pieces + 1);
+    if (most <= 4)
+      down_batch<MX, 1>(P, U, begin, end, most, n0, plane, xs);
+    else if (MAXB == 2 || most <= 8)
+      down_batch<MX, 2>(P, U, begin, end, most, n0, plane, xs);
+    else if (MAXB == 4 || most <= 16)
+      down_batch<MX, MAXB >= 4 ? 4 : 2>(P, U, begin, end, most, n0, plane, xs);
+    else
+      down_batch<MX, MAXB >= 8 ? 8 : 2>(P, U, begin, end, most, n0, plane, xs);
+  }
   // the wave's own rows of the part's sums
   for (int i = lane; i < T * 4; i += kWave) {
     const int t = i >> 2, r = (i & 3) * 4;
@@ -1321,7 +1356,7 @@ int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   const int64_t steps = most * ((f + 255) / 256);
   const int64_t groups = (d + kBatchRows - 1) / kBatchRows;
   int parts = 8;
-  while (parts < 32 && groups * parts < 512 && steps >= parts * 8) parts *= 2;
+  while (parts < 32 && groups * parts < 512 && steps >= parts * 16) parts *= 2;
   return parts;
 }
 
