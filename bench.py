@@ -619,6 +619,37 @@ def torch_cat_gate_up(w_gu, f, fs, ds):
     return torch.cat([w_gu[:, :fs, :ds], w_gu[:, f:f + fs, :ds]], dim=1)
 
 
+def time_adamw(path, inp, args):
+    """The optimizer step on the gradients that the timed steps left: ms, and
+    the bytes that it reads and writes a second."""
+    import torch
+    from mixture_experts_expert_top_amd import moe
+    from mixture_experts_expert_top_amd.layer import AdamW
+    # copies: the CPU baseline reads the weights
+    w = {n: None if inp[n] is None else inp[n].clone()
+         for n in ("w_gu", "w2", "w_g", "bias")}
+    fp8 = args.adamw == "fp8"
+    opt = AdamW(path.gradients(**w), max_norm=1.0,
+                moments=moe.MOE_MOMENTS_FP8 if fp8 else moe.MOE_MOMENTS_FP32)
+    for _ in range(args.warmup):
+        opt.step()
+    a = torch.cuda.Event(enable_timing=True)
+    b = torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(args.steps):
+        opt.step()
+    b.record()
+    torch.cuda.synchronize()
+    ms = a.elapsed_time(b) / args.steps
+    # gradients twice; parameter written, its copy and the moments both ways
+    moments = 4 + 16 / moe.MOE_ADAMW_BLOCK if fp8 else 16
+    nbytes = sum(r["g"].numel() * (2 * r["g"].element_size() +
+                                   r["p"].element_size() + 8 + moments)
+                 for r in opt.rows)
+    return {"moments": args.adamw, "ms_per_step": round(ms, 4),
+            "gbs": round(nbytes / (ms / 1e3) / 1e9, 1)}
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -635,6 +666,10 @@ def main():
     ap.add_argument("--graph", action="store_true",
                     help="also time the step captured as a HIP graph and "
                          "replayed (reported under 'graph')")
+    ap.add_argument("--adamw", choices=("fp32", "fp8"),
+                    help="also time an AdamW step of the layer's weights, "
+                         "clipped, with moments in 32 or 8 bits (reported "
+                         "under 'adamw')")
     ap.add_argument("--copy-calibration", action="store_true",
                     help="only run the 1 GiB device copy that calibrates "
                          "the HBM traffic counters")
@@ -772,6 +807,8 @@ def main():
         gms = gs.elapsed_time(ge) / args.steps
         out["graph"] = {"ms_per_step": round(gms, 4),
                         "tokens_per_s": round(T / (gms / 1e3), 1)}
+    if args.adamw and wl.backward:
+        out["adamw"] = time_adamw(path, inp, args)
     if not args.no_cpu_baseline:
         out["cpu_baseline"] = (cpu_baseline_mx(inp, wl) if mx else
                                cpu_baseline(inp, wl, min(args.cpu_tokens, T)))

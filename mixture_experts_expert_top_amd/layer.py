@@ -31,6 +31,10 @@ instead of re-permuting bf16 x.
 front, optionally a dense gated feed-forward block that every token passes
 beside its routed experts, and the residual sum with dropout behind.
 
+``MoEDecode`` is the layer for the few tokens of generation, one call without
+a dispatch plan or a backward, in a block as the other two are; ``AdamW`` is
+the step that uses the gradients that they leave.
+
 No arithmetic happens here: every step runs in the library's kernels.
 """
 
@@ -41,8 +45,9 @@ import torch
 
 from . import moe
 from .moe import (MOE_ACT_SILU, MOE_BF16, MOE_ENTRY_FFN_BWD,
-                  MOE_ENTRY_FFN_FWD, MOE_ENTRY_MLP_BWD, MOE_ENTRY_MLP_FWD,
-                  MOE_ENTRY_NORM_BWD, MOE_ENTRY_PERMUTE, MOE_ENTRY_ROUTER_BWD,
+                  MOE_ENTRY_FFN_FWD, MOE_ENTRY_GRAD_NORM, MOE_ENTRY_LAYER_FWD,
+                  MOE_ENTRY_MLP_BWD, MOE_ENTRY_MLP_FWD, MOE_ENTRY_NORM_BWD,
+                  MOE_ENTRY_PERMUTE, MOE_ENTRY_ROUTER_BWD, MOE_MOMENTS_FP32,
                   MOE_MXFP4, MOE_MXFP8, MOE_NORM_LAYER, MOE_NORM_RMS)
 
 
@@ -136,6 +141,18 @@ class MoEPath:
         self.ws_router = torch.empty(max(ws_r, 16), dtype=torch.uint8,
                                      device=dev)
         self._bwd_ready = True
+
+    def gradients(self, w_gu, w2, w_g=None, bias=None):
+        """(weight, gradient[, weight decay]) of the weights that a backward
+        with them leaves gradients for, as ``AdamW`` takes them."""
+        if not self._bwd_ready:
+            self._alloc_bwd()
+        out = [(w_gu, self.dw_gu), (w2, self.dw2)]
+        if w_g is not None:
+            out.append((w_g, self.dw_g))
+        if bias is not None:
+            out.append((bias, self.db, 0.0))
+        return out
 
     # ------------------------------------------------------------------
     def route(self, x=None, w_g=None, bias=None, logits=None, timers=None):
@@ -441,6 +458,122 @@ class MoEPathMX(MoEPath):
         return self.dx, self.dw_gu, self.dw2, self.dp
 
 
+class MoEDecode:
+    """The layer for a fixed number of tokens, up to
+    ``moe.MOE_LAYER_MAX_TOKENS``, forward only: one library call that reads
+    the weights of the experts it reaches once.  With prec MOE_MXFP8 w_gu and
+    w2 are pairs of codes and scales, as ``quantize`` makes them of the bf16
+    weights once."""
+
+    def __init__(self, T, d, f, E, k, renorm=True, prec=MOE_BF16,
+                 device="cuda"):
+        n = moe.moe_workspace_bytes(MOE_ENTRY_LAYER_FWD, prec, T, E, k, d, f)
+        if n == 0:
+            raise ValueError("MoEDecode takes 1 to "
+                             f"{moe.MOE_LAYER_MAX_TOKENS} tokens and k <= E")
+        self.T, self.d, self.f, self.E, self.k = T, d, f, E, k
+        self.renorm, self.prec = renorm, prec
+        dev = torch.device(device)
+        self.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        self.topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        self.y = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        self._forwards = 0
+
+    @staticmethod
+    def quantize(w):
+        """MXFP8 codes and scales of a bf16 weight [E, rows, cols] along its
+        last axis."""
+        E, rows, cols = w.shape
+        z = lambda n: torch.empty(E, rows, n, dtype=torch.uint8,  # noqa: E731
+                                  device=w.device)
+        codes, scales = z(cols), z(cols // 32)
+        for e in range(E):
+            moe.moe_mxfp8_quantize(w[e], 0, None, codes[e], scales[e])
+        return codes, scales
+
+    def forward(self, x, w_gu, w2, w_g=None, bias=None, logits=None,
+                timers=None, y_add=None):
+        """y = y_add + the layer's output for x."""
+        self._forwards += 1
+        gu, gu_s = (w_gu, None) if self.prec == MOE_BF16 else w_gu
+        dn, dn_s = (w2, None) if self.prec == MOE_BF16 else w2
+        given = logits is not None
+        with _around(timers, "layer_fwd"):
+            moe.moe_layer_fwd(self.prec, x, None if given else w_g,
+                              None if given else bias, logits, self.k,
+                              self.renorm, gu, gu_s, dn, dn_s, y_add,
+                              self.topk_idx, self.topk_w, self.y, self.ws)
+        return self.y
+
+    def _alloc_bwd(self):
+        raise NotImplementedError("MoEDecode has no backward: use MoEPath or "
+                                  "MoEPathMX")
+
+    _bwd_ready = False
+
+
+class AdamW:
+    """AdamW over the weights of paths and blocks, one library call a step.
+
+    params: (weight, gradient) or (weight, gradient, weight_decay), as the
+    ``gradients`` methods of paths and blocks give them; the gradients' buffers
+    are read anew at every step.  moments: MOE_MOMENTS_FP32 or
+    MOE_MOMENTS_FP8 (8 bits and a scale for 256 values).  master: keep an fp32
+    copy of each bf16 weight, from which it is updated.  max_norm: clip the
+    gradients to that norm over all of them, and leave a step out whose norm
+    is not finite.  lr, the number of steps made and the norm live on the
+    device, so that ``step`` can be captured; ``lr.fill_`` changes the rate of
+    captured steps too.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
+                 weight_decay=0.1, moments=MOE_MOMENTS_FP32, master=True,
+                 max_norm=None):
+        self.betas, self.eps, self.max_norm = betas, eps, max_norm
+        rows = []
+        for w, g, *wd in params:
+            row = {"p": w, "g": g, "weight_decay": wd[0] if wd else
+                   weight_decay}
+            if master and w.dtype == torch.bfloat16:
+                row["master"] = w.float()
+            if moments == MOE_MOMENTS_FP32:
+                for n in ("m", "v"):
+                    row[n] = torch.zeros_like(w, dtype=torch.float32)
+            else:
+                blocks = -(-w.numel() // moe.MOE_ADAMW_BLOCK)
+                for n in ("m", "v"):
+                    row[n] = torch.zeros_like(w, dtype=torch.uint8).view(
+                        torch.float8_e4m3fn)
+                    row[n + "_scale"] = torch.zeros(
+                        blocks, dtype=torch.float32, device=w.device)
+            rows.append(row)
+        self.table = moe.adamw_table(rows)
+        self.grads = moe.grad_table([r["g"] for r in rows])
+        self.rows = rows
+        dev = rows[0]["p"].device
+        self.lr = torch.full((1,), lr, dtype=torch.float32, device=dev)
+        self.steps = torch.zeros(1, dtype=torch.int64, device=dev)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        n = moe.moe_workspace_bytes(MOE_ENTRY_GRAD_NORM, MOE_BF16, 1, 1, 1, 8,
+                                    8)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+
+    def step(self, timers=None):
+        with torch.cuda.device(self.norm.device):
+            norm = None
+            if self.max_norm is not None:
+                norm = self.norm
+                with _around(timers, "grad_norm"):
+                    moe.moe_grad_norm(self.grads, norm, self.ws)
+                self.steps.add_(torch.isfinite(norm))
+            else:
+                self.steps.add_(1)
+            with _around(timers, "adamw"):
+                moe.moe_adamw(self.table, self.steps, self.lr, *self.betas,
+                              self.eps, norm, self.max_norm or 1.0)
+
+
 def _extent(t):
     """First byte of a contiguous tensor and the byte past its last."""
     lo = t.data_ptr()
@@ -474,8 +607,8 @@ def _on_its_device(call):
 
 
 class MoEBlock:
-    """Pre-norm residual block around an expert layer (a ``MoEPath`` or
-    ``MoEPathMX`` with bf16 output):
+    """Pre-norm residual block around an expert layer (a ``MoEPath``,
+    ``MoEPathMX`` or, forward only, ``MoEDecode`` with bf16 output):
 
       n = norm(x);  z = experts(n) [+ ffn(n)];  y = x + dropout(z)
 
@@ -546,6 +679,20 @@ class MoEBlock:
                           _buffers(self, "the block's", ("y", "dx")))
         self._dx_buf = [("the block's dx", *_extent(self.dx))]
         self._bwd_ready = True
+
+    def gradients(self, gamma, w_gu, w2, beta=None, w_g=None, bias=None,
+                  sw_gu=None, sw2=None):
+        """(weight, gradient[, weight decay]) of the block's and the path's
+        weights, as ``AdamW`` takes them; the norm's have no weight decay."""
+        if not self._bwd_ready:
+            self._alloc_bwd()
+        out = [(gamma, self.dgamma, 0.0)]
+        if beta is not None:
+            out.append((beta, self.dbeta, 0.0))
+        out += self.path.gradients(w_gu, w2, w_g, bias)
+        if self.f_shared:
+            out += [(sw_gu, self.dsw_gu), (sw2, self.dsw2)]
+        return out
 
     @_on_its_device
     def forward(self, x, gamma, w_gu, w2, beta=None, w_g=None, bias=None,

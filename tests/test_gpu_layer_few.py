@@ -373,3 +373,43 @@ def test_binding_refuses():
     big.p = torch.zeros(65, 1, device="cuda:0")
     with pytest.raises(moe.MoeError, match="64"):
         big.run()
+
+
+@gpu
+@pytest.mark.parametrize("T,E,k", [(1, 64, 8), (4, 65, 3), (8, 200, 32),
+                                   (7, 256, 9), (8, 257, 5), (9, 256, 8),
+                                   (2, 130, 32), (8, 5, 5)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_routing_inside_the_first_product_and_apart(T, E, k, renorm):
+    """Both sides of what is chosen inside a kernel, ties and special values
+    included, are moe_route's choices."""
+    c = Case(T, 16, 16, E, k, seed=E)
+    L = (I.make_tensor((T, E), seed=2, dtype=F32, device="cuda:0") * 2).round()
+    L[0, E // 2] = float("nan")
+    L[T - 1, :] = 1.5
+    L[T // 2, ::2] = float("-inf")
+    L[T // 2, 1::4] = -0.0
+    c.logits = L
+    c.run(renorm)
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda:0")
+    w = torch.empty(T, k, device="cuda:0")
+    moe.moe_route(L, k, renorm, idx, w)
+    assert torch.equal(c.idx, idx)
+    ok = ~torch.isnan(w)
+    assert torch.equal(ok, ~torch.isnan(c.p))
+    assert ((c.p - w).abs()[ok] <= (2 * E + 8) * U * w[ok] + 1e-37).all()
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+def test_an_expert_past_32_members_and_small_ones(mx):
+    """Parts of y whose experts hold 0 to 64 of the tokens."""
+    T, E = 64, 20
+    c = Case(T, 640, 1152, E, 3, mx=mx, add=True, seed=9)
+    L = I.make_tensor((T, E), seed=3, dtype=F32, device="cuda:0")
+    L[:, 7] = 9.0
+    L[:40, 3] = 8.0
+    L[:, 11:] -= 4.0
+    c.logits = L
+    c.run()
+    check(c)
