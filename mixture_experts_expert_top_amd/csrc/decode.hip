@@ -320,8 +320,10 @@ struct Weights {
         const i32x4 v = buf_load16(rs, at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = static_cast<uint32_t>(v[i]);
+      } else if constexpr (kLoads == 1) {
+        s[0] = buf_load4(rs, at);
       } else {
-        static_assert(kLoads == 2, "256 or 512 codes");
+        static_assert(kLoads == 2, "128, 256 or 512 codes");
         const i32x2 v = __builtin_bit_cast(
             i32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0));
         s[0] = static_cast<uint32_t>(v[0]);
@@ -687,20 +689,25 @@ constexpr int kBatchThreads = 256;
 constexpr int kBatchWaves = kBatchThreads / kWave;
 constexpr int kBatchRows = kBatchWaves * 2 * kRows;
 
-// bytes of a step's columns, of the largest of the shapes up to `blocks`
-template <bool MX>
-constexpr int batch_bytes(int blocks) {
-  return blocks * (MX && blocks <= 4 ? 8192 : 4096);
-}
-
+// Fewer k a step, and more steps in flight, keep the columns of many blocks
+// within 16 KB a buffer: with 32 KB for eight blocks a CU held one workgroup
+// (61 tokens, 41 experts of 1032 x 680: the second product 30 us).
 template <bool MX, int NB>
 struct BatchShape {
-  static constexpr int kStepK = MX && NB <= 4 ? 512 : 256;
-  static constexpr int kAhead = 2;
+  static constexpr int kStepK =
+      MX ? (NB <= 2 ? 512 : NB == 4 ? 256 : 128) : (NB <= 4 ? 256 : 128);
+  static constexpr int kAhead = kStepK == (MX ? 512 : 256) ? 2 : 4;
   static constexpr int kPieces = kStepK / 8;            // of 16 bytes a column
-  static constexpr int kLoads = kPieces * 8 / kBatchThreads;  // a block
+  static constexpr int kLoads = NB * 8 * kPieces / kBatchThreads;
   static constexpr int kBytes = NB * 8 * kPieces * 16;  // of a buffer
+  static_assert(kLoads * kBatchThreads == NB * 8 * kPieces, "whole loads");
 };
+// the most of them up to `blocks`
+template <bool MX>
+constexpr int batch_bytes(int blocks) {
+  return MX ? 8192 * (blocks < 2 ? blocks : 2)
+            : 4096 * (blocks < 4 ? blocks : 4);
+}
 
 // The columns' k in LDS: 16-byte piece p of column c lies at p ^ swizzle(c),
 // so that the sixteen lanes of a fragment read that share a cycle (8 columns
@@ -754,30 +761,28 @@ __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
   const int tid = threadIdx.x, lane = tid & 63;
   const int fr = lane & 15, g = lane >> 4, col = fr & 7;
   struct Columns {
-    i32x4 v[NB * H::kLoads];
+    i32x4 v[H::kLoads];
   };
   Columns cx[2];
   Weights<MX, H::kStepK> wa[D], wb[D];
   Cursor at_x(U, begin, end, src.mids, src.rounds), at_w = at_x, at = at_x;
+  // piece i of the thread: 16 bytes of column `col_of(i)` (8 a block)
+  auto col_of = [&](int i) { return (tid + i * kBatchThreads) / H::kPieces; };
+  auto piece_of = [&](int i) { return (tid + i * kBatchThreads) % H::kPieces; };
   // byte offsets of the thread's pieces at k = 0, which change with the
-  // expert; kOob and on: none
-  uint32_t from[NB * H::kLoads];
+  // expert; kOob: none
+  uint32_t from[H::kLoads];
   auto find_columns = [&]() {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int j = 0; j < H::kLoads; ++j) {
-        const int id = tid + j * kBatchThreads;
-        from[b * H::kLoads + j] = src.column(at_x, id / H::kPieces, b);
-      }
+    for (int i = 0; i < H::kLoads; ++i)
+      from[i] = src.column(at_x, col_of(i) & 7, col_of(i) >> 3);
   };
   find_columns();
   auto load_columns = [&](Columns& x) {
     const int k0 = at_x.left > 0 ? at_x.r * H::kStepK : src.K;
 #pragma unroll
-    for (int i = 0; i < NB * H::kLoads; ++i) {
-      const int id = tid + i % H::kLoads * kBatchThreads;
-      const int k = k0 + (id % H::kPieces) * 8;
+    for (int i = 0; i < H::kLoads; ++i) {
+      const int k = k0 + piece_of(i) * 8;
       x.v[i] = buf_load16(src.rx, k < src.K && from[i] != kOob
                                       ? from[i] + static_cast<uint32_t>(k) * 2
                                       : kOob);
@@ -792,15 +797,12 @@ __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
   };
   auto store_columns = [&](const Columns& x, uint8_t* to) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int j = 0; j < H::kLoads; ++j) {
-        const int id = tid + j * kBatchThreads;
-        const int c = id / H::kPieces, p = id % H::kPieces;
-        *reinterpret_cast<i32x4*>(
-            to + ((b * 8 + c) * H::kPieces + (p ^ swizzle<MX>(c))) * 16) =
-            x.v[b * H::kLoads + j];
-      }
+    for (int i = 0; i < H::kLoads; ++i) {
+      const int c = col_of(i);
+      *reinterpret_cast<i32x4*>(
+          to + (c * H::kPieces + (piece_of(i) ^ swizzle<MX>(c & 7))) * 16) =
+          x.v[i];
+    }
   };
   // byte offset of fragment i of the lane's column of a block
   auto piece = [&](int i) {
@@ -1356,7 +1358,7 @@ int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   const int64_t steps = most * ((f + 255) / 256);
   const int64_t groups = (d + kBatchRows - 1) / kBatchRows;
   int parts = 8;
-  while (parts < 32 && groups * parts < 512 && steps >= parts * 16) parts *= 2;
+  while (parts < 32 && groups * parts < 512 && steps >= parts * 8) parts *= 2;
   return parts;
 }
 
