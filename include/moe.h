@@ -711,12 +711,13 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
  *   quantization of both.  d and f multiples of 128.  A scale byte of 0
  *   stands for 0 or 2^-127.
  * prec == MOE_MXFP4: MOE_ERR_UNSUPPORTED.
- * Sums are fp32 in a fixed order, S is rounded to bf16 for the second
- * product, y is rounded once.  A token's bits may differ between calls of
+ * Sums are fp32 in a fixed order, S is held as the sum of two bf16 values (16
+ * significant bits), y is rounded once.  A token's bits may differ between calls of
  * different tokens around it.  y may be y_add itself; otherwise outputs and
  * the workspace overlap neither inputs nor each other.  1 <= T <=
  * MOE_LAYER_MAX_TOKENS, E, k and the size of an expert's weight as
- * moe_grouped_mlp_fwd.  Workspace: MOE_ENTRY_LAYER_FWD.
+ * moe_grouped_mlp_fwd, d and f up to 2^20, T k f up to 2^30.  Workspace:
+ * MOE_ENTRY_LAYER_FWD.
  */
 moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
                          const float* bias, const float* logits, int64_t T,

@@ -6,16 +6,25 @@
 //   S_j = p_j silu(x G_{i_j}^T) (x U_{i_j}^T),  y = y_add + sum_j S_j W2_{i_j}^T
 //
 // Bound by reading the weights of the experts that are reached, once: nothing
-// is permuted or staged, weights go from global memory straight into MFMA
-// fragments.
+// is permuted, weights go from global memory straight into MFMA fragments.
+// A kernel that only reads gets 6.1 TB/s here; times below are of kernels
+// alone, traced, weights not in any cache.
 //
-//  * few_route_kernel, a workgroup a token: its scores, their order, the
-//    routing weights.
-//  * few_up_kernel, a workgroup for 8 gate and 8 up rows of an expert: S for
-//    all of the expert's tokens.
-//  * few_down_kernel, a workgroup for 8 rows of y: the sum over all experts
-//    that are reached, in order, so nothing is added twice or in another
-//    order.
+//  * few_logits_kernel: the scores.
+//  * few_topk_kernel: the choice, where the first product does not make it.
+//  * the first product, S for the tokens of each expert: few_up_kernel (up to
+//    8 tokens, bf16 weights) or few_up_batch_kernel.
+//  * the second, the sums over all experts: few_down_kernel (few tokens, few
+//    weights) or few_down_batch_kernel.
+//  * few_sum_kernel, where the second product is cut into parts: y.
+//
+// S is held as the sum of two bf16 values, the second what the first leaves:
+// 16 significant bits, so that y has the error of its own rounding alone.
+// The second product multiplies both as two columns of the same MFMA, which
+// has columns to spare.  (As one bf16 value S would lose up to 2^-8 of each
+// term, more than y's own rounding where terms cancel.)
+//
+// All sums are made in one order, so that equal calls give equal bits.
 //
 // A tile is 8 weight rows x 64 k (bf16), one 16-byte load a lane that covers
 // whole 128-byte lines of a row: lanes 0-7 of each 16 hold the rows' first 32
@@ -54,7 +63,9 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + shfl_xor(v, 32);
 }
 
-// Scores: a wave an expert and token, 4 KB of both in flight.
+// Scores: a wave an expert and token, 4 KB of both in flight.  64 experts of
+// 2048: 3 us for one token, 4.7 for 24, of which a kernel that does next to
+// nothing takes 2 to 4.
 constexpr int kLogitThreads = 256;
 constexpr int kLogitWaves = kLogitThreads / kWave;
 
@@ -91,7 +102,8 @@ __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
     logits[static_cast<int64_t>(t) * E + e] = bias ? z + bias[e] : z;
 }
 
-// The choice of one token from its scores, any number of experts.
+// The choice of one token from its scores, any number of experts.  4.6 us
+// for 24 tokens of 64 experts.
 __global__ __launch_bounds__(kRouteThreads) void few_topk_kernel(
     const float* __restrict__ logits, int E, int k, int renorm,
     int32_t* __restrict__ idx, float* __restrict__ wt) {
@@ -293,8 +305,21 @@ __device__ __forceinline__ bf16x8_v widen(int c0, int c1, uint32_t scale,
   return __builtin_bit_cast(bf16x8_v, o);
 }
 
+// 16 bytes of weights.  NT: rows of whole 128-byte lines; no one else reads
+// these, and marked as non-temporal they come faster (24 tokens, 64 experts of
+// 2048 x 1408 in MXFP8: the first product 70 -> 62 us; one token of 2 experts
+// of 4096 x 14336: 81 -> 73).  Lines that two rows share are read twice, and
+// then the mark costs (61 tokens, 41 experts of 1032 x 680: 28 -> 30 us).
+template <bool NT>
+__device__ __forceinline__ i32x4 weight16(__amdgpu_buffer_rsrc_t r,
+                                          uint32_t off) {
+  constexpr int kNonTemporal = 2;
+  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0,
+                                               NT ? kNonTemporal : 0);
+}
+
 // KC k of 8 weight rows, as loaded; KC / 64 MFMA operands.
-template <bool MX, int KC = kChunkK>
+template <bool MX, bool NT, int KC = kChunkK>
 struct Weights {
   static constexpr int kLoadK = MX ? 128 : 64;
   static constexpr int kLoads = KC / kLoadK;
@@ -310,7 +335,7 @@ struct Weights {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int k = k0 + i * kLoadK + L.k;
-      w[i] = buf_load16(
+      w[i] = weight16<NT>(
           r, k < K ? row + static_cast<uint32_t>(k) * (MX ? 1 : 2) : kOob);
     }
     if constexpr (MX) {
@@ -385,12 +410,37 @@ struct Units {
   }
 };
 
-// Up to kDirect tokens take the kernels whose waves divide the reduction.
-constexpr int kDirect = 4;
+// The direct forms, in which the waves of a workgroup divide the reduction and
+// read the tokens' values themselves, against the batch forms, which stage
+// them in LDS (us):
+//   first product, bf16         direct   batch
+//     8 tokens, 64 x 2048 x 1408    83      96
+//     8 tokens, 8 x 4096 x 14336   262     272
+//     1 token, 64 x 2048 x 1408     20      23
+//   first product, MXFP8, where a token's values are as many loads as the
+//   weights
+//     8 tokens, 64 x 2048 x 1408    55      47
+//     1 token, 8 x 4096 x 14336     50      46
+//     1 token, 64 x 2048 x 1408     14      15
+//   second product, to which the batch form adds few_sum_kernel's 4.7
+//     1 token, bf16, 8 x 4096 x 14336     43    38 + 4.7
+//     4 tokens, bf16, 8 x 4096 x 14336   135   117 + 4.7
+//     2 tokens, bf16, 64 x 2048 x 1408    18    18 + 4.7
+//     4 tokens, MXFP8, 64 x 2048 x 1408   25    20 + 4.7
+// So: the first product direct for bf16 weights up to the 8 columns that a
+// tile has, the second up to the 4 whose two parts fit and as long as few_sum
+// weighs more, by the values that it may have to read.
+constexpr int kDirectUp = 8;
+constexpr int kDirectDown = 4;
+constexpr int64_t kDirectValues = 80000000;
+constexpr int kMaxParts = 32;
 // Up to kChooseTokens and 64 kChooseLanes experts: the waves of a workgroup
 // of the first product choose for the tokens themselves, and the first one
-// writes the choices down.  8 tokens of 8 experts cost 1 us there, 5 in a
-// kernel of its own; from 24 tokens of 64 experts on it is the reverse.
+// writes the choices down: two tokens a wave cost less than few_topk_kernel
+// and its launch (one token of 64 experts, the whole layer 36.8 -> 34.7 us).
+// With six tokens a wave (24 of 64 experts, 8 each) the first product takes 6
+// to 10 us longer, more than the kernel's 4.6; with sixteen (61 of 41, 3
+// each) 13 longer.
 constexpr int kChooseTokens = 8;
 constexpr int kChooseLanes = 4;
 
@@ -555,14 +605,14 @@ __device__ __forceinline__ float swiglu(float a, float u, float wt) {
 // Tiles [t0, t1) of an expert, 8 gate and 8 up rows each, for up to 8 members;
 // the waves divide the reduction.  red: two buffers, `flip` tells which is
 // next.
-template <bool MX>
+template <bool NT>
 __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
                                          int un, int t0, int t1,
                                          float* __restrict__ red, int* flip) {
-  const Lane<MX> L;
+  const Lane<false> L;
   Reached X;
   X.read(U, un);
-  const UpWeights<MX> W(P, X.id);
+  const UpWeights<false> W(P, X.id);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int K = P.d;
@@ -580,8 +630,8 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
   // branch around its loads would make the compiler wait for all that is in
   // flight, every time.
   struct Item {
-    Weights<MX> g, u;
-    Tokens<MX> x;
+    Weights<false, NT> g, u;
+    Tokens<false> x;
   };
   auto load = [&](Item& it, int tile, int k0) {
     const int n = tile * kRows + L.r;
@@ -650,12 +700,13 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
 
 // All tiles of all reached experts in order, divided evenly over the
 // workgroups (what the CUs hold at once, so that starting and finding the
-// experts is paid once).
-template <bool MX>
+// experts is paid once).  One token: 8 experts of 2048 x 1408, 92 MB, 20.8 us;
+// 2 of 4096 x 14336, 470 MB, 73 us (6.4 TB/s).
+template <bool NT>
 __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ __attribute__((aligned(16))) float red[2 * kUpWaves * 512];
-  static_assert(sizeof(red) >= kDirect * kMaxTopK * 8, "room for choices");
+  static_assert(sizeof(red) >= kChooseTokens * kMaxTopK * 8, "room for choices");
   Units U;
   find_units<kUpThreads>(
       P, choose_here<kUpThreads>(P, reinterpret_cast<uint8_t*>(red)), lds, &U);
@@ -669,7 +720,7 @@ __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
   while (at < end) {
     const int un = at / tiles;
     const int t0 = at - un * tiles, t1 = min(tiles, t0 + end - at);
-    up_tiles<MX>(P, U, un, t0, t1, red, &flip);
+    up_tiles<NT>(P, U, un, t0, t1, red, &flip);
     at += t1 - t0;
   }
 }
@@ -680,14 +731,25 @@ __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
 // and a wave holds the sums of its two 8-row tiles whole, so nothing is added
 // across waves.  Tokens stand in blocks of eight columns.
 //
-// A step is kStepK k (512 bytes of a weight row): D of a wave's steps are in
-// flight, 16 KB or more, and 8 waves a CU then cover the memory's latency
-// (128 KB; a kernel that only reads needs as much for 6 TB/s).  The columns
-// of step s + 2 are requested before the weights of step s + D, since loads
-// return in order and waiting for the columns must not wait for those.
-constexpr int kBatchThreads = 256;
-constexpr int kBatchWaves = kBatchThreads / kWave;
-constexpr int kBatchRows = kBatchWaves * 2 * kRows;
+// kAhead steps of kStepK k are in flight, 16 KB a wave and 128 KB a CU; twice
+// as many are no faster, since a CU's rate stops at 25 GB/s for every count of
+// CUs at work (64 workgroups on 64 CUs take four times as long as 256 on
+// 256).  The columns of step s + 2 are requested before the weights of step
+// s + kAhead, since loads return in order and waiting for the columns must not
+// wait for those.
+//
+// First product: two workgroups of four waves a CU.  One of eight waves is
+// faster where all experts are large and 5% slower where they are many (24
+// tokens, 64 experts of 2048 x 1408 62 against 64 us; 64 tokens, 8 of 4096 x
+// 14336 306 against 300).  Second product: one of eight waves, for S's columns
+// are as many bytes as the weights and 128 rows share them (64 tokens, 8 of
+// 4096 x 14336 192 -> 169 us; 24 tokens, 64 of 2048 x 1408 in MXFP8 42 -> 40).
+constexpr int kUpBatchThreads = 256;
+constexpr int kUpBatchWaves = kUpBatchThreads / kWave;
+constexpr int kUpBatchRows = kUpBatchWaves * kRows;
+constexpr int kDownBatchThreads = 512;
+constexpr int kDownBatchWaves = kDownBatchThreads / kWave;
+constexpr int kBatchRows = kDownBatchWaves * 2 * kRows;
 
 // Fewer k a step, and more steps in flight, keep the columns of many blocks
 // within 16 KB a buffer: with 32 KB for eight blocks a CU held one workgroup
@@ -698,9 +760,8 @@ struct BatchShape {
       MX ? (NB <= 2 ? 512 : NB == 4 ? 256 : 128) : (NB <= 4 ? 256 : 128);
   static constexpr int kAhead = kStepK == (MX ? 512 : 256) ? 2 : 4;
   static constexpr int kPieces = kStepK / 8;            // of 16 bytes a column
-  static constexpr int kLoads = NB * 8 * kPieces / kBatchThreads;
+  static constexpr int kColumns = NB * 8 * kPieces;     // pieces of a step
   static constexpr int kBytes = NB * 8 * kPieces * 16;  // of a buffer
-  static_assert(kLoads * kBatchThreads == NB * 8 * kPieces, "whole loads");
 };
 // the most of them up to `blocks`
 template <bool MX>
@@ -751,37 +812,45 @@ struct Cursor {
 //   column(cursor, c, b): byte offset of column c of block b in rx, kOob for
 //     none; K: the columns' length
 //   done(cursor, a, b): called at every step; true clears the sums
-template <bool MX, int NB, class Source>
+template <bool MX, bool NT, int NB, class Source>
 __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
                                       int end, uint8_t* xs) {
   using H = BatchShape<MX, NB>;
   constexpr int D = H::kAhead;
+  constexpr int kThreads = Source::kThreads;
+  // columns' pieces of a thread; a small step leaves some threads none
+  constexpr int kLoads =
+      H::kColumns < kThreads ? 1 : H::kColumns / kThreads;
+  static_assert(H::kColumns % kThreads == 0 || H::kColumns < kThreads,
+                "whole loads");
   static_assert(D % 2 == 0, "the LDS buffer is a compile-time constant");
   const Lane<MX> L;
   const int tid = threadIdx.x, lane = tid & 63;
   const int fr = lane & 15, g = lane >> 4, col = fr & 7;
   struct Columns {
-    i32x4 v[H::kLoads];
+    i32x4 v[kLoads];
   };
   Columns cx[2];
-  Weights<MX, H::kStepK> wa[D], wb[D];
+  Weights<MX, NT, H::kStepK> wa[D], wb[D];
   Cursor at_x(U, begin, end, src.mids, src.rounds), at_w = at_x, at = at_x;
   // piece i of the thread: 16 bytes of column `col_of(i)` (8 a block)
-  auto col_of = [&](int i) { return (tid + i * kBatchThreads) / H::kPieces; };
-  auto piece_of = [&](int i) { return (tid + i * kBatchThreads) % H::kPieces; };
+  auto col_of = [&](int i) { return (tid + i * kThreads) / H::kPieces; };
+  auto piece_of = [&](int i) { return (tid + i * kThreads) % H::kPieces; };
   // byte offsets of the thread's pieces at k = 0, which change with the
   // expert; kOob: none
-  uint32_t from[H::kLoads];
+  uint32_t from[kLoads];
+  const bool has_column = H::kColumns >= kThreads || tid < H::kColumns;
   auto find_columns = [&]() {
 #pragma unroll
-    for (int i = 0; i < H::kLoads; ++i)
-      from[i] = src.column(at_x, col_of(i) & 7, col_of(i) >> 3);
+    for (int i = 0; i < kLoads; ++i)
+      from[i] = has_column ? src.column(at_x, col_of(i) & 7, col_of(i) >> 3)
+                           : kOob;
   };
   find_columns();
   auto load_columns = [&](Columns& x) {
     const int k0 = at_x.left > 0 ? at_x.r * H::kStepK : src.K;
 #pragma unroll
-    for (int i = 0; i < H::kLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const int k = k0 + piece_of(i) * 8;
       x.v[i] = buf_load16(src.rx, k < src.K && from[i] != kOob
                                       ? from[i] + static_cast<uint32_t>(k) * 2
@@ -796,8 +865,9 @@ __device__ __forceinline__ void batch(Source& src, const Units& U, int begin,
     __builtin_amdgcn_sched_barrier(0);
   };
   auto store_columns = [&](const Columns& x, uint8_t* to) {
+    if (!has_column) return;
 #pragma unroll
-    for (int i = 0; i < H::kLoads; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const int c = col_of(i);
       *reinterpret_cast<i32x4*>(
           to + (c * H::kPieces + (piece_of(i) ^ swizzle<MX>(c & 7))) * 16) =
@@ -871,8 +941,9 @@ __device__ __forceinline__ f32x4 join_halves(f32x4 v) {
 
 // Gate and up: steps are (expert, group of 32 rows each, k), a wave's tiles
 // its gate and its up rows.
-template <bool MX, int NB>
+template <bool MX, bool NT, int NB>
 struct UpSource {
+  static constexpr int kThreads = kUpBatchThreads;
   using H = BatchShape<MX, NB>;
   const FewParams& P;
   const Units& U;
@@ -884,7 +955,7 @@ struct UpSource {
       : P(p), U(u),
         rx(make_rsrc(p.x, static_cast<uint32_t>(p.T) * p.d * 2)), K(p.d),
         rounds((p.d + H::kStepK - 1) / H::kStepK),
-        mids((p.f + 4 * kRows - 1) / (4 * kRows)),
+        mids((p.f + kUpBatchRows - 1) / kUpBatchRows),
         wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {}
   __device__ __forceinline__ uint32_t column(const Cursor& at, int c,
                                              int b) const {
@@ -894,10 +965,10 @@ struct UpSource {
                : kOob;
   }
   __device__ __forceinline__ void weights(const Cursor& at,
-                                          Weights<MX, H::kStepK>& a,
-                                          Weights<MX, H::kStepK>& b) const {
+                                          Weights<MX, NT, H::kStepK>& a,
+                                          Weights<MX, NT, H::kStepK>& b) const {
     const UpWeights<MX> W(P, at.X.id);
-    const int n = (at.mid * kBatchWaves + wave) * kRows;
+    const int n = (at.mid * kUpBatchWaves + wave) * kRows;
     const int k0 = at.left > 0 && n < P.f ? at.r * H::kStepK : K;
     a.load(W.rw, W.rs, W.row(P, n + L.r, false), k0, K, L);
     b.load(W.rw, W.rs, W.row(P, n + L.r, true), k0, K, L);
@@ -906,7 +977,7 @@ struct UpSource {
                                        const f32x4* b) const {
     if (at.r + 1 < rounds) return false;
     const int lane = lane_id(), c = lane & 15, qr = lane >> 4;
-    const int n = (at.mid * kBatchWaves + wave) * kRows;
+    const int n = (at.mid * kUpBatchWaves + wave) * kRows;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       if (i * 8 >= at.X.members) break;
@@ -944,23 +1015,27 @@ __device__ __forceinline__ int most_members(const Units& U, int u0, int u1) {
   return __builtin_amdgcn_readfirstlane(most);
 }
 
-template <bool MX, int NB>
+template <bool MX, bool NT, int NB>
 __device__ __forceinline__ void up_batch(const FewParams& P, const Units& U,
                                          int first, int last, uint8_t* xs) {
-  UpSource<MX, NB> src(P, U);
-  batch<MX, NB>(src, U, first * src.rounds, last * src.rounds, xs);
+  UpSource<MX, NT, NB> src(P, U);
+  batch<MX, NT, NB>(src, U, first * src.rounds, last * src.rounds, xs);
 }
 
-// MAXB: blocks of 8 that T tokens can fill.
-template <bool MX, int MAXB>
-__global__ __launch_bounds__(kBatchThreads, 2) void few_up_batch_kernel(
+// MAXB: blocks of 8 that T tokens can fill.  24 tokens, 64 experts of 2048 x
+// 1408 in MXFP8, 368 MB: 62 us (5.9 TB/s); 64 tokens, 8 of 4096 x 14336 in
+// bf16, 1.88 GB: 306 us (6.1 TB/s).  What is left: 2 us until the experts are
+// found, 5 to 15 until the first weights come, and workgroups that have 6
+// groups of rows where others have 5.
+template <bool MX, bool NT, int MAXB>
+__global__ __launch_bounds__(kUpBatchThreads, 2) void few_up_batch_kernel(
     FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   Units U;
   uint8_t* const xs = lds + Units::bytes(P.E, P.T * P.k);
   static_assert(2 * 4096 >= kChooseTokens * kMaxTopK * 8, "room for choices");
-  find_units<kBatchThreads>(P, choose_here<kBatchThreads>(P, xs), lds, &U);
-  const int groups = (P.f + 4 * kRows - 1) / (4 * kRows);
+  find_units<kUpBatchThreads>(P, choose_here<kUpBatchThreads>(P, xs), lds, &U);
+  const int groups = (P.f + kUpBatchRows - 1) / kUpBatchRows;
   const int total = U.count * groups;
   const int n = gridDim.x, me = blockIdx.x;
   const int per = total / n, more = total - per * n;
@@ -969,22 +1044,22 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_up_batch_kernel(
   if (first >= last) return;
   const int most = most_members(U, first / groups, (last - 1) / groups + 1);
   if (MAXB == 1 || most <= 8)
-    up_batch<MX, 1>(P, U, first, last, xs);
+    up_batch<MX, NT, 1>(P, U, first, last, xs);
   else if (MAXB == 2 || most <= 16)
-    up_batch<MX, MAXB >= 2 ? 2 : 1>(P, U, first, last, xs);
+    up_batch<MX, NT, MAXB >= 2 ? 2 : 1>(P, U, first, last, xs);
   else if (MAXB == 4 || most <= 32)
-    up_batch<MX, MAXB >= 4 ? 4 : 1>(P, U, first, last, xs);
+    up_batch<MX, NT, MAXB >= 4 ? 4 : 1>(P, U, first, last, xs);
   else
-    up_batch<MX, MAXB >= 8 ? 8 : 1>(P, U, first, last, xs);
+    up_batch<MX, NT, MAXB >= 8 ? 8 : 1>(P, U, first, last, xs);
 }
 
 // Down: steps are (expert, k), a wave's tiles 16 rows of y.  A block holds
 // four members, each as two columns, S's larger and smaller part; members
 // past what NB blocks hold are left to further passes.
-template <bool MX, int NB>
+template <bool MX, bool NT, int NB>
 struct DownSource {
+  static constexpr int kThreads = kDownBatchThreads;
   using H = BatchShape<MX, NB>;
-  static constexpr int kMembers = 4 * NB;
   const FewParams& P;
   const Units& U;
   __amdgpu_buffer_rsrc_t rx;
@@ -1007,8 +1082,8 @@ struct DownSource {
                : kOob;
   }
   __device__ __forceinline__ void weights(const Cursor& at,
-                                          Weights<MX, H::kStepK>& a,
-                                          Weights<MX, H::kStepK>& b) const {
+                                          Weights<MX, NT, H::kStepK>& a,
+                                          Weights<MX, NT, H::kStepK>& b) const {
     // an expert without members in this pass is not read
     const bool in = at.left > 0 && n0 < P.d && skip < at.X.members;
     const int64_t o = (at.X.id * static_cast<int64_t>(P.d) + (in ? n0 : 0)) *
@@ -1054,7 +1129,7 @@ struct DownSource {
 template <bool MX>
 constexpr int kPartK = MX ? 512 : 256;
 
-template <bool MX, int NB>
+template <bool MX, bool NT, int NB>
 __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
                                            int begin, int end, int most,
                                            int n0, float* plane,
@@ -1063,14 +1138,16 @@ __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
   const int rounds = (P.f + kPartK<MX> - 1) / kPartK<MX> * kSteps;
   for (int skip = 0; skip < most; skip += 4 * NB) {
     if (skip) __syncthreads();        // xs is free again
-    DownSource<MX, NB> src(P, U, rounds, n0, skip, plane);
-    batch<MX, NB>(src, U, begin * kSteps, end * kSteps, xs);
+    DownSource<MX, NT, NB> src(P, U, rounds, n0, skip, plane);
+    batch<MX, NT, NB>(src, U, begin * kSteps, end * kSteps, xs);
   }
 }
 
-// MAXB: blocks of 4 members that T tokens can fill, up to 8.
-template <bool MX, int MAXB>
-__global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
+// MAXB: blocks of 4 members that T tokens can fill, up to 8.  24 tokens, 64
+// experts of 2048 x 1408 in MXFP8, 184 MB: 40 us; 64 tokens, 8 of 4096 x 14336
+// in bf16, 0.94 GB: 169 us.
+template <bool MX, bool NT, int MAXB>
+__global__ __launch_bounds__(kDownBatchThreads, 2) void few_down_batch_kernel(
     FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, T = P.T;
@@ -1078,13 +1155,13 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
   const int group = blockIdx.x / P.parts, part = blockIdx.x - group * P.parts;
   float* const planes =
       reinterpret_cast<float*>(lds + Units::bytes(P.E, T * P.k));
-  for (int i = tid; i < kBatchWaves * T * 16; i += kBatchThreads)
+  for (int i = tid; i < kDownBatchWaves * T * 16; i += kDownBatchThreads)
     planes[i] = 0;
   Units U;
-  find_units<kBatchThreads>(P, Choices{P.idx, P.wt}, lds, &U);
+  find_units<kDownBatchThreads>(P, Choices{P.idx, P.wt}, lds, &U);
   float* const plane = planes + wave * T * 16;
   uint8_t* const xs =
-      reinterpret_cast<uint8_t*>(planes + kBatchWaves * T * 16);
+      reinterpret_cast<uint8_t*>(planes + kDownBatchWaves * T * 16);
   const int n0 = group * kBatchRows + wave * 16;
   const int pieces = (P.f + kPartK<MX> - 1) / kPartK<MX>;
   const int64_t total = static_cast<int64_t>(U.count) * pieces;
@@ -1094,13 +1171,13 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
     const int most =
         most_members(U, begin / pieces, (end - 1) / pieces + 1);
     if (most <= 4)
-      down_batch<MX, 1>(P, U, begin, end, most, n0, plane, xs);
+      down_batch<MX, NT, 1>(P, U, begin, end, most, n0, plane, xs);
     else if (MAXB == 2 || most <= 8)
-      down_batch<MX, 2>(P, U, begin, end, most, n0, plane, xs);
+      down_batch<MX, NT, 2>(P, U, begin, end, most, n0, plane, xs);
     else if (MAXB == 4 || most <= 16)
-      down_batch<MX, MAXB >= 4 ? 4 : 2>(P, U, begin, end, most, n0, plane, xs);
+      down_batch<MX, NT, MAXB >= 4 ? 4 : 2>(P, U, begin, end, most, n0, plane, xs);
     else
-      down_batch<MX, MAXB >= 8 ? 8 : 2>(P, U, begin, end, most, n0, plane, xs);
+      down_batch<MX, NT, MAXB >= 8 ? 8 : 2>(P, U, begin, end, most, n0, plane, xs);
   }
   // the wave's own rows of the part's sums
   for (int i = lane; i < T * 4; i += kWave) {
@@ -1113,8 +1190,9 @@ __global__ __launch_bounds__(kBatchThreads, 2) void few_down_batch_kernel(
 }
 
 // -------------------------------------------------------------------- down
-// Up to kDirect tokens: the columns of a tile are the tokens, each as two,
-// S's larger and smaller part, and a wave's sums run over all experts.
+// The direct form: the columns of a tile are the tokens, each as two, S's
+// larger and smaller part, and a wave's sums run over all experts.  One token,
+// 8 experts of 2048 x 1408, 46 MB: 10.3 us.
 constexpr int kDownThreads = 1024;
 constexpr int kDownWaves = kDownThreads / kWave;
 constexpr int kAhead = 3;             // chunks of a wave in flight
@@ -1122,7 +1200,7 @@ constexpr int kAhead = 3;             // chunks of a wave in flight
 // A workgroup of sixteen waves a CU goes through its tiles of y: (tile,
 // expert, chunk) in order, dealt in turn to the waves, the next tile's loads
 // in flight while one is added up.
-template <bool MX>
+template <bool MX, bool NT>
 __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     FewParams P) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -1143,7 +1221,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
   const int t = L.r >> 1;              // the token of the lane's column
 
   struct Item {
-    Weights<MX> w;
+    Weights<MX, NT> w;
     Tokens<MX> x;
   };
   // items of a tile are dealt in turn to the waves of all parts; a wave makes
@@ -1239,7 +1317,8 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     if (i < left) one(it[i]);
 }
 
-// y = y_add + the parts; n values, a multiple of 8.  Four lanes share four
+// y = y_add + the parts; n values, a multiple of 8.  4.7 us, as for any kernel
+// that waits for memory once after a large one.  Four lanes share four
 // values, each with every fourth part.
 __global__ __launch_bounds__(256) void few_sum_kernel(
     const float* __restrict__ part, int parts, int64_t n, const bf16_t* y_add,
@@ -1274,65 +1353,82 @@ __global__ __launch_bounds__(256) void few_sum_kernel(
 // Experts that T tokens can reach.
 int most_units(int T, int k, int E) { return T * k < E ? T * k : E; }
 
-template <bool MX>
-hipError_t launch_direct(const FewParams& P, hipStream_t s) {
-  const int units = Units::bytes(P.E, P.T * P.k);
+// Whether a product of T tokens takes its direct form.
+bool direct_up(bool mx, int T) { return !mx && T <= kDirectUp; }
+bool direct_down(int64_t T, int k, int E, int64_t d, int64_t f) {
+  return T <= kDirectDown &&
+         most_units(static_cast<int>(T), k, E) * d * f <= kDirectValues;
+}
+
+template <bool NT>
+hipError_t launch_up(const FewParams& P, hipStream_t s) {
   // four workgroups a CU, or fewer where the tiles cannot be more
   const int64_t most =
       static_cast<int64_t>(most_units(P.T, P.k, P.E)) * (P.f / kRows);
-  hipLaunchKernelGGL(few_up_kernel<MX>,
+  hipLaunchKernelGGL(few_up_kernel<NT>,
                      dim3(static_cast<uint32_t>(most < 1024 ? most : 1024)),
-                     dim3(kUpThreads), units, s, P);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const uint32_t tiles = P.d / kRows;
-  hipLaunchKernelGGL(few_down_kernel<MX>,
-                     dim3((tiles < 256 ? tiles : 256) * P.parts),
-                     dim3(kDownThreads), units, s, P);
+                     dim3(kUpThreads), Units::bytes(P.E, P.T * P.k), s, P);
   return hipGetLastError();
 }
 
-template <bool MX, int MAXB>
+template <bool MX, bool NT, int MAXB>
 hipError_t launch_up_batch(const FewParams& P, hipStream_t s) {
   // two workgroups a CU, or fewer where the groups cannot be more
   const int64_t most = static_cast<int64_t>(most_units(P.T, P.k, P.E)) *
-                       ((P.f + 4 * kRows - 1) / (4 * kRows));
+                       ((P.f + kUpBatchRows - 1) / kUpBatchRows);
   hipLaunchKernelGGL(
-      (few_up_batch_kernel<MX, MAXB>),
+      (few_up_batch_kernel<MX, NT, MAXB>),
       dim3(static_cast<uint32_t>(most < 512 ? most : 512)),
-      dim3(kBatchThreads),
+      dim3(kUpBatchThreads),
       Units::bytes(P.E, P.T * P.k) + 2 * batch_bytes<MX>(MAXB), s, P);
   return hipGetLastError();
 }
 
-template <bool MX, int MAXB>
+template <bool MX, bool NT>
+hipError_t launch_first(const FewParams& P, hipStream_t s) {
+  if constexpr (!MX)
+    if (direct_up(MX, P.T)) return launch_up<NT>(P, s);
+  if constexpr (MX)
+    if (P.T <= 8) return launch_up_batch<MX, NT, 1>(P, s);
+  return P.T <= 16   ? launch_up_batch<MX, NT, 2>(P, s)
+         : P.T <= 32 ? launch_up_batch<MX, NT, 4>(P, s)
+                     : launch_up_batch<MX, NT, 8>(P, s);
+}
+
+template <bool MX, bool NT, int MAXB>
 hipError_t launch_down_batch(const FewParams& P, hipStream_t s) {
   const uint32_t groups = (P.d + kBatchRows - 1) / kBatchRows;
   hipLaunchKernelGGL(
-      (few_down_batch_kernel<MX, MAXB>), dim3(groups * P.parts),
-      dim3(kBatchThreads),
-      Units::bytes(P.E, P.T * P.k) + kBatchWaves * P.T * 64 +
+      (few_down_batch_kernel<MX, NT, MAXB>), dim3(groups * P.parts),
+      dim3(kDownBatchThreads),
+      Units::bytes(P.E, P.T * P.k) + kDownBatchWaves * P.T * 64 +
           2 * batch_bytes<MX>(MAXB),
       s, P);
   return hipGetLastError();
 }
 
-template <bool MX>
-hipError_t launch_batch(const FewParams& P, hipStream_t s) {
-  hipError_t e = P.T <= 8    ? launch_up_batch<MX, 1>(P, s)
-                 : P.T <= 16 ? launch_up_batch<MX, 2>(P, s)
-                 : P.T <= 32 ? launch_up_batch<MX, 4>(P, s)
-                             : launch_up_batch<MX, 8>(P, s);
-  if (e != hipSuccess) return e;
-  return P.T <= 8    ? launch_down_batch<MX, 2>(P, s)
-         : P.T <= 16 ? launch_down_batch<MX, 4>(P, s)
-                     : launch_down_batch<MX, 8>(P, s);
+template <bool MX, bool NT>
+hipError_t launch_second(const FewParams& P, hipStream_t s) {
+  if (direct_down(P.T, P.k, P.E, P.d, P.f)) {
+    const uint32_t tiles = P.d / kRows;
+    hipLaunchKernelGGL((few_down_kernel<MX, NT>),
+                       dim3((tiles < 256 ? tiles : 256) * P.parts),
+                       dim3(kDownThreads), Units::bytes(P.E, P.T * P.k), s, P);
+    return hipGetLastError();
+  }
+  return P.T <= 8    ? launch_down_batch<MX, NT, 2>(P, s)
+         : P.T <= 16 ? launch_down_batch<MX, NT, 4>(P, s)
+                     : launch_down_batch<MX, NT, 8>(P, s);
 }
 
 template <bool MX>
 hipError_t launch_few(const FewParams& P, hipStream_t s) {
-  const hipError_t e = P.T <= kDirect ? launch_direct<MX>(P, s)
-                                      : launch_batch<MX>(P, s);
+  // rows of whole 128-byte lines
+  hipError_t e = MX || P.d % 64 == 0 ? launch_first<MX, true>(P, s)
+                                     : launch_first<MX, MX>(P, s);
+  if (e != hipSuccess) return e;
+  e = MX || P.f % 64 == 0 ? launch_second<MX, true>(P, s)
+                          : launch_second<MX, MX>(P, s);
   if (e != hipSuccess || P.parts == 1) return e;
   const int64_t n = static_cast<int64_t>(P.T) * P.d;
   hipLaunchKernelGGL(few_sum_kernel,
@@ -1341,11 +1437,14 @@ hipError_t launch_few(const FewParams& P, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts that the reduction of y is cut into, so that all CUs have work, but
-// not more than its steps allow.
+// Parts that the reduction of y is cut into.  The direct form: so that all
+// CUs have work, but a round of the waves at least.  The batch form always
+// leaves its sums to few_sum_kernel: one workgroup a CU, four steps each at
+// least (61 tokens, 41 experts of 1032 x 680: 28 parts 20.5 us; by eight steps
+// 8 parts, 26 us).
 int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   const int64_t most = most_units(static_cast<int>(T), k, E);
-  if (T <= kDirect) {
+  if (direct_down(T, k, E, d, f)) {
     const int64_t items = most * ((f + kChunkK - 1) / kChunkK);
     int parts = 1;
     while (parts < 8 && d / kRows * parts * 2 <= 256 &&
@@ -1353,13 +1452,11 @@ int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
       parts *= 2;
     return parts;
   }
-  // a multiple of 8: workgroups of the same part then lie on the same XCD,
-  // whose L2 holds the part's rows of S
   const int64_t steps = most * ((f + 255) / 256);
   const int64_t groups = (d + kBatchRows - 1) / kBatchRows;
-  int parts = 8;
-  while (parts < 32 && groups * parts < 512 && steps >= parts * 8) parts *= 2;
-  return parts;
+  int64_t parts = 256 / groups < steps / 4 ? 256 / groups : steps / 4;
+  parts = parts < kMaxParts ? parts : kMaxParts;
+  return static_cast<int>(parts > 2 ? parts : 2);
 }
 
 // Workspace: S, the parts' sums, the scores.

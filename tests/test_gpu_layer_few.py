@@ -5,15 +5,20 @@ kernel's arithmetic, u = 2^-24:
     additions in a row, e_z = (d / 64 + 16) u sum |x w|;
   * a routing weight: its exponent is off by 2 e_z, expf and the division by
     4 u, the sum by (E + 16) u at most: w (2 e_z + (E + 24) u);
-  * gate and up: a wave adds 4 products of 32 k for each 2048 k, then 16
-    sums are added: c = 128 ceil(d / 2048) + 16 additions in a row at most,
-    e_a = c u sum |x G|;
+  * gate and up: each half of a wave's lanes adds 32 products for every 64 k.
+    Where a wave goes through the whole sum it joins two halves, 32 ceil(d /
+    64) + 1 additions in a row at most; where four waves take 256 k in turn,
+    128 ceil(d / 1024) and 8 sums: with c the larger, e_a = c u sum |x G|;
   * S = w silu(a) v: silu has a slope below 1.1 and costs 8 u (exponential,
     reciprocal, products): e_S = |w| (|v| (1.1 e_a + 8 u |a|) + |silu(a)|
-    e_v) + |S| (2 e_z + (E + 28) u), and half a step of bf16, 2^-8 |S|;
-  * y: a wave adds 4 products of 32 k for each 2048 k of the experts reached
-    and joins n of them (n, and 16 sums): with c' the additions,
-    sum (e_S + 2^-8 |S| + c' u |S|) |W2| + 2 u |y_add| + 2^-8 |y|.
+    e_v) + |S| (2 e_z + (E + 28) u), and it is held as two bf16 values, the
+    second of which rounds what the first leaves: 2^-8 2^-8 |S|;
+  * y: where a wave adds an expert's products whole, 32 ceil(f / 64) in a row
+    and then two halves, S's two parts, n experts, and at most 32 parts of the
+    reduction (8 in a row, then 2 sums); where 16 waves take 256 k of the n
+    experts in turn, 128 ceil(n ceil(f / 256) / 16), then 32 sums, S's parts
+    and up to 8 parts: with c' the larger, sum (e_S + c' u |S| (1 + 2^-7))
+    |W2| + 2 u |y_add| + 2^-8 |y|, where 1 + 2^-7 is above |S's parts| / |S|.
 """
 
 import math
@@ -114,9 +119,10 @@ def reference(c, renorm=True):
     y = torch.zeros(T, d, dtype=torch.float64, device=x.device)
     b = torch.zeros_like(y)
     reached = torch.unique(idx).tolist()
-    cy = 128 * math.ceil(len(reached) * math.ceil(f / 256) / 8) + len(
-        reached) + 16
-    ca = 128 * math.ceil(d / 2048) + 16
+    n = len(reached)
+    ca = max(32 * math.ceil(d / 64) + 1, 128 * math.ceil(d / 1024) + 8)
+    cy = max(32 * math.ceil(f / 64) + 2 + n + 10,
+             128 * math.ceil(n * math.ceil(f / 256) / 16) + 32 + 1 + 8)
     for e in reached:
         tok, slot = torch.nonzero(idx == e, as_tuple=True)
         if c.mx:
@@ -130,9 +136,9 @@ def reference(c, renorm=True):
         pw = w[tok, slot][:, None]
         S = pw * sl * v
         eS = (pw * (v.abs() * (1.1 * ea + 8 * U * a.abs()) + sl.abs() * ev) +
-              S.abs() * (rel[tok] + 4 * U) + 2.0 ** -8 * S.abs())
+              S.abs() * (rel[tok] + 4 * U) + 2.0 ** -16 * S.abs())
         y[tok] += S @ w2.t()
-        b[tok] += (eS + cy * U * S.abs()) @ w2.abs().t()
+        b[tok] += (eS + cy * U * (1 + 2.0 ** -7) * S.abs()) @ w2.abs().t()
     if c.y_add is not None:
         y += c.y_add.double()
         b += 2 * U * c.y_add.double().abs()
