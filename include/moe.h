@@ -716,7 +716,7 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
  * different tokens around it.  y may be y_add itself; otherwise outputs and
  * the workspace overlap neither inputs nor each other.  1 <= T <=
  * MOE_LAYER_MAX_TOKENS, E, k and the size of an expert's weight as
- * moe_grouped_mlp_fwd, d and f up to 2^20, T k f up to 2^30.  Workspace:
+ * moe_grouped_mlp_fwd, d and f up to 2^20, 4 T k f up to 4 GiB - 256.  Workspace:
  * MOE_ENTRY_LAYER_FWD.
  */
 moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,

@@ -202,6 +202,11 @@ constexpr int kNormTensors = 160;
 constexpr int kNormGroups = 1024;
 constexpr int kNormBytes = kThreads * 32;       // a chunk: 32 bytes a thread
 constexpr int kNormAhead = 2;                   // chunks in flight
+// Gradients of more than the memory-side cache holds are read as non-temporal
+// (64 experts of 2048 x 1408, 1.1 GB: 181 -> 173 us); smaller ones are left
+// where the step that follows finds them (three blocks of 7 experts of 1032 x
+// 680, norm and step 142 us, and 149 with the mark).
+constexpr int64_t kNormCached = int64_t{256} << 20;
 
 struct NormTable {
   const void* g[kNormTensors];
@@ -228,6 +233,7 @@ __device__ __forceinline__ double square_add(float v, double s) {
 // Chunks are counted in bytes, so that what is in flight does not depend on a
 // tensor's type; a resource that ends with the tensor zeroes what lies past
 // it.
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(
     NormTable P, double* __restrict__ part) {
   __shared__ double red[kThreads / kWave];
@@ -253,7 +259,9 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t off = (h * kThreads + threadIdx.x) * 16;
-        raw[u][h] = buf_load16(rs, off);
+        constexpr int kNonTemporal = 2;
+        raw[u][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            rs, off, 0, NT ? kNonTemporal : 0);
         if (bytes & 2)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -494,8 +502,13 @@ hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
   const auto chunks_of = [&](int i) {
     return (bytes(i) + kNormBytes - 1) / kNormBytes;
   };
-  int64_t all = 0;
-  for (int i = 0; i < count; ++i) all += chunks_of(i);
+  int64_t all = 0, total = 0;
+  for (int i = 0; i < count; ++i) {
+    all += chunks_of(i);
+    total += bytes(i);
+  }
+  const auto kernel =
+      total > kNormCached ? grad_norm_kernel<true> : grad_norm_kernel<false>;
   const int groups = static_cast<int>(
       all < 1 ? 1 : all < kNormGroups ? all : kNormGroups);
   // each launch adds to what the ones before it left
@@ -519,7 +532,7 @@ hipError_t launch_grad_norm(const moe_grad* grads, int count, float* norm,
     P.chunks = static_cast<uint32_t>(chunks);
     P.add = !first;
     first = false;
-    hipLaunchKernelGGL(grad_norm_kernel, dim3(groups), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL(kernel, dim3(groups), dim3(kThreads), 0, s,
                        P, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

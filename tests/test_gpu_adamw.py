@@ -17,6 +17,8 @@ bounds from the arithmetic of include/moe.h, u = 2^-24:
     and half a step of p's type.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -223,6 +225,23 @@ def test_grad_norm_extremes_and_many_tensors():
     assert of(many) == float("inf")
     many[300][0] = float("nan")
     assert np.isnan(of(many))
+
+
+@gpu
+@pytest.mark.parametrize("more", [-3, 5])
+def test_grad_norm_around_256_mib(more):
+    """Both ways of reading, a whole one below and one above 256 MiB; fp64
+    sums of a hundred million terms are far below the one rounding."""
+    dev = torch.device("cuda:0")
+    n = (1 << 27) - 16 + more
+    gs = [I.make_tensor((n,), seed=3, dtype=BF, device=dev),
+          torch.tensor([2e4, -3e4, 1e4], device=dev), _grad(11, BF, 4, 1e3)]
+    norm = torch.empty(1, device=dev)
+    ws = torch.empty(8192, dtype=torch.uint8, device=dev)
+    moe.moe_grad_norm(moe.grad_table(gs), norm, ws)
+    want = math.sqrt(sum(float((q.double() ** 2).sum()) for g in gs
+                         for q in g.split(1 << 24)))
+    assert abs(float(norm.double()) - want) <= 1.001 * U * want
 
 
 @gpu
