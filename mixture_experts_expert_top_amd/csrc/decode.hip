@@ -1223,6 +1223,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
   struct Item {
     Weights<MX, NT> w;
     Tokens<MX> x;
+    bool has;                         // the lane's token, this expert
   };
   // items of a tile are dealt in turn to the waves of all parts; a wave makes
   // `rounds` of them, the last one masked where there are fewer
@@ -1245,6 +1246,7 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
                        : rw;
     it.w.load(rw, rs, row, k0, K, L);
     const bool has = (X.tokens >> t) & 1;
+    it.has = has;
     const int sl = U.slot[X.first +
                           (has ? __popc(X.tokens & ((1 << t) - 1)) : 0)];
     it.x.load(rx,
@@ -1292,9 +1294,14 @@ __global__ __launch_bounds__(kDownThreads, 4) void few_down_kernel(
     flip ^= 1;
     acc = f32x4{};
   };
-  auto multiply = [&](const Item& c) {
+  // Columns of tokens that are not the expert's are left out: 0 times one of
+  // its infinities or NaN is no 0.
+  auto multiply = [&](const Item& i) {
+    f32x4 sum = {};
 #pragma unroll
-    for (int s = 0; s < 4; ++s) acc = mma(c.w.frag(s, L), c.x.frag(s), acc);
+    for (int s = 0; s < 4; ++s) sum = mma(i.w.frag(s, L), i.x.frag(s), sum);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += i.has ? sum[v] : 0.0f;
   };
   int tile = group, c = 0;
   auto one = [&](const Item& i) {

@@ -419,3 +419,30 @@ def test_an_expert_past_32_members_and_small_ones(mx):
     c.logits = L
     c.run()
     check(c)
+
+
+@gpu
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [2, 3, 4, 7, 20])
+def test_bad_weights_stay_with_their_expert(T, mx):
+    """A NaN, an infinity or (MXFP8) a NaN scale reaches the tokens of its
+    expert, in the columns that it belongs to, and no others."""
+    c = Case(T, 256, 384, 4, 1, mx=mx, seed=8)
+    c.logits = torch.full((T, 4), -9.0, device="cuda:0")
+    t = torch.arange(T, device="cuda:0")
+    c.logits[t, t % 3] = 2.0
+    want = c.run().clone()
+    if mx:
+        c.w[0][3].fill_(127)               # nobody's
+        c.w[1][0, 9, 77] = 127             # a NaN of E4M3
+        c.s[1][1, 30, 5] = 255             # a NaN of E8M0
+    else:
+        c.w[0][3].fill_(float("nan"))
+        c.w[1][0, 9, 77] = float("nan")
+        c.w[1][1, 30, 5] = float("inf")
+    got = c.run()
+    bad = torch.zeros(T, 256, dtype=torch.bool, device="cuda:0")
+    bad[t % 3 == 0, 9] = True
+    bad[t % 3 == 1, 30] = True
+    assert torch.equal(got[~bad], want[~bad])
+    assert not torch.isfinite(got[bad]).any()
