@@ -530,6 +530,8 @@ class AdamW:
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
                  weight_decay=0.1, moments=MOE_MOMENTS_FP32, master=True,
                  max_norm=None):
+        if max_norm is not None and not 0 < max_norm <= 3.4e38:
+            raise ValueError("AdamW: max_norm must be finite and above 0")
         self.betas, self.eps, self.max_norm = betas, eps, max_norm
         rows = []
         for w, g, *wd in params:

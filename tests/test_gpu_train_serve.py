@@ -232,3 +232,11 @@ def test_refusals():
         AdamW([(w["w2"].cpu(), w["w2"].cpu())])
     with pytest.raises(ValueError):
         AdamW([])
+
+
+@gpu
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("nan"), float("inf")])
+def test_adamw_refuses_a_norm_to_clip_to(bad):
+    w = torch.zeros(8, dtype=BF, device="cuda:0")
+    with pytest.raises(ValueError, match="max_norm"):
+        AdamW([(w, torch.zeros_like(w))], max_norm=bad)
