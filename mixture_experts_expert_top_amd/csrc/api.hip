@@ -552,7 +552,8 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
       return mx_bwd_layout(Tk, E, d, f, mx_bwd_base(Tk, f)).total;
     case MOE_ENTRY_LAYER_FWD:
-      if (T > moe::kFewTokens || k > moe::kMaxTopK || d < 1 || f < 1) return 0;
+      if (T > moe::kFewTokens || k > moe::kMaxTopK) return 0;
+      if (d < 1 || d > moe::kFewWidth || f < 1 || f > moe::kFewWidth) return 0;
       return moe::layer_fwd_workspace(T, k, E, d, f);
     default:
       break;
@@ -1559,7 +1560,7 @@ moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
   if (moe_status st = check_mlp_dims(E, T * k, d, f, prec)) return st;
   if (mx)
     if (moe_status st = check_mx_dims(d, f)) return st;
-  REQUIRE(d <= (int64_t{1} << 20) && f <= (int64_t{1} << 20),
+  REQUIRE(d <= moe::kFewWidth && f <= moe::kFewWidth,
           MOE_ERR_UNSUPPORTED, "d and f must be at most 2^20");
   REQUIRE(T * k * f * 4 <= kMaxRange, MOE_ERR_UNSUPPORTED,
           "T * k * f is too large");

@@ -10,6 +10,8 @@ namespace moe {
 
 // tokens of a call: a wave has a lane for each
 constexpr int kFewTokens = 64;
+// d and f of a call: byte offsets within a few rows stay below 2^32
+constexpr int64_t kFewWidth = int64_t{1} << 20;
 
 struct LayerArgs {
   const uint16_t* x;           // [T][d]

@@ -72,5 +72,6 @@ def test_workspace():
     assert W() >= 4 * 2 * 128 * 2
     assert W(T=64) >= 64 * 2 * 128 * 2
     for kw in (dict(T=65), dict(T=0), dict(k=9), dict(E=0), dict(E=2000),
-               dict(E=64, k=33), dict(d=0), dict(f=0), dict(prec=9)):
+               dict(E=64, k=33), dict(d=0), dict(f=0), dict(prec=9),
+               dict(d=(1 << 20) + 8), dict(f=1 << 40)):
         assert W(**kw) == 0, kw
