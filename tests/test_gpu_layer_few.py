@@ -292,9 +292,10 @@ def test_sum_into_y_and_neighbours(mx):
 
 
 @gpu
-def test_past_32_bit_offsets():
+@pytest.mark.parametrize("T", [2, 12])
+def test_past_32_bit_offsets(T):
     """Weights past 4 GiB, the last and the first expert."""
-    T, d, f, E, k = 2, 4096, 14336, 20, 2
+    d, f, E, k = 4096, 14336, 20, 2
     c = Case(1, 8, 8, 1, 1)
     dev = torch.device("cuda:0")
     c.T, c.d, c.f, c.E, c.k = T, d, f, E, k
