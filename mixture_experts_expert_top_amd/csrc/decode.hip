@@ -433,7 +433,6 @@ struct Units {
 constexpr int kDirectUp = 8;
 constexpr int kDirectDown = 4;
 constexpr int64_t kDirectValues = 80000000;
-constexpr int kMaxParts = 32;
 // Up to kChooseTokens and 64 kChooseLanes experts: the waves of a workgroup
 // of the first product choose for the tokens themselves, and the first one
 // writes the choices down: two tokens a wave cost less than few_topk_kernel
@@ -1446,9 +1445,12 @@ hipError_t launch_few(const FewParams& P, hipStream_t s) {
 
 // Parts that the reduction of y is cut into.  The direct form: so that all
 // CUs have work, but a round of the waves at least.  The batch form always
-// leaves its sums to few_sum_kernel: one workgroup a CU, four steps each at
-// least (61 tokens, 41 experts of 1032 x 680: 28 parts 20.5 us; by eight steps
-// 8 parts, 26 us).
+// leaves its sums to few_sum_kernel: one workgroup a CU, a step each at least
+// (34 tokens, 11 experts of 1664 x 160: 11 parts 11.7 us, 5 parts 18.6, 2
+// parts 27; 61 tokens, 41 experts of 1032 x 680: 28 parts 20.5, 8 parts 26),
+// and up to kMaxParts, past which few_sum_kernel takes what the product gains
+// (11 tokens, 111 experts of 512 x 2688 in MXFP8: 64 parts 20 us, 32 30).
+constexpr int kMaxParts = 64;
 int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   const int64_t most = most_units(static_cast<int>(T), k, E);
   if (direct_down(T, k, E, d, f)) {
@@ -1461,7 +1463,7 @@ int down_parts(int64_t T, int k, int E, int64_t d, int64_t f) {
   }
   const int64_t steps = most * ((f + 255) / 256);
   const int64_t groups = (d + kBatchRows - 1) / kBatchRows;
-  int64_t parts = 256 / groups < steps / 4 ? 256 / groups : steps / 4;
+  int64_t parts = 256 / groups < steps ? 256 / groups : steps;
   parts = parts < kMaxParts ? parts : kMaxParts;
   return static_cast<int>(parts > 2 ? parts : 2);
 }

@@ -14,8 +14,8 @@ kernel's arithmetic, u = 2^-24:
     e_v) + |S| (2 e_z + (E + 28) u), and it is held as two bf16 values, the
     second of which rounds what the first leaves: 2^-8 2^-8 |S|;
   * y: where a wave adds an expert's products whole, 32 ceil(f / 64) in a row
-    and then two halves, S's two parts, n experts, and at most 32 parts of the
-    reduction (8 in a row, then 2 sums); where 16 waves take 256 k of the n
+    and then two halves, S's two parts, n experts, and at most 64 parts of the
+    reduction (16 in a row, then 2 sums); where 16 waves take 256 k of the n
     experts in turn, 128 ceil(n ceil(f / 256) / 16), then 32 sums, S's parts
     and up to 8 parts: with c' the larger, sum (e_S + c' u |S| (1 + 2^-7))
     |W2| + 2 u |y_add| + 2^-8 |y|, where 1 + 2^-7 is above |S's parts| / |S|.
@@ -121,7 +121,7 @@ def reference(c, renorm=True):
     reached = torch.unique(idx).tolist()
     n = len(reached)
     ca = max(32 * math.ceil(d / 64) + 1, 128 * math.ceil(d / 1024) + 8)
-    cy = max(32 * math.ceil(f / 64) + 2 + n + 10,
+    cy = max(32 * math.ceil(f / 64) + 2 + n + 18,
              128 * math.ceil(n * math.ceil(f / 256) / 16) + 32 + 1 + 8)
     for e in reached:
         tok, slot = torch.nonzero(idx == e, as_tuple=True)
@@ -167,7 +167,8 @@ SIZES = [
     (17, 136, 1000, 5, 1), (24, 512, 264, 64, 8), (32, 2304, 40, 2, 1),
     (33, 72, 2600, 6, 2), (61, 1032, 680, 41, 3), (64, 128, 128, 1, 1),
     (64, 96, 48, 130, 32), (7, 16, 24, 1024, 32), (64, 24, 16, 1024, 4),
-    (1, 4104, 2056, 3, 2), (40, 4096, 24, 300, 2)]
+    (1, 4104, 2056, 3, 2), (40, 4096, 24, 300, 2), (34, 1664, 160, 11, 6),
+    (64, 512, 2048, 20, 8)]
 
 
 @gpu
