@@ -63,25 +63,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v + shfl_xor(v, 32);
 }
 
-// Scores: a wave an expert and token, 4 KB of both in flight.  64 experts of
-// 2048: 3 us for one token, 4.7 for 24, of which a kernel that does next to
-// nothing takes 2 to 4.
-constexpr int kLogitThreads = 256;
-constexpr int kLogitWaves = kLogitThreads / kWave;
-
-__global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
-    const bf16_t* __restrict__ x, const bf16_t* __restrict__ w_g,
-    const float* __restrict__ bias, int d, int E, float* __restrict__ logits) {
-  const int lane = threadIdx.x & 63;
-  const int e = __builtin_amdgcn_readfirstlane(
-      blockIdx.x * kLogitWaves + (threadIdx.x >> 6));
-  const int t = blockIdx.y;
-  if (e >= E) return;
+// x[t] . w_g[e] by one wave, 4 KB of both in flight; in every lane.
+__device__ __forceinline__ float score(const bf16_t* __restrict__ x,
+                                       const bf16_t* __restrict__ w_g, int d,
+                                       int t, int e) {
   const auto rx = make_rsrc(x + static_cast<int64_t>(t) * d, d * 2);
   const auto rw = make_rsrc(w_g + static_cast<int64_t>(e) * d, d * 2);
   // loads past the row read zeros
   float acc = 0.0f;
-  for (int k0 = lane * 16; k0 < d * 2; k0 += 4096) {
+  for (int k0 = lane_id() * 16; k0 < d * 2; k0 += 4096) {
     i32x4 xv[4], wv[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -97,16 +87,36 @@ __global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
         acc = fmaf(bf_hi(a), bf_hi(b), acc);
       }
   }
-  const float z = wave_sum(acc);
-  if (lane == 0)
+  return wave_sum(acc);
+}
+
+// Scores: a wave an expert and token.  64 experts of 2048: 3 us for one token,
+// 4.7 for 24, of which a kernel that does next to nothing takes 2 to 4.
+constexpr int kLogitThreads = 256;
+constexpr int kLogitWaves = kLogitThreads / kWave;
+
+__global__ __launch_bounds__(kLogitThreads) void few_logits_kernel(
+    const bf16_t* __restrict__ x, const bf16_t* __restrict__ w_g,
+    const float* __restrict__ bias, int d, int E, float* __restrict__ logits) {
+  const int e = __builtin_amdgcn_readfirstlane(
+      blockIdx.x * kLogitWaves + (threadIdx.x >> 6));
+  const int t = blockIdx.y;
+  if (e >= E) return;
+  const float z = score(x, w_g, d, t, e);
+  if (lane_id() == 0)
     logits[static_cast<int64_t>(t) * E + e] = bias ? z + bias[e] : z;
 }
 
 // The choice of one token from its scores, any number of experts.  4.6 us
-// for 24 tokens of 64 experts.
+// for 24 tokens of 64 experts.  logits null: the scores too, which saves a
+// launch and pays where a wave has one expert (whole layers: 16 tokens, 8
+// experts of 4096 x 256 35.7 -> 34.3 us, 24 tokens, 16 of 1024 x 256 25.2 ->
+// 24.2; 24 tokens, 64 of 1024 x 256 31.3 -> 33.0).
 __global__ __launch_bounds__(kRouteThreads) void few_topk_kernel(
-    const float* __restrict__ logits, int E, int k, int renorm,
-    int32_t* __restrict__ idx, float* __restrict__ wt) {
+    const float* __restrict__ logits, const bf16_t* __restrict__ x,
+    const bf16_t* __restrict__ w_g, const float* __restrict__ bias, int d,
+    int E, int k, int renorm, int32_t* __restrict__ idx,
+    float* __restrict__ wt) {
   __shared__ float s_z[kMaxExperts];
   __shared__ __attribute__((aligned(16))) uint32_t s_key[kMaxExperts];
   __shared__ int s_place[kMaxExperts];
@@ -119,8 +129,18 @@ __global__ __launch_bounds__(kRouteThreads) void few_topk_kernel(
   // multiple of four that nothing is worse than) are compared by `segs`
   // threads an expert, each with its share of them.
   const int E4 = (E + 3) & ~3;
+  if (!logits) {
+    for (int e = __builtin_amdgcn_readfirstlane(wave); e < E;
+         e += kRouteWaves) {
+      const float z = score(x, w_g, d, t, e);
+      if (lane == 0) s_z[e] = bias ? z + bias[e] : z;
+    }
+    __syncthreads();
+  }
   if (tid < E4) {
-    const float z = tid < E ? logits[static_cast<int64_t>(t) * E + tid] : 0.0f;
+    const float z = tid >= E ? 0.0f
+                    : logits ? logits[static_cast<int64_t>(t) * E + tid]
+                             : s_z[tid];
     s_z[tid] = z;
     s_key[tid] = tid < E ? score_key(z) : 0;
     s_place[tid] = 0;
@@ -1513,8 +1533,9 @@ hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
   P.parts = w.parts;
   P.renorm = a.renorm;
   P.inv_k = (65536 + a.k - 1) / a.k;
+  const bool here = a.T <= kChooseTokens && a.E <= kWave * kChooseLanes;
   const float* logits = a.logits;
-  if (!logits) {
+  if (!logits && (here || a.E > kRouteWaves)) {
     float* const z = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                               w.logits);
     hipLaunchKernelGGL(few_logits_kernel,
@@ -1525,11 +1546,12 @@ hipError_t launch_layer_fwd(bool mx, const LayerArgs& a, void* ws,
     if (e != hipSuccess) return e;
     logits = z;
   }
-  if (a.T <= kChooseTokens && a.E <= kWave * kChooseLanes) {
+  if (here) {
     P.logits = logits;
   } else {
     hipLaunchKernelGGL(few_topk_kernel, dim3(a.T), dim3(kRouteThreads), 0, s,
-                       logits, a.E, a.k, a.renorm, a.topk_idx, a.topk_w);
+                       logits, a.x, a.w_g, a.bias, a.d, a.E, a.k, a.renorm,
+                       a.topk_idx, a.topk_w);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
