@@ -346,6 +346,7 @@ struct Weights {
   static constexpr int kFrags = KC / 64;
   i32x4 w[kLoads];
   uint32_t s[MX ? kLoads : 1];         // MX: 4 scale bytes a load
+  int end;                            // MX: k from k0 to the row's end
 
   // row: byte offset of the lane's row (MX: of a byte a value)
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r,
@@ -359,6 +360,7 @@ struct Weights {
           r, k < K ? row + static_cast<uint32_t>(k) * (MX ? 1 : 2) : kOob);
     }
     if constexpr (MX) {
+      end = K - k0;
       const uint32_t at =
           k0 < K ? row / 32 + static_cast<uint32_t>(k0) / 32 : kOob;
       if constexpr (kLoads == 4) {
@@ -377,11 +379,16 @@ struct Weights {
     }
   }
   __device__ __forceinline__ bf16x8_v frag(int i, const Lane<MX>& L) const {
-    if constexpr (!MX)
+    if constexpr (!MX) {
       return __builtin_bit_cast(bf16x8_v, w[i]);
-    else
-      return widen(w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1],
-                   s[i >> 1], L.k >> 5);
+    } else {
+      // where the row ends inside the chunk the scales behind it are the next
+      // row's: one that is NaN would make NaN of the zeros that stand there
+      const uint32_t sc =
+          (i >> 1) == 0 || (i >> 1) * kLoadK < end ? s[i >> 1] : 0;
+      return widen(w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1], sc,
+                   L.k >> 5);
+    }
   }
 };
 
