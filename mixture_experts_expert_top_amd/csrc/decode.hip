@@ -623,9 +623,15 @@ struct UpWeights {
   }
 };
 
-// S = wt silu(a) u in two bf16 parts, the second what the first leaves.
+// S = wt silu(a) u, held in two bf16 parts, the second what the first leaves.
 __device__ __forceinline__ float swiglu(float a, float u, float wt) {
   return a * sigmoidf_(a) * u * wt;
+}
+// What the first part is rounded from: always finite in bf16, so that the
+// second is infinite or NaN where S is, and not by taking infinities apart.
+__device__ __forceinline__ float first_part(float h) {
+  constexpr float kMost = 0x1.fep127f;          // bf16's largest value
+  return __builtin_amdgcn_fmed3f(h, -kMost, kMost);
 }
 
 // Tiles [t0, t1) of an expert, 8 gate and 8 up rows each, for up to 8 members;
@@ -700,7 +706,7 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
       }
       if (slot >= 0) {
         const float h = swiglu(a, v, wt);
-        const bf16_t hi = f2bf(h);
+        const bf16_t hi = f2bf(first_part(h));
         bf16_t* const o =
             P.s + static_cast<int64_t>(slot) * 2 * P.f + tile * kRows + row;
         o[0] = hi;
@@ -1015,8 +1021,9 @@ struct UpSource {
       float h[4], l[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        h[v] = swiglu(ga[v], up[v], wt);
-        l[v] = h[v] - bf2f(f2bf(h[v]));
+        const float S = swiglu(ga[v], up[v], wt);
+        h[v] = first_part(S);
+        l[v] = S - bf2f(f2bf(h[v]));
       }
       bf16_t* const o =
           P.s + static_cast<int64_t>(slot) * 2 * P.f + n + qr * 4;
