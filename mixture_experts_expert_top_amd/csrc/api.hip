@@ -444,6 +444,16 @@ moe_status check_adamw_tensor(int i, const moe_adamw_tensor& t, bool fp8) {
   return MOE_OK;
 }
 
+// What moe_layer_fwd takes of a precision, tokens, choices and widths.
+bool layer_dims_ok(moe_prec prec, int64_t T, int32_t k, int64_t d, int64_t f) {
+  if (prec != MOE_BF16 && prec != MOE_MXFP8) return false;
+  if (T > moe::kFewTokens || k > moe::kMaxTopK) return false;
+  const int64_t q = prec == MOE_BF16 ? 8 : moe::kMxPad;
+  for (const int64_t v : {d, f})
+    if (v < q || v > moe::kFewWidth || v % q) return false;
+  return 4 * d * f <= kMaxRange && 4 * T * k * f <= kMaxRange;
+}
+
 // A tile's 256 rows of the widest operand (dAB, 2f wide) stay inside a
 // buffer resource up to this width.
 constexpr int64_t kMaxFfnWidth = int64_t{1} << 21;
@@ -552,8 +562,7 @@ size_t moe_workspace_bytes(moe_entry entry, moe_prec prec, int64_t T,
       if (prec == MOE_BF16) return bwd_layout(Tk, f).total;
       return mx_bwd_layout(Tk, E, d, f, mx_bwd_base(Tk, f)).total;
     case MOE_ENTRY_LAYER_FWD:
-      if (T > moe::kFewTokens || k > moe::kMaxTopK) return 0;
-      if (d < 1 || d > moe::kFewWidth || f < 1 || f > moe::kFewWidth) return 0;
+      if (!layer_dims_ok(prec, T, k, d, f)) return 0;
       return moe::layer_fwd_workspace(T, k, E, d, f);
     default:
       break;

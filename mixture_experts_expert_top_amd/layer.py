@@ -469,8 +469,12 @@ class MoEDecode:
                  device="cuda"):
         n = moe.moe_workspace_bytes(MOE_ENTRY_LAYER_FWD, prec, T, E, k, d, f)
         if n == 0:
-            raise ValueError("MoEDecode takes 1 to "
-                             f"{moe.MOE_LAYER_MAX_TOKENS} tokens and k <= E")
+            raise ValueError(
+                f"MoEDecode takes 1 to {moe.MOE_LAYER_MAX_TOKENS} tokens, "
+                "k <= 32 of up to 1024 experts, prec MOE_BF16 (d and f "
+                "multiples of 8) or MOE_MXFP8 (of 128) and an expert's weight "
+                f"below 4 GiB; got T={T}, d={d}, f={f}, E={E}, k={k}, "
+                f"prec={prec}")
         self.T, self.d, self.f, self.E, self.k = T, d, f, E, k
         self.renorm, self.prec = renorm, prec
         dev = torch.device(device)

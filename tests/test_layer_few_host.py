@@ -75,3 +75,56 @@ def test_workspace():
                dict(E=64, k=33), dict(d=0), dict(f=0), dict(prec=9),
                dict(d=(1 << 20) + 8), dict(f=1 << 40)):
         assert W(**kw) == 0, kw
+
+
+@pytest.mark.parametrize("kw", [
+    dict(prec=2), dict(d=12), dict(f=12), dict(d=4), dict(f=4),
+    dict(prec=1, d=160), dict(prec=1, f=160), dict(prec=1, d=64),
+    dict(d=1 << 16, f=1 << 15), dict(prec=1, d=1 << 15, f=1 << 16),
+    dict(T=64, E=64, k=32, d=8, f=1 << 19), dict(T=64, E=64, k=32, d=8,
+                                                 f=1 << 20)])
+def test_no_workspace_for_what_the_call_refuses(kw):
+    """moe_workspace_bytes gives 0 where moe_layer_fwd refuses the same
+    precision and sizes whatever workspace it is given."""
+    a = {**dict(prec=0, T=4, E=8, k=2, d=256, f=128), **kw}
+    n = moe.moe_workspace_bytes(moe.MOE_ENTRY_LAYER_FWD, a["prec"], a["T"],
+                                a["E"], a["k"], a["d"], a["f"])
+    assert n == 0
+    # tensors far apart, so that nothing but the sizes can be at fault
+    far = {n: (i + 1) << 44 for i, n in enumerate(
+        ("x", "w_g", "w_gu", "w2", "idx", "w", "y", "ws"))}
+    if a["prec"] != 0:
+        far.update(w_gu_s=20 << 44, w2_s=21 << 44)
+    st, msg = call(**{**far, **a}, nbytes=1 << 62)
+    assert st in (INVALID, UNSUP), msg
+    assert b"workspace" not in msg and b"overlap" not in msg
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(prec=1), dict(d=8, f=8, T=1, E=1, k=1),
+    dict(T=64, E=64, k=32, d=8, f=524280), dict(d=32768, f=32760),
+    dict(prec=1, d=32768, f=32640)])
+def test_workspace_up_to_the_limits(kw):
+    """Sizes next to the refused ones have a workspace, and pass the call's
+    checks as far as the workspace's own."""
+    a = {**dict(prec=0, T=4, E=8, k=2, d=256, f=128), **kw}
+    n = moe.moe_workspace_bytes(moe.MOE_ENTRY_LAYER_FWD, a["prec"], a["T"],
+                                a["E"], a["k"], a["d"], a["f"])
+    assert n > 0
+    far = {n: (i + 1) << 44 for i, n in enumerate(
+        ("x", "w_g", "w_gu", "w2", "idx", "w", "y", "ws"))}
+    if a["prec"] != 0:
+        far.update(w_gu_s=20 << 44, w2_s=21 << 44)
+    st, msg = call(**{**far, **a}, nbytes=n - 1)
+    assert st == WS, msg
+
+
+@pytest.mark.parametrize("kw", [
+    dict(prec=2), dict(d=12), dict(prec=1, f=160), dict(T=65), dict(T=0),
+    dict(k=9), dict(d=1 << 16, f=1 << 15)])
+def test_moe_decode_refuses_when_it_is_made(kw):
+    """Before any buffer is, with the sizes in the message."""
+    from mixture_experts_expert_top_amd.layer import MoEDecode
+    a = {**dict(T=4, d=256, f=128, E=8, k=2, prec=0), **kw}
+    with pytest.raises(ValueError, match=f"d={a['d']}.*prec={a['prec']}"):
+        MoEDecode(**a)
