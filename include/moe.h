@@ -797,11 +797,17 @@ typedef struct moe_adamw_tensor {
  *   moments are updated in fp32, every operation rounded by itself, from
  *   m = q_m s_m and r = q_v s_v, v = r^2; r' = sqrt(beta2 r^2 +
  *   (1 - beta2) g'^2) (0 where the sum is below 2^-96) is held in place of v
- *   and also used as it is for p.  A block's scale is its largest |m| or r over 256 (0, with codes 0, where
- *   that is below 1e-30); a value over its scale, y, is given u 2^-20ths of
- *   its fourth significant bit (u = (t * 0x9E3779B1 mod 2^32) >> 12, in the
- *   bits of the fp32 value), cut to four significant bits, and rounded to
- *   the nearest E4M3 value; an r above 0 keeps at least the smallest code.
+ *   and also used as it is for p.  A block's scale is its largest |m| or r
+ *   over 256 (0, with codes 0, where that is below 1e-30).  A value over its
+ *   scale, y (of an r above 0 at least 2^-9, the smallest code), is given u
+ *   2^-20ths of its fourth significant bit (u = (t * 0x9E3779B1 mod 2^32) >> 12,
+ *   in the bits of the fp32 value), cut to four significant bits, and rounded to
+ *   the nearest E4M3 value.  Where |y| is below 2^-6 and that is the code that
+ *   the value had before the step, it is given u 2^-20ths of 2^-9, the distance
+ *   between codes there, and cut to a multiple of that: the first cut of |y| +
+ *   2^-6 (rounded to fp32), less 2^-6, with y's sign.  u is one for all values
+ *   of a step: what a value is held as averages out over the steps, not over
+ *   the values of a tensor.
  *   Codes and scales are exact (bit-identical to this definition).
  * Moments of a tensor that was never stepped are all zero bytes, scales
  * included.  Gradients are finite, g'^2 too, unless grad_norm leaves the step

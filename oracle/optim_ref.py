@@ -33,8 +33,14 @@ def parameter(p, m, r, t, lr, b1, b2, eps, wd):
 
 
 # -------------------------------------------------------------- 8 bits
+class Moment(np.ndarray):
+    """float32 values of a moment after a step, and (``codes``) the E4M3 codes
+    that they had before it."""
+    codes = None
+
+
 def dither(t):
-    """Units of 2^-20 of the fourth significant bit added at step t."""
+    """Units of 2^-20 of the distance between codes added at step t."""
     return ((t * 0x9E3779B1) & 0xFFFFFFFF) >> 12
 
 
@@ -48,11 +54,22 @@ def moments8(qm, sm, qr, sr, g, b1, b2):
     m = m * b1f + g * c1f
     v = r * r * b2f + g * g * c2f
     r = np.where(v >= F(2.0 ** -96), np.sqrt(v), F(0.0))
+    m, r = m.view(Moment), r.view(Moment)
+    m.codes, r.codes = np.array(qm), np.array(qr)
     return m, r
 
 
+def _cut(y, t):
+    """y after the dither of step t, cut to four significant bits."""
+    bits = np.ascontiguousarray(y, F).view(np.uint32).astype(np.int64)
+    return ((bits + dither(t)) & 0xFFF00000).astype(np.uint32).view(F)
+
+
 def quantize8(x, t, second):
-    """(codes, scales) of float32 x at step t; second: of r."""
+    """(codes, scales) of float32 x at step t; second: of r.  Values that
+    moments8 gave know the codes that they had; others had none."""
+    had = getattr(x, "codes", None)
+    x = np.asarray(x)
     n = x.size
     blocks = -(-n // BLOCK)
     pad = np.zeros(blocks * BLOCK, F)
@@ -65,8 +82,15 @@ def quantize8(x, t, second):
     y = b * inv[:, None]
     if second:
         y = np.where(b > 0, np.maximum(y, F(2.0 ** -9)), F(0.0)).astype(F)
-    bits = np.ascontiguousarray(y).view(np.uint32).astype(np.int64)
-    cut = ((bits + dither(t)) & 0xFFF00000).astype(np.uint32).view(F)
-    codes = mx_ref.e4m3_encode(cut.astype(np.float64))
+    y = y.reshape(-1)[:n]
+    codes = mx_ref.e4m3_encode(_cut(y, t).astype(np.float64))
+    if had is not None:
+        # below 2^-6 a value that would keep its code is cut to the code's
+        # unit, 2^-9, which is that of four bits from 2^-6 to 2^-5
+        held = (np.abs(y) < F(2.0 ** -6)) & (codes == had)
+        low = np.copysign(F(2.0 ** -6), y)
+        small = _cut(y + low, t) - low
+        codes = np.where(held, mx_ref.e4m3_encode(small.astype(np.float64)),
+                         codes)
     scales = np.where(live, top * F(2.0 ** -8), F(0.0)).astype(F)
-    return codes.reshape(-1)[:n], scales
+    return codes, scales

@@ -184,3 +184,58 @@ def test_adamw_oracle_by_hand():
     assert R.grad_norm([np.array([3.0]), np.array([0.0, 4.0])]) == 5.0
     assert R.clip_factor(5.0, 1.0) == 1.0 / (5.0 + 1e-6)
     assert R.clip_factor(0.5, 1.0) == 1.0
+
+
+def small_codes(sign):
+    """A block whose first value holds the scale and whose others are the
+    codes up to 2^-6 in turn; as E4M3 codes and scale."""
+    codes = np.zeros(256, np.uint8)
+    codes[0] = mx_ref.e4m3_encode(np.array(256.0))[()]
+    codes[1:] = 1 + np.arange(255) % 8
+    if sign:
+        codes[2::2] |= 0x80
+    return codes, np.full(1, 1.0 / 256, np.float32)
+
+
+def test_small_codes_of_a_moment_without_gradients_fall():
+    """Codes up to 2^-6 move too when they are read, updated and stored again
+    beside a value that keeps the scale.  Code n falls at the latest where the
+    step's fraction is below n (1 - sqrt(beta2)) (of m: n (1 - beta1)); N
+    multiples of the golden ratio leave no gap of 2 / N or more, so from 8 down
+    to 1 it takes at most 2 / 0.0005 (1/8 + ... + 1/2), 6870 steps, by when the
+    true value is below a quarter of the smallest code, and m is 0 after 2 /
+    0.1 (1/8 + ... + 1), 55 steps."""
+    (qm, sm), (qr, sr) = small_codes(True), small_codes(False)
+    g = np.zeros(256, np.float32)
+    g[0] = 1.0
+    for t in range(1, 6871):
+        m, r = R.moments8(qm, sm, qr, sr, g, 0.9, 0.999)
+        (qm, sm), (qr, sr) = R.quantize8(m, t, False), R.quantize8(r, t, True)
+        if t == 55:
+            assert not (qm[1:] & 0x7F).any()
+    assert (qr[1:] == 1).all()
+    assert abs(sr[0] * 256 - 1.0) < 0.1     # the scale was kept
+
+
+@pytest.mark.parametrize("second", [False, True])
+def test_small_codes_follow_a_small_gradient(second):
+    """Values whose moment belongs between two codes below 2^-6 come to it and
+    alternate between the two: over the last half of 8000 steps at beta 0.99
+    the mean is off by less than a code each, and by less than a quarter, what
+    the nearest code would be off by, on average; m starts at 0."""
+    want = np.full(256, 256.0)
+    want[1:] = np.linspace(1.3, 7.4, 255) / 512     # in units of the scale
+    if not second:
+        want[2::2] *= -1
+        want[3:60] *= 0.2
+    g = (want / 256).astype(np.float32)
+    q = [np.zeros(256, np.uint8), np.zeros(1, np.float32)]
+    mean, steps = np.zeros(256), 8000
+    for t in range(1, steps + 1):
+        m, r = R.moments8(*q, *q, g, 0.99, 0.99)
+        q = R.quantize8(r if second else m, t, second)
+        if t > steps // 2:
+            mean += mx_ref.e4m3_decode(q[0]) * 2 / steps
+    off = np.abs(mean - want)[1:] * 512
+    assert off.max() < 1.0
+    assert off.mean() < 0.25

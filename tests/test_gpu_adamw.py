@@ -456,3 +456,43 @@ def test_binding_refuses():
         moe.moe_adamw(moe.adamw_table([one, one]), t, lr, 0.9, 0.95, 1e-8)
     with pytest.raises(moe.MoeError):
         moe.moe_grad_norm(grads, z(1), z(2))
+
+
+@gpu
+def test_small_codes_fall_step_by_step():
+    """Codes below 2^-6 beside a live value, read, updated and stored again for
+    as many steps as the largest of them needs to become the smallest
+    (test_adamw_host.py), bit for bit with the oracle's."""
+    dev = torch.device("cuda:0")
+    n = 600
+    codes = {"m": np.zeros(n, np.uint8), "v": np.zeros(n, np.uint8)}
+    codes["m"][:] = 1 + np.arange(n) % 8
+    codes["m"][::2] |= 0x80
+    codes["v"][:] = 1 + np.arange(n) * 7 % 8
+    g = np.zeros(n, np.float32)
+    for i in (0, 300, 599):
+        codes["m"][i] = codes["v"][i] = 0x78        # 256
+        g[i] = 1.0
+    scales = {k: np.full(3, 1.0 / 256, np.float32) for k in "mv"}
+    t = dict(p=torch.zeros(n, dtype=BF, device=dev),
+             g=torch.from_numpy(g).to(dev), weight_decay=0.0)
+    for k in "mv":
+        t[k] = torch.from_numpy(codes[k]).to(dev).view(F8)
+        t[k + "_scale"] = torch.from_numpy(scales[k]).to(dev)
+    table = moe.adamw_table([t])
+    step, lr = _scalars(0)
+    for i in range(1, 6871):
+        step += 1
+        moe.moe_adamw(table, step, lr, 0.9, 0.999, 1e-8)
+        m, r = R.moments8(codes["m"], scales["m"], codes["v"], scales["v"], g,
+                          0.9, 0.999)
+        for k, x, second in (("m", m, False), ("v", r, True)):
+            codes[k], scales[k] = R.quantize8(x, i, second)
+        if i in (1, 10, 55, 1000, 6870):
+            for k in "mv":
+                assert np.array_equal(_bits(t[k]), codes[k]), (i, k)
+                assert np.array_equal(t[k + "_scale"].cpu().numpy(),
+                                      scales[k]), (i, k)
+    rest = np.ones(n, bool)
+    rest[[0, 300, 599]] = False
+    assert (codes["v"][rest] == 1).all() and not codes["m"][rest].any()
