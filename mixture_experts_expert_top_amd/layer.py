@@ -542,7 +542,7 @@ class AdamW:
             row = {"p": w, "g": g, "weight_decay": wd[0] if wd else
                    weight_decay}
             if master and w.dtype == torch.bfloat16:
-                row["master"] = w.float()
+                row["master"] = w.detach().float()
             if moments == MOE_MOMENTS_FP32:
                 for n in ("m", "v"):
                     row[n] = torch.zeros_like(w, dtype=torch.float32)
