@@ -690,6 +690,10 @@ class MoEBlock:
                   sw_gu=None, sw2=None):
         """(weight, gradient[, weight decay]) of the block's and the path's
         weights, as ``AdamW`` takes them; the norm's have no weight decay."""
+        if self.f_shared and (sw_gu is None or sw2 is None):
+            raise ValueError("f_shared > 0 needs sw_gu and sw2")
+        if beta is not None and self.norm != MOE_NORM_LAYER:
+            raise ValueError("beta goes with layer norm")
         if not self._bwd_ready:
             self._alloc_bwd()
         out = [(gamma, self.dgamma, 0.0)]
