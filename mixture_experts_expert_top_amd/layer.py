@@ -492,8 +492,9 @@ class MoEDecode:
         z = lambda n: torch.empty(E, rows, n, dtype=torch.uint8,  # noqa: E731
                                   device=w.device)
         codes, scales = z(cols), z(cols // 32)
-        for e in range(E):
-            moe.moe_mxfp8_quantize(w[e], 0, None, codes[e], scales[e])
+        with torch.cuda.device(w.device):
+            for e in range(E):
+                moe.moe_mxfp8_quantize(w[e], 0, None, codes[e], scales[e])
         return codes, scales
 
     def forward(self, x, w_gu, w2, w_g=None, bias=None, logits=None,

@@ -128,3 +128,30 @@ def test_moe_decode_refuses_when_it_is_made(kw):
     a = {**dict(T=4, d=256, f=128, E=8, k=2, prec=0), **kw}
     with pytest.raises(ValueError, match=f"d={a['d']}.*prec={a['prec']}"):
         MoEDecode(**a)
+
+
+def test_quantize_runs_on_its_weights_device(monkeypatch):
+    """The quantizer launches on the current device's stream, so that device
+    is made the weight's; a weight in host memory is refused."""
+    import contextlib
+
+    import torch
+
+    from mixture_experts_expert_top_amd.layer import MoEDecode
+    made, current = [], []
+
+    @contextlib.contextmanager
+    def device(d):
+        current.append(d)
+        yield
+        current.pop()
+    monkeypatch.setattr(moe, "moe_mxfp8_quantize",
+                        lambda *a, **k: made.append(list(current)))
+    w = torch.zeros(3, 32, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        MoEDecode.quantize(w)
+    assert not made
+    monkeypatch.setattr(torch.cuda, "device", device)
+    codes, scales = MoEDecode.quantize(w)
+    assert made == [[w.device]] * 3
+    assert codes.shape == w.shape and scales.shape == (3, 32, 4)
