@@ -5,8 +5,13 @@ import pytest
 import torch
 
 import test_gpu_layer_few as L
+from mixture_experts_expert_top_amd import inputs as I
 
 gpu = pytest.mark.gpu
+BF, U8 = torch.bfloat16, torch.uint8
+
+if torch.cuda.is_available():
+    from mixture_experts_expert_top_amd import moe
 
 
 def to_one_expert_each(c, hot=3):
@@ -87,3 +92,73 @@ def test_values_of_s_past_the_end_of_bf16(T, first, mx):
             want = sign * float(S) * 2.0 ** -100
             tol = (2.0 ** -8 + 2.0 ** -15) * want.abs()
             assert ((y[t] - want).abs() <= tol).all(), i
+
+
+@gpu
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("mx,T,d,f,E,k", [
+    (False, 1, 1024, 1024, 64, 8),      # 2 parts, 128 tiles
+    (False, 1, 520, 1096, 40, 8),       # 2 parts, odd widths
+    (False, 2, 264, 2056, 16, 8),       # 4 parts, 33 tiles
+    (False, 4, 256, 1000, 64, 8),       # 8 parts
+    (False, 3, 16, 264, 300, 32),       # 8 parts of 2 tiles
+    (True, 1, 1024, 1024, 64, 8), (True, 4, 256, 1152, 33, 8),
+    (True, 2, 128, 640, 24, 12)])
+def test_direct_second_product_in_parts(mx, T, d, f, E, k, same):
+    """Up to 4 tokens, narrow y and many items of the reduction: the direct
+    form leaves parts for the sum.  same: all tokens choose the same experts,
+    fewer than the parts were counted for."""
+    c = L.Case(T, d, f, E, k, mx=mx, bias=not same, add=T > 1, seed=T + d)
+    if same:
+        c.logits = I.make_tensor((1, E), seed=5, dtype=torch.float32,
+                                 device="cuda:0").repeat(T, 1)
+    S = (T * k * f * 4 + 255) // 256 * 256
+    z = (T * E * 4 + 255) // 256 * 256
+    parts = (c.ws.numel() - S - z) // (T * d * 4)
+    assert parts >= 2                   # what the test is for
+    c.run()
+    L.check(c)
+    if c.y_add is not None:             # the sum may go into y itself
+        want = c.y.clone()
+        y = c.y_add.clone()
+        c.run(y=y, y_add=y)
+        assert torch.equal(y, want)
+
+
+@gpu
+@pytest.mark.parametrize("T,mx", [(1, False), (2, False), (12, False),
+                                  (1, True), (2, True), (12, True)])
+def test_second_product_past_32_bit_offsets(T, mx):
+    """w2 past 4 GiB (w_gu past 8), the first and the last expert; one or two
+    of them are few enough values for the direct second product, 12 tokens
+    take the batch form."""
+    dev = torch.device("cuda:0")
+    d = f = 4096
+    E = 330 if mx else 160
+    c = L.Case(1, 128, 128, 1, 1, mx=mx)
+    c.T, c.d, c.f, c.E, c.k = T, d, f, E, 1
+    c.x = I.make_tensor((T, d), seed=1, device=dev)
+    c.y_add = None
+    for i, (rows, cols) in enumerate(((2 * f, d), (d, f))):
+        w = torch.zeros(E, rows, cols, dtype=U8 if mx else BF, device=dev)
+        assert w.numel() * w.element_size() > 1 << 32
+        s = torch.zeros(E, rows, cols // 32, dtype=U8, device=dev)
+        for e in (0, E - 2, E - 1):
+            v = I.make_tensor((rows, cols), seed=e + 7 * i, scale=0.02,
+                              device=dev)
+            if mx:
+                moe.moe_mxfp8_quantize(v, 0, None, w[e], s[e])
+            else:
+                w[e] = v
+        c.w[i], c.s[i] = w, s if mx else None
+    c.logits = torch.full((T, E), -5.0, device=dev)
+    hot = torch.tensor([E - 1, 0, E - 2], device=dev)
+    t = torch.arange(T, device=dev)
+    c.logits[t, hot[t % 3]] = 1.0
+    c.ws = torch.empty(moe.moe_workspace_bytes(
+        moe.MOE_ENTRY_LAYER_FWD, c.prec, T, E, 1, d, f), dtype=U8, device=dev)
+    c.y = torch.empty(T, d, dtype=BF, device=dev)
+    c.idx = torch.empty(T, 1, dtype=torch.int32, device=dev)
+    c.p = torch.empty(T, 1, device=dev)
+    c.run()
+    L.check(c)
