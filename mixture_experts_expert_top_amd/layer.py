@@ -529,8 +529,12 @@ class AdamW:
     gradients to that norm over all of them, and leave a step out whose norm
     is not finite.  lr, the number of steps made and the norm live on the
     device, so that ``step`` can be captured; ``lr.fill_`` changes the rate of
-    captured steps too.
+    captured steps too.  ``state_dict`` and ``load_state_dict`` store and load
+    what a run that goes on needs beside the weights: the number of steps, the
+    rate, the moments with their scales and the fp32 copies.
     """
+
+    _KEPT = ("master", "m", "v", "m_scale", "v_scale")
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps=1e-8,
                  weight_decay=0.1, moments=MOE_MOMENTS_FP32, master=True,
@@ -579,6 +583,36 @@ class AdamW:
             with _around(timers, "adamw"):
                 moe.moe_adamw(self.table, self.steps, self.lr, *self.betas,
                               self.eps, norm, self.max_norm or 1.0)
+
+
+    def state_dict(self):
+        """The optimizer's own tensors (not copies of them), those of a weight
+        in a dict each, in the order of the weights."""
+        return {"steps": self.steps, "lr": self.lr,
+                "weights": [{n: r[n] for n in self._KEPT if n in r}
+                            for r in self.rows]}
+
+    def load_state_dict(self, state):
+        """Copies a state_dict of the same weights, moments and copies into
+        this optimizer's tensors, which stay where they are (so captured steps
+        go on with them); anything else is refused before the first copy."""
+        mine = self.state_dict()
+        if len(state["weights"]) != len(mine["weights"]):
+            raise ValueError(f"state of {len(state['weights'])} weights, not "
+                             f"of {len(mine['weights'])}")
+        pairs = [("steps", self.steps, state["steps"]),
+                 ("lr", self.lr, state["lr"])]
+        for i, (a, b) in enumerate(zip(mine["weights"], state["weights"])):
+            if a.keys() != b.keys():
+                raise ValueError(f"weight {i}: state of {sorted(b)}, not of "
+                                 f"{sorted(a)}")
+            pairs += [(f"weight {i}: {n}", a[n], b[n]) for n in a]
+        for name, a, b in pairs:
+            if a.shape != b.shape or a.dtype != b.dtype:
+                raise ValueError(f"{name}: {b.dtype} {tuple(b.shape)}, not "
+                                 f"{a.dtype} {tuple(a.shape)}")
+        for _, a, b in pairs:
+            a.copy_(b)
 
 
 def _extent(t):

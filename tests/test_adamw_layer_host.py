@@ -1,6 +1,8 @@
 """layer.AdamW and the gradients methods where no kernel has to run: tables
 are replaced by the rows that they would be made of."""
 
+import io
+
 import pytest
 import torch
 
@@ -47,3 +49,56 @@ def test_a_blocks_gradients_go_with_its_weights(norm, f_shared, but, word):
     w = {n: t for n, t in w.items() if n not in ("beta", "sw_gu", "sw2")}
     if not f_shared:
         assert len(block.gradients(**w)) == 3
+
+
+def _optimizer(moments, master=True, shapes=((6, 8), (300,)), **kw):
+    ws = [torch.randn(*s).to(BF) for s in shapes] + [torch.randn(5)]
+    return layer.AdamW([(w, torch.zeros_like(w)) for w in ws],
+                       moments=moments, master=master, **kw)
+
+
+@pytest.mark.parametrize("moments", [moe.MOE_MOMENTS_FP32,
+                                     moe.MOE_MOMENTS_FP8])
+@pytest.mark.parametrize("master", [True, False])
+def test_state_through_a_file(tables, moments, master):
+    a, b = (_optimizer(moments, master, lr=lr) for lr in (1e-3, 5e-2))
+    a.steps.fill_(12)
+    for r in a.rows:
+        for n in ("m", "v"):
+            r[n].view(torch.uint8).random_(0, 100)
+            if moments == moe.MOE_MOMENTS_FP8:
+                r[n + "_scale"].uniform_()
+    f = io.BytesIO()
+    torch.save(a.state_dict(), f)
+    f.seek(0)
+    at = [t.data_ptr() for r in b.rows for t in r.values()
+          if torch.is_tensor(t)]
+    b.load_state_dict(torch.load(f, weights_only=True))
+    assert at == [t.data_ptr() for r in b.rows for t in r.values()
+                  if torch.is_tensor(t)]
+    assert int(b.steps) == 12 and torch.equal(b.lr, a.lr)
+    kept = ("m", "v") + ("m_scale", "v_scale") * moments
+    for x, y in zip(a.rows, b.rows):
+        assert ("master" in y) == (master and y["p"].dtype == BF)
+        for n in kept + ("master",) * ("master" in y):
+            assert torch.equal(x[n].view(torch.uint8), y[n].view(torch.uint8))
+        assert not torch.equal(x["p"], y["p"])      # weights are their owner's
+
+
+def test_state_of_something_else_is_refused(tables):
+    """Before anything is copied."""
+    a = _optimizer(moe.MOE_MOMENTS_FP8)
+    before = [r["m"].clone() for r in a.rows]
+    for b in (_optimizer(moe.MOE_MOMENTS_FP32),
+              _optimizer(moe.MOE_MOMENTS_FP8, master=False),
+              _optimizer(moe.MOE_MOMENTS_FP8, shapes=((6, 8),)),
+              _optimizer(moe.MOE_MOMENTS_FP8, shapes=((6, 8), (301,))),
+              _optimizer(moe.MOE_MOMENTS_FP8, shapes=((8, 6), (300,)))):
+        for r in b.rows:
+            r["m"].view(torch.uint8).fill_(1)
+        b.steps.fill_(5)
+        with pytest.raises(ValueError):
+            a.load_state_dict(b.state_dict())
+        assert int(a.steps) == 0
+        assert all(torch.equal(r["m"].view(torch.uint8), m.view(torch.uint8))
+                   for r, m in zip(a.rows, before))

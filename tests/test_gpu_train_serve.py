@@ -240,3 +240,34 @@ def test_adamw_refuses_a_norm_to_clip_to(bad):
     w = torch.zeros(8, dtype=BF, device="cuda:0")
     with pytest.raises(ValueError, match="max_norm"):
         AdamW([(w, torch.zeros_like(w))], max_norm=bad)
+
+
+@gpu
+@pytest.mark.parametrize("moments", [0, 1], ids=["fp32", "fp8"])
+def test_training_goes_on_from_a_stored_state(moments):
+    """Three steps, store, two more: another program that loads the weights
+    and the state makes the same two, bit for bit, also by a step captured
+    before it loaded them."""
+    a, b = Training(_path(False), moments), Training(_path(False), moments)
+    g = StepGraph(b.step)
+    for _ in range(3):
+        a.step()
+    state = {k: v.clone() if torch.is_tensor(v) else
+             [{n: t.clone() for n, t in w.items()} for w in v]
+             for k, v in a.opt.state_dict().items()}
+    for n, w in b.w.items():
+        w.copy_(a.w[n])
+    b.opt.load_state_dict(state)
+    for i in range(2):
+        a.step()
+        if i:
+            g.replay()
+        else:
+            b.step()
+        torch.cuda.synchronize()
+        assert int(a.opt.steps) == int(b.opt.steps) == 4 + i
+        for x, y in zip(a.opt.rows, b.opt.rows):
+            for n in x:
+                if torch.is_tensor(x[n]):
+                    assert torch.equal(x[n].view(torch.uint8),
+                                       y[n].view(torch.uint8)), (i, n)
