@@ -48,7 +48,8 @@ from .moe import (MOE_ACT_SILU, MOE_BF16, MOE_ENTRY_FFN_BWD,
                   MOE_ENTRY_FFN_FWD, MOE_ENTRY_GRAD_NORM, MOE_ENTRY_LAYER_FWD,
                   MOE_ENTRY_MLP_BWD, MOE_ENTRY_MLP_FWD, MOE_ENTRY_NORM_BWD,
                   MOE_ENTRY_PERMUTE, MOE_ENTRY_ROUTER_BWD, MOE_MOMENTS_FP32,
-                  MOE_MXFP4, MOE_MXFP8, MOE_NORM_LAYER, MOE_NORM_RMS)
+                  MOE_MOMENTS_FP8, MOE_MXFP4, MOE_MXFP8, MOE_NORM_LAYER,
+                  MOE_NORM_RMS)
 
 
 class StageTimers:
@@ -541,6 +542,13 @@ class AdamW:
                  max_norm=None):
         if max_norm is not None and not 0 < max_norm <= 3.4e38:
             raise ValueError("AdamW: max_norm must be finite and above 0")
+        if moments not in (MOE_MOMENTS_FP32, MOE_MOMENTS_FP8):
+            raise ValueError(f"AdamW: unknown form of the moments {moments}")
+        if not all(0 <= b < 1 for b in betas):
+            raise ValueError("AdamW: betas must be in [0, 1)")
+        least = 1e-12 if moments == MOE_MOMENTS_FP8 else 1e-20
+        if not least <= eps <= 1:
+            raise ValueError(f"AdamW: eps must be in [{least}, 1]")
         self.betas, self.eps, self.max_norm = betas, eps, max_norm
         rows = []
         for w, g, *wd in params:

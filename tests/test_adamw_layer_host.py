@@ -102,3 +102,24 @@ def test_state_of_something_else_is_refused(tables):
         assert int(a.steps) == 0
         assert all(torch.equal(r["m"].view(torch.uint8), m.view(torch.uint8))
                    for r, m in zip(a.rows, before))
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(moments=2), "moments"), (dict(moments=None), "moments"),
+    (dict(betas=(1.0, 0.95)), "betas"), (dict(betas=(0.9, -0.1)), "betas"),
+    (dict(betas=(0.9, float("nan"))), "betas"), (dict(eps=0.0), "eps"),
+    (dict(eps=2.0), "eps"), (dict(eps=1e-13, moments=1), "eps"),
+    (dict(eps=float("nan")), "eps")])
+def test_adamw_refuses_when_it_is_made(tables, kw, word):
+    """What every step of it would be refused for, after the step had been
+    counted."""
+    w = torch.zeros(8, dtype=BF)
+    with pytest.raises(ValueError, match=word):
+        layer.AdamW([(w, torch.zeros_like(w))], **kw)
+
+
+def test_adamw_takes_the_ends_of_its_ranges(tables):
+    w = torch.zeros(8, dtype=BF)
+    for kw in (dict(betas=(0.0, 0.0), eps=1.0), dict(eps=1e-20),
+               dict(eps=1e-12, moments=1)):
+        layer.AdamW([(w, torch.zeros_like(w))], **kw)
