@@ -51,11 +51,11 @@ constexpr int kThreads = 256;
 constexpr int kVec = 8;
 constexpr int kChunk = kThreads * kVec;         // values a workgroup and pass
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
-// Passes a workgroup of the 8-bit form, which the vector units bound (75
-// instructions a value with one pass, 53 with eight: what all values share,
+// Passes a workgroup of the 8-bit form, which the vector units bound (74
+// instructions a value with one pass, 60 with eight: what all values share,
 // the corrections' exponentials among it, is computed once a workgroup): as
 // many as leave the CUs 16 rounds of workgroups, up to eight.  554 M values
-// 1332 -> 1210 us with the norm; 45 M, where eight passes would leave 11
+// 1420 -> 1208 us with the norm; 45 M, where eight passes would leave 11
 // workgroups a CU, 143 us with one and 163 with eight.  The fp32 form is bound
 // by memory and stays at one (2820 us for 2986).
 constexpr int kMostPasses = 8;
@@ -391,7 +391,8 @@ __device__ __forceinline__ i32x2 new_codes(const float* y, i32x2 old,
 // The correctly rounded root of x >= 2^-96, by the last step of Newton's
 // method on a root and half its reciprocal (each good to about an ulp) with
 // the residual x - s^2 exact: five instructions where the library's root for
-// every float takes 14.  Equal to it on every float of [2^-96, 2^100).
+// every float takes 14 (60 instructions a value for 71; 554 M values with the
+// norm 1208 us for 1249).
 __device__ __forceinline__ float root(float x) {
   const float y = __builtin_amdgcn_rsqf(x);
   const float s = x * y;

@@ -496,3 +496,29 @@ def test_small_codes_fall_step_by_step():
     rest = np.ones(n, bool)
     rest[[0, 300, 599]] = False
     assert (codes["v"][rest] == 1).all() and not codes["m"][rest].any()
+
+
+@gpu
+@pytest.mark.parametrize("b2", [0.0, 0.5, 0.95, 0.999])
+def test_roots_of_second_moments_are_rounded_correctly(b2):
+    """A block's scale is its largest r over 256, exactly, so blocks of one
+    gradient each show the root of (1 - beta2) g^2, every operation rounded by
+    itself, over the range of exponents that it is taken of."""
+    dev = torch.device("cuda:0")
+    blocks = 1 << 16
+    n = blocks * 256
+    rng = np.random.default_rng(int(b2 * 1000))
+    g = rng.uniform(1, 2, blocks) * 2.0 ** rng.integers(-40, 63, blocks)
+    g = g.astype(np.float32)
+    full = torch.zeros(n, device=dev)
+    full[::256] = torch.from_numpy(g).to(dev)
+    t = dict(p=torch.zeros(n, dtype=BF, device=dev), g=full, weight_decay=0.0)
+    for k in "mv":
+        t[k] = torch.zeros(n, dtype=torch.uint8, device=dev).view(F8)
+        t[k + "_scale"] = torch.zeros(blocks, device=dev)
+    step, lr = _scalars(1)
+    moe.moe_adamw(moe.adamw_table([t]), step, lr, 0.9, b2, 1e-8)
+    c2 = np.float32(1.0 - b2)
+    want = np.sqrt(g * g * c2) * np.float32(2.0 ** -8)
+    assert want.dtype == np.float32 and (g * g * c2 >= 2.0 ** -96).all()
+    assert np.array_equal(t["v_scale"].cpu().numpy(), want)
