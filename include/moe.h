@@ -694,7 +694,7 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
  * end of a prompt) without a dispatch plan: the router of moe_router_logits
  * and moe_route, the experts of moe_grouped_mlp_fwd and the combine of
  * moe_unpermute in one call that reads the weights of the experts it
- * reaches once.
+ * reaches once (w2 of an expert that more than 32 tokens choose twice).
  *   z[t] = x[t] . w_g^T (+ bias)            (or logits[t])
  *   topk_idx[t], topk_w[t]: as moe_route chooses from z[t]
  *   S[t][j] = topk_w[t][j] * silu(x[t] . G^T) * (x[t] . U^T), e =
@@ -712,12 +712,12 @@ moe_status moe_ffn_bwd(moe_act act, const void* dy, const void* x,
  *   stands for 0 or 2^-127.
  * prec == MOE_MXFP4: MOE_ERR_UNSUPPORTED.
  * Sums are fp32 in a fixed order, S is held as the sum of two bf16 values (16
- * significant bits), y is rounded once.  A token's bits may differ between calls of
- * different tokens around it.  y may be y_add itself; otherwise outputs and
- * the workspace overlap neither inputs nor each other.  1 <= T <=
+ * significant bits), y is rounded once.  A token's bits may differ between
+ * calls of different tokens around it.  y may be y_add itself; otherwise
+ * outputs and the workspace overlap neither inputs nor each other.  1 <= T <=
  * MOE_LAYER_MAX_TOKENS, E, k and the size of an expert's weight as
- * moe_grouped_mlp_fwd, d and f up to 2^20, 4 T k f up to 4 GiB - 256.  Workspace:
- * MOE_ENTRY_LAYER_FWD.
+ * moe_grouped_mlp_fwd, d and f up to 2^20, 4 T k f up to 4 GiB - 256.
+ * Workspace: MOE_ENTRY_LAYER_FWD.
  */
 moe_status moe_layer_fwd(moe_prec prec, const void* x, const void* w_g,
                          const float* bias, const float* logits, int64_t T,

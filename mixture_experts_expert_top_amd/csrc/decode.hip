@@ -5,8 +5,9 @@
 //   z = x W_g^T + b, (i_j, p_j) = top-k softmax of z
 //   S_j = p_j silu(x G_{i_j}^T) (x U_{i_j}^T),  y = y_add + sum_j S_j W2_{i_j}^T
 //
-// Bound by reading the weights of the experts that are reached, once: nothing
-// is permuted, weights go from global memory straight into MFMA fragments.
+// Bound by reading the weights of the experts that are reached, once (w2 twice
+// for an expert of more than 32 tokens): nothing is permuted, weights go from
+// global memory straight into MFMA fragments.
 // A kernel that only reads gets 6.1 TB/s here; times below are of kernels
 // alone, traced, weights not in any cache.
 //
@@ -456,7 +457,8 @@ struct Units {
 //     4 tokens, MXFP8, 64 x 2048 x 1408   25    20 + 4.7
 // So: the first product direct for bf16 weights up to the 8 columns that a
 // tile has, the second up to the 4 whose two parts fit and as long as few_sum
-// weighs more, by the values that it may have to read.
+// weighs more, by the values that it may have to read (one limit for both
+// types; between 46 and 92 million values neither was measured).
 constexpr int kDirectUp = 8;
 constexpr int kDirectDown = 4;
 constexpr int64_t kDirectValues = 80000000;
@@ -732,7 +734,7 @@ __device__ __forceinline__ void up_tiles(const FewParams& P, const Units& U,
 
 // All tiles of all reached experts in order, divided evenly over the
 // workgroups (what the CUs hold at once, so that starting and finding the
-// experts is paid once).  One token: 8 experts of 2048 x 1408, 92 MB, 20.8 us;
+// experts is paid once).  One token: 8 experts of 2048 x 1408, 92 MB, 20.6 us;
 // 2 of 4096 x 14336, 470 MB, 73 us (6.4 TB/s).
 template <bool NT>
 __global__ __launch_bounds__(kUpThreads, 4) void few_up_kernel(FewParams P) {
@@ -1056,8 +1058,8 @@ __device__ __forceinline__ void up_batch(const FewParams& P, const Units& U,
 }
 
 // MAXB: blocks of 8 that T tokens can fill.  24 tokens, 64 experts of 2048 x
-// 1408 in MXFP8, 368 MB: 62 us (5.9 TB/s); 64 tokens, 8 of 4096 x 14336 in
-// bf16, 1.88 GB: 306 us (6.1 TB/s).  What is left: 2 us until the experts are
+// 1408 in MXFP8, 358 MB: 63 us (5.7 TB/s); 64 tokens, 8 of 4096 x 14336 in
+// bf16, 1.88 GB: 305 us (6.2 TB/s).  What is left: 2 us until the experts are
 // found, 5 to 15 until the first weights come, and workgroups that have 6
 // groups of rows where others have 5.
 template <bool MX, bool NT, int MAXB>
@@ -1162,6 +1164,9 @@ struct DownSource {
 template <bool MX>
 constexpr int kPartK = MX ? 512 : 256;
 
+// Experts of more than the 4 NB members that the columns hold, NB 8 at most,
+// are read again for the others (64 tokens of one expert of 4096 x 14336 in
+// bf16 123 us for the layer, 32 tokens 86; of two, all chosen, 216 and 150).
 template <bool MX, bool NT, int NB>
 __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
                                            int begin, int end, int most,
@@ -1177,8 +1182,8 @@ __device__ __forceinline__ void down_batch(const FewParams& P, const Units& U,
 }
 
 // MAXB: blocks of 4 members that T tokens can fill, up to 8.  24 tokens, 64
-// experts of 2048 x 1408 in MXFP8, 184 MB: 40 us; 64 tokens, 8 of 4096 x 14336
-// in bf16, 0.94 GB: 169 us.
+// experts of 2048 x 1408 in MXFP8, 181 MB: 41 us; 64 tokens, 8 of 4096 x 14336
+// in bf16, 0.94 GB: 168 us.
 template <bool MX, bool NT, int MAXB>
 __global__ __launch_bounds__(kDownBatchThreads, 2) void few_down_batch_kernel(
     FewParams P) {
@@ -1225,7 +1230,7 @@ __global__ __launch_bounds__(kDownBatchThreads, 2) void few_down_batch_kernel(
 // -------------------------------------------------------------------- down
 // The direct form: the columns of a tile are the tokens, each as two, S's
 // larger and smaller part, and a wave's sums run over all experts.  One token,
-// 8 experts of 2048 x 1408, 46 MB: 10.3 us.
+// 8 experts of 2048 x 1408, 46 MB: 10.0 us.
 constexpr int kDownThreads = 1024;
 constexpr int kDownWaves = kDownThreads / kWave;
 constexpr int kAhead = 3;             // chunks of a wave in flight

@@ -462,9 +462,9 @@ class MoEPathMX(MoEPath):
 class MoEDecode:
     """The layer for a fixed number of tokens, up to
     ``moe.MOE_LAYER_MAX_TOKENS``, forward only: one library call that reads
-    the weights of the experts it reaches once.  With prec MOE_MXFP8 w_gu and
-    w2 are pairs of codes and scales, as ``quantize`` makes them of the bf16
-    weights once."""
+    the weights of the experts it reaches once (w2 twice for an expert of
+    more than 32 tokens).  With prec MOE_MXFP8 w_gu and w2 are pairs of codes
+    and scales, as ``quantize`` makes them of the bf16 weights once."""
 
     def __init__(self, T, d, f, E, k, renorm=True, prec=MOE_BF16,
                  device="cuda"):
